@@ -1,0 +1,456 @@
+"""Cases for the operators around the experts' grouped products: the router
+with its balance loss, dispatch and combine of tokens by expert, and the
+Newton-Schulz orthogonalisation of expert weight updates.
+
+Each operator has a plain form in elementary torch operations (32 bits, one
+rounding at the end), and `exact` gives the same outputs in 64 bits from the
+definitions. With `own` true, `run` calls the package instead.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+NS_COEF = (3.4445, -4.7750, 2.0315)
+NS_EPS = 1e-7
+TYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+# ------------------------------------------------------------------- cases
+def _route(name, T, E, k, dtype, renorm=False, masked=0.0, closed=0, train=True):
+    return {"name": name, "op": "route", "T": T, "E": E, "k": k, "dtype": dtype, "renorm": renorm,
+            "masked": masked, "closed": closed, "train": train}
+
+
+def _rows(op, name, T, E, k, K, dtype, dropped=0.0, train=True):
+    return {"name": name, "op": op, "T": T, "E": E, "k": k, "K": K, "dtype": dtype, "dropped": dropped,
+            "train": train}
+
+
+def _ns(name, E, N, K, dtype):
+    return {"name": name, "op": "orthogonalize", "E": E, "N": N, "K": K, "dtype": dtype}
+
+
+def listed():
+    return [
+        # evaluation of one short prompt: only the forward, latency alone
+        _route("route-short", 64, 64, 8, "bf16", train=False),
+        # a padded batch of an odd number of tokens, fp32 router, three experts taken out
+        _route("route-padded", 12345, 60, 4, "fp32", masked=0.15, closed=3),
+        # one training step's tokens of the largest batch, many experts
+        _route("route-many", 65536, 256, 8, "bf16", renorm=True),
+        # a short prompt on its way to the experts, forward only
+        _rows("dispatch", "dispatch-short", 48, 16, 2, 2048, "bf16", train=False),
+        # odd token count and width, fp32 rows, some entries dropped
+        _rows("dispatch", "dispatch-odd", 5003, 60, 6, 1419, "fp32", dropped=0.1),
+        # a long training batch with many small experts
+        _rows("dispatch", "dispatch-long", 16384, 64, 8, 4096, "bf16"),
+        # the way back of a short prompt
+        _rows("combine", "combine-short", 48, 16, 2, 2048, "bf16", train=False),
+        # odd token count and width, fp32 rows, some entries dropped
+        _rows("combine", "combine-odd", 5003, 60, 6, 1419, "fp32", dropped=0.1),
+        # a long training batch of wide rows
+        _rows("combine", "combine-wide", 16384, 16, 4, 7168, "bf16"),
+        # the update of a small layer: a few small experts
+        _ns("orthogonalize-small", 4, 96, 224, "bf16"),
+        # experts of odd sizes, taller than wide, fp32 momentum
+        _ns("orthogonalize-odd", 5, 1409, 577, "fp32"),
+        # the expert weights of one wide layer
+        _ns("orthogonalize-wide", 16, 2048, 7168, "bf16"),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(("route", "dispatch", "combine", "orthogonalize"))
+    dtype = rng.choice(("bf16", "fp32"))
+    if op == "route":
+        E = _log_int(rng, 4, 512)
+        T = min(_log_int(rng, 1, 65536), 65536 * 256 // (E * (2 if dtype == "fp32" else 1)))
+        k = rng.randint(1, min(E, 10))
+        return {"op": op, "T": T, "E": E, "k": k, "dtype": dtype, "renorm": rng.random() < 0.5,
+                "masked": rng.choice((0.0, 0.2)), "closed": rng.choice((0, 0, min(E - 1, 2))),
+                "train": rng.random() < 0.7}
+    if op in ("dispatch", "combine"):
+        E, k, K = _log_int(rng, 4, 256), rng.randint(1, 8), _log_int(rng, 64, 7168)
+        k = min(k, E)
+        T = min(_log_int(rng, 1, 32768), 2 ** 28 // (k * K))
+        return {"op": op, "T": T, "E": E, "k": k, "K": K, "dtype": dtype, "dropped": rng.choice((0.0, 0.15)),
+                "train": rng.random() < 0.7}
+    while True:
+        c = {"op": op, "E": _log_int(rng, 1, 32), "N": _log_int(rng, 16, 4096), "K": _log_int(rng, 16, 4096),
+             "dtype": dtype}
+        if work(c)["flops"] <= 1e12:
+            return c
+
+
+# ------------------------------------------------------------------ inputs
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def _ids(c, gen):
+    """Top-k expert ids of random scores with a skewed expert popularity; a
+    share of the entries dropped."""
+    s = torch.randn(c["T"], c["E"], generator=gen, device=DEV) + torch.randn(c["E"], generator=gen, device=DEV)
+    ids = torch.topk(s, c["k"], dim=1).indices.to(torch.int32)
+    if c["dropped"]:
+        ids[torch.rand(ids.shape, generator=gen, device=DEV) < c["dropped"]] = -1
+    return ids.contiguous()
+
+
+def _sorted_rows(c):
+    return (c["T"] * c["k"] + 15) // 16 * 16
+
+
+def prepare(case, seed):
+    c, gen = case, _gen(seed)
+    dt = TYPES[c["dtype"]]
+    s = {"case": c}
+    if c["op"] == "route":
+        T, E, k = c["T"], c["E"], c["k"]
+        bias = 0.7 * torch.randn(E, generator=gen, device=DEV)
+        l = torch.randn(T, E, generator=gen, device=DEV) * 1.5 + bias
+        if c["closed"]:
+            l[:, torch.randperm(E, generator=gen, device=DEV)[:c["closed"]]] = -math.inf
+        s["logits"] = l.to(dt)
+        s["valid"] = torch.rand(T, generator=gen, device=DEV) >= c["masked"] if c["masked"] else None
+        s["gw"] = torch.randn(T, k, generator=gen, device=DEV)
+        s["gl"] = 0.01 * (0.5 + torch.rand((), generator=gen, device=DEV))
+        if c["train"]:
+            s["logits"].requires_grad_(True)
+    elif c["op"] == "dispatch":
+        s["ids"] = _ids(c, gen)
+        s["x"] = torch.randn(c["T"], c["K"], generator=gen, device=DEV).to(dt)
+        if c["train"]:
+            s["x"].requires_grad_(True)
+            s["gxs"] = torch.randn(_sorted_rows(c), c["K"], generator=gen, device=DEV).to(dt)
+    elif c["op"] == "combine":
+        s["pos"], _ = _plan(_ids(c, gen), c["E"])
+        s["y"] = torch.randn(_sorted_rows(c), c["K"], generator=gen, device=DEV).to(dt)
+        s["w"] = torch.rand(c["T"], c["k"], generator=gen, device=DEV)
+        if c["train"]:
+            s["y"].requires_grad_(True)
+            s["w"].requires_grad_(True)
+            s["dout"] = torch.randn(c["T"], c["K"], generator=gen, device=DEV).to(dt)
+    else:
+        E, N, K = c["E"], c["N"], c["K"]
+        # gradients: a few strong directions over noise, rows of unlike size
+        r = max(1, min(N, K) // 16)
+        g = torch.randn(E, N, K, generator=gen, device=DEV)
+        g += torch.bmm(torch.randn(E, N, r, generator=gen, device=DEV),
+                       torch.randn(E, r, K, generator=gen, device=DEV)) * (2.0 / math.sqrt(r))
+        g *= torch.exp(0.5 * torch.randn(E, N, 1, generator=gen, device=DEV)) * 1e-3
+        s["g"] = g.to(dt)
+    return s
+
+
+# ------------------------------------------------------------- plain forms
+def _route_plain(logits, valid, k, renorm, gw, gl, train):
+    T, E = logits.shape
+    l = logits.detach().float()
+    ok = torch.ones(T, dtype=torch.bool, device=l.device) if valid is None else valid
+    top, ids = torch.sort(l, dim=1, descending=True, stable=True)
+    top, ids = top[:, :k], ids[:, :k]
+    chosen = (top > -math.inf) & ok[:, None]
+    mx = l.max(dim=1, keepdim=True).values
+    some = (mx > -math.inf) & ok[:, None]
+    ex = torch.where(some, torch.exp(l - mx), torch.zeros_like(l))
+    z = ex.sum(dim=1, keepdim=True)
+    p = torch.where(some, ex / z, torch.zeros_like(l))
+    wt = torch.where(chosen, torch.gather(p, 1, ids), torch.zeros_like(top))
+    S = wt.sum(dim=1, keepdim=True)
+    if renorm:
+        wt = torch.where(chosen, wt / S, torch.zeros_like(wt))
+    ids = torch.where(chosen, ids, torch.full_like(ids, -1))
+    counts = (ids.reshape(-1, 1) == torch.arange(E, device=l.device)).sum(dim=0) if T * k * E < 2 ** 24 else \
+        torch.stack([(ids == e).sum() for e in range(E)])
+    n = ok.sum().double()
+    f = counts.double() / (k * n)
+    loss = (E * (f * (p.sum(dim=0, dtype=torch.float64) / n)).sum()).float()
+    loss = torch.where(n > 0, loss, torch.zeros_like(loss))
+    out = [wt, ids.to(torch.int32), counts.to(torch.int32), loss]
+    if train:
+        u = torch.where(chosen, gw, torch.zeros_like(gw))
+        if renorm:
+            u = torch.where(chosen, (u - (u * wt).sum(dim=1, keepdim=True)) / S, torch.zeros_like(u))
+        h = torch.zeros(T, E + 1, device=l.device)
+        h.scatter_add_(1, torch.where(chosen, ids, torch.full_like(ids, E)), u)
+        h = h[:, :E] + (gl.double() * E * f / n).float()
+        dl = p * (h - (h * p).sum(dim=1, keepdim=True))
+        out.append(torch.where(some, dl, torch.zeros_like(dl)).to(logits.dtype))
+    return out
+
+
+def _plan(ids, E):
+    """Position of every entry in the order by expert (stable), and the ends."""
+    flat = ids.reshape(-1).long()
+    key = torch.where(flat >= 0, flat, torch.full_like(flat, E))
+    order = torch.sort(key, stable=True).indices
+    pos = torch.empty_like(flat)
+    pos[order] = torch.arange(flat.numel(), device=flat.device)
+    pos = torch.where(flat >= 0, pos, torch.full_like(pos, -1))
+    ends = torch.searchsorted(key[order], torch.arange(E, device=flat.device), right=True)
+    return pos.reshape(ids.shape).to(torch.int32), ends.to(torch.int32)
+
+
+def _spread(x, pos, M, scale=None):
+    """rows x[t] (times scale[t, j]) at pos[t, j] of an (M, K) tensor of zeros."""
+    T, k = pos.shape
+    out = torch.zeros(M + 1, x.shape[1], dtype=torch.float32, device=x.device)
+    for j in range(k):
+        row = x.float() if scale is None else x.float() * scale[:, j:j + 1]
+        p = pos[:, j].long()
+        out[torch.where(p >= 0, p, torch.full_like(p, M))] = row
+    return out[:M]
+
+
+def _gather_sum(y, pos, scale=None):
+    out = torch.zeros(pos.shape[0], y.shape[1], dtype=torch.float32, device=y.device)
+    for j in range(pos.shape[1]):
+        p = pos[:, j].long()
+        row = y[p.clamp(min=0)].float()
+        if scale is not None:
+            row = row * scale[:, j:j + 1]
+        out += torch.where((p >= 0)[:, None], row, torch.zeros_like(row))
+    return out
+
+
+def _dispatch_plain(c, x, ids, gxs):
+    pos, ends = _plan(ids, c["E"])
+    x = x.detach()
+    out = [_spread(x, pos, _sorted_rows(c)).to(x.dtype), pos, ends]
+    if c["train"]:
+        out.append(_gather_sum(gxs, pos).to(x.dtype))
+    return out
+
+
+def _combine_plain(c, y, pos, w, dout):
+    y, w = y.detach(), w.detach()
+    out = [_gather_sum(y, pos, w).to(y.dtype)]
+    if c["train"]:
+        out.append(_spread(dout, pos, y.shape[0], w).to(y.dtype))
+        dw = torch.zeros_like(w)
+        for j in range(pos.shape[1]):
+            p = pos[:, j].long()
+            dot = (y[p.clamp(min=0)].float() * dout.float()).sum(dim=1)
+            dw[:, j] = torch.where(p >= 0, dot, torch.zeros_like(dot))
+        out.append(dw)
+    return out
+
+
+def _ns_plain(g):
+    x = g.float()
+    norm = torch.sqrt((g.double() * g.double()).sum(dim=(1, 2), keepdim=True))
+    x = (x / (norm + NS_EPS)).float()
+    tall = x.shape[1] > x.shape[2]
+    if tall:
+        x = x.transpose(1, 2)
+    a, b, c = NS_COEF
+    for _ in range(5):
+        A = torch.bmm(x, x.transpose(1, 2))
+        B = b * A + c * torch.bmm(A, A)
+        x = a * x + torch.bmm(B, x)
+    if tall:
+        x = x.transpose(1, 2)
+    return [x.to(torch.bfloat16).contiguous()]
+
+
+# --------------------------------------------------------------------- run
+def _run_own(s):
+    from mxfp8_quantization_moe_device_b200 import autograd, binding
+    c = s["case"]
+    if c["op"] == "route":
+        if not c["train"]:
+            return list(binding.moe_route(s["logits"], c["k"], valid=s["valid"], renormalize=c["renorm"]))
+        w, ids, counts, loss = autograd.moe_route(s["logits"], c["k"], valid=s["valid"], renormalize=c["renorm"])
+        (dl,) = torch.autograd.grad((w, loss), (s["logits"],), (s["gw"], s["gl"]))
+        return [w.detach(), ids, counts, loss.detach(), dl]
+    if c["op"] == "dispatch":
+        if not c["train"]:
+            pos, offs = binding.moe_dispatch_plan(s["ids"], c["E"])
+            return [binding.moe_dispatch(s["x"], pos, offs), pos, offs]
+        xs, pos, offs = autograd.moe_dispatch(s["x"], s["ids"], c["E"])
+        (dx,) = torch.autograd.grad((xs,), (s["x"],), (s["gxs"],))
+        return [xs.detach(), pos, offs, dx]
+    if c["op"] == "combine":
+        if not c["train"]:
+            return [binding.moe_combine(s["y"], s["pos"], s["w"])]
+        out = autograd.moe_combine(s["y"], s["pos"], s["w"])
+        dy, dw = torch.autograd.grad((out,), (s["y"], s["w"]), (s["dout"],))
+        return [out.detach(), dy, dw]
+    return [binding.newton_schulz(s["g"], steps=5, coefficients=NS_COEF, eps=NS_EPS)]
+
+
+def run(state):
+    if own:
+        return _run_own(state)
+    s, c = state, state["case"]
+    if c["op"] == "route":
+        return _route_plain(s["logits"], s["valid"], c["k"], c["renorm"], s["gw"], s["gl"], c["train"])
+    if c["op"] == "dispatch":
+        return _dispatch_plain(c, s["x"], s["ids"], s.get("gxs"))
+    if c["op"] == "combine":
+        return _combine_plain(c, s["y"], s["pos"], s["w"], s.get("dout"))
+    return _ns_plain(s["g"])
+
+
+# -------------------------------------------------------------------- work
+def work(case):
+    c = case
+    e = 2 if c["dtype"] == "bf16" else 4
+    if c["op"] == "route":
+        T, E, k = c["T"], c["E"], c["k"]
+        mask = T if c["masked"] else 0
+        b, f = T * E * e + mask + 8 * T * k + 4 * E + 4, 6 * T * E
+        if c["train"]:
+            b, f = b + T * E * e + 4 * T * k + 4, f + 6 * T * E
+        return {"bytes": b, "flops": f}
+    if c["op"] == "dispatch":
+        T, k, K, M = c["T"], c["k"], c["K"], _sorted_rows(c)
+        b, f = T * K * e + M * K * e + 8 * T * k + 4 * c["E"], 0
+        if c["train"]:
+            b, f = 2 * b - 8 * T * k - 4 * c["E"], T * k * K
+        return {"bytes": b, "flops": f}
+    if c["op"] == "combine":
+        T, k, K, M = c["T"], c["k"], c["K"], _sorted_rows(c)
+        b, f = T * K * e + T * k * K * e + 8 * T * k, 2 * T * k * K
+        if c["train"]:
+            b, f = b + T * K * e + M * K * e + 4 * T * k, f + 3 * T * k * K
+        return {"bytes": b, "flops": f}
+    E, m, n = c["E"], min(c["N"], c["K"]), max(c["N"], c["K"])
+    # A = X X^T and A A are symmetric: half of each product
+    return {"bytes": E * m * n * (e + 2), "flops": 5 * E * (3 * m * m * n + m * m * m)}
+
+
+# ------------------------------------------------------------------- exact
+def _exact_route(s):
+    c = s["case"]
+    T, E, k = c["T"], c["E"], c["k"]
+    l = s["logits"].detach().double()
+    live = torch.isfinite(l)
+    if s["valid"] is not None:
+        live = live & s["valid"][:, None]
+    # log p by the log of the sum over the live experts; a dead row keeps p = 0
+    lse = torch.logsumexp(torch.where(live, l, torch.full_like(l, -1e300)), dim=1, keepdim=True)
+    p = torch.where(live, torch.exp(l - lse), torch.zeros_like(l))
+    # the k best one after another, the first of equals
+    left = torch.where(live, l, torch.full_like(l, -math.inf))
+    sel = torch.zeros(T, E, dtype=torch.bool, device=l.device)
+    ids, rows = [], torch.arange(T, device=l.device)
+    index = torch.arange(E, device=l.device).expand(T, E)
+    for _ in range(k):
+        best = left.max(dim=1, keepdim=True).values
+        first = torch.where(left == best, index, torch.full_like(index, E)).min(dim=1).values
+        hit = best[:, 0] > -math.inf
+        ids.append(torch.where(hit, first, torch.full_like(first, -1)))
+        sel[rows[hit], first[hit]] = True
+        left[rows, first] = -math.inf
+    ids = torch.stack(ids, dim=1)
+    psel = torch.where(sel, p, torch.zeros_like(p))
+    S = psel.sum(dim=1, keepdim=True) if c["renorm"] else torch.ones(T, 1, dtype=torch.float64, device=l.device)
+    share = torch.where(S > 0, psel / S, torch.zeros_like(psel))
+    got = ids >= 0
+    w = torch.where(got, share.gather(1, ids.clamp(min=0)), torch.zeros(T, k, dtype=torch.float64, device=l.device))
+    counts = sel.sum(dim=0)
+    n = float(T if s["valid"] is None else int(s["valid"].sum()))
+    loss = (p.sum(dim=0) * counts).sum() * (E / (k * n * n)) if n else torch.zeros((), dtype=torch.float64)
+    out = [w, ids.to(torch.int32), counts.to(torch.int32), loss]
+    if c["train"]:
+        # d/dl_e of sum_j g_j w_j: with renormalisation a softmax over the
+        # chosen experts, without it the full softmax
+        g = torch.zeros_like(p)
+        g.scatter_add_(1, ids.clamp(min=0), torch.where(got, s["gw"].double(), torch.zeros_like(w)))
+        q = share if c["renorm"] else p
+        dl = q * (g - (share * g).sum(dim=1, keepdim=True))
+        if n:
+            hb = counts.double() * (float(s["gl"]) * E / (k * n * n))
+            dl = dl + p * (hb - (p * hb).sum(dim=1, keepdim=True))
+        out.append(dl)
+    return out
+
+
+def _exact_pos(ids, E):
+    """Positions by counting: entries of smaller experts, then earlier entries of the same."""
+    flat = ids.reshape(-1).long()
+    pos = torch.full_like(flat, -1)
+    start, ends = 0, []
+    for e in range(E):
+        mine = (flat == e).nonzero()[:, 0]
+        pos[mine] = start + torch.arange(mine.numel(), device=flat.device)
+        start += mine.numel()
+        ends.append(start)
+    return pos.reshape(ids.shape), torch.tensor(ends, dtype=torch.int32, device=flat.device)
+
+
+def _source(pos, M):
+    """token and slot of every sorted row, -1 where none."""
+    T, k = pos.shape
+    src = torch.full((M,), -1, dtype=torch.long, device=pos.device)
+    flat = pos.reshape(-1).long()
+    entry = torch.arange(T * k, device=pos.device)
+    src[flat[flat >= 0]] = entry[flat >= 0]
+    return src
+
+
+def _exact_rows(x, src, k, scale=None):
+    r = x.double()[(src.clamp(min=0) // k)]
+    if scale is not None:
+        r = r * scale.double().reshape(-1)[src.clamp(min=0)][:, None]
+    r[src < 0] = 0
+    return r
+
+
+def _exact_sum(y, src, T, k, scale=None):
+    live = src >= 0
+    r = y.double()[:src.numel()][live]
+    if scale is not None:
+        r = r * scale.double().reshape(-1)[src[live]][:, None]
+    return torch.zeros(T, y.shape[1], dtype=torch.float64, device=y.device).index_add_(0, src[live] // k, r)
+
+
+def _exact_ns(g):
+    """X_s = P_s X_0 with P <- Q P, A <- Q A Q and Q = a + b A + c A A, all
+    functions of the Gram matrix of X_0."""
+    x = g.double()
+    x = x / (torch.linalg.vector_norm(x, dim=(1, 2), keepdim=True) + NS_EPS)
+    if x.shape[1] > x.shape[2]:
+        return _exact_ns(g.transpose(1, 2)).transpose(1, 2)
+    a, b, c = NS_COEF
+    A = x @ x.mT
+    eye = torch.eye(A.shape[1], dtype=torch.float64, device=g.device)
+    P = eye.expand_as(A)
+    for _ in range(5):
+        Q = a * eye + A @ (b * eye + c * A)
+        P, A = Q @ P, Q @ A @ Q
+    return P @ x
+
+
+def exact(case, seed):
+    c, s = case, prepare(case, seed)
+    with torch.no_grad():
+        if c["op"] == "route":
+            return _exact_route(s)
+        if c["op"] == "dispatch":
+            pos, ends = _exact_pos(s["ids"], c["E"])
+            src = _source(pos, _sorted_rows(c))
+            out = [_exact_rows(s["x"], src, c["k"]), pos.to(torch.int32), ends]
+            return out + [_exact_sum(s["gxs"], src, c["T"], c["k"])] if c["train"] else out
+        if c["op"] == "combine":
+            k, w, y = c["k"], s["w"], s["y"]
+            src = _source(s["pos"], _sorted_rows(c))
+            out = [_exact_sum(y, src, c["T"], k, w)]
+            if c["train"]:
+                live = src >= 0
+                dw = torch.zeros(c["T"] * k, dtype=torch.float64, device=w.device)
+                dw[src[live]] = (y.double()[live] * s["dout"].double()[src[live] // k]).sum(dim=1)
+                out += [_exact_rows(s["dout"], src, k, w), dw.reshape(w.shape)]
+            return out
+        return [_exact_ns(s["g"])]

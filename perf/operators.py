@@ -133,7 +133,7 @@ def prepare(case, seed):
             s["x"].requires_grad_(True)
             s["gxs"] = torch.randn(_sorted_rows(c), c["K"], generator=gen, device=DEV).to(dt)
     elif c["op"] == "combine":
-        s["pos"], _ = _plan(_ids(c, gen), c["E"])
+        s["pos"], s["offs"] = _plan(_ids(c, gen), c["E"])
         s["y"] = torch.randn(_sorted_rows(c), c["K"], generator=gen, device=DEV).to(dt)
         s["w"] = torch.rand(c["T"], c["k"], generator=gen, device=DEV)
         if c["train"]:
@@ -283,7 +283,7 @@ def _run_own(s):
     if c["op"] == "combine":
         if not c["train"]:
             return [binding.moe_combine(s["y"], s["pos"], s["w"])]
-        out = autograd.moe_combine(s["y"], s["pos"], s["w"])
+        out = autograd.moe_combine(s["y"], s["pos"], s["w"], s["offs"])
         dy, dw = torch.autograd.grad((out,), (s["y"], s["w"]), (s["dout"],))
         return [out.detach(), dy, dw]
     return [binding.newton_schulz(s["g"], steps=5, coefficients=NS_COEF, eps=NS_EPS)]

@@ -64,7 +64,8 @@ typedef enum mxq_status {
     MXQ_ERR_BAD_OFFSETS = 6, /* device: offsets decreasing, negative or > extent */
     MXQ_ERR_TIMEOUT = 7,     /* device: a bounded wait expired                  */
     MXQ_ERR_WORKSPACE = 8,   /* workspace missing or smaller than required      */
-    MXQ_ERR_CUDA = 9         /* another CUDA runtime error                      */
+    MXQ_ERR_CUDA = 9,        /* another CUDA runtime error                      */
+    MXQ_ERR_BAD_INDEX = 10   /* device: an expert id or a row place out of range */
 } mxq_status;
 
 typedef enum mxq_scale_mode {
@@ -444,6 +445,85 @@ int fp8_quant_jagged_colwise_noalloc(const void *in, int64_t rows, int64_t cols,
 
 /* Size in bytes of the fixed scratch array of the allocation-free entry point. */
 size_t fp8_quant_jagged_colwise_noalloc_max_scratch_bytes(void);
+
+/* ------------------------------------------------------------------------ *
+ * Around the experts' grouped GEMMs: the router, the order of the tokens by
+ * expert, and the rows' way into that order and back. Rows are bf16 or fp32
+ * (mxq_dtype); sums are taken in fp32 or more, in a fixed order, and rounded
+ * once.
+ * ------------------------------------------------------------------------ */
+typedef enum mxq_dtype {
+    MXQ_BF16 = 0,
+    MXQ_FP32 = 1
+} mxq_dtype;
+
+/* Router. For every token t of logits (tokens, experts), row t at logits +
+ * t * row_stride elements:
+ *   p = softmax(logits[t]);  ids[t][:] = the top_k largest logits, largest
+ *   first, equal ones by lowest index;  weights[t][j] = p[ids[t][j]], divided
+ *   by their sum when `renormalize`.
+ *   counts[e] = how often expert e was chosen (int32, experts)
+ *   loss      = E sum_e (counts[e] / (top_k n)) (sum_t p[t][e] / n), n the
+ *               number of valid tokens (0 when n is 0)
+ *   loss_grad = NULL, or fp32 (experts): d loss / d p[t][e], the same for
+ *               every t (counts taken as constants); the backward reads it.
+ * valid: NULL, or one byte per token; a token whose byte is 0 is padding: ids
+ * -1, weights 0, no part in counts and loss. An expert with logit -inf is
+ * never chosen; where fewer than top_k experts are left the slots' ids are -1
+ * and their weights 0. A row with a NaN or +inf chooses nothing, its weights
+ * are NaN, and so is the loss. experts <= 1024, top_k <= 32. workspace:
+ * moe_route_workspace_bytes() bytes, 256-byte aligned, not shared by calls
+ * that overlap on the GPU. */
+size_t moe_route_workspace_bytes(int64_t tokens, int64_t experts);
+int moe_route(const void *logits, int32_t dtype, int64_t tokens, int64_t experts, int64_t row_stride,
+              const uint8_t *valid, int32_t top_k, int32_t renormalize, float *weights, int32_t *ids,
+              int32_t *counts, float *loss, float *loss_grad, void *workspace, size_t workspace_bytes,
+              cudaStream_t stream);
+
+/* Gradient of moe_route by the logits: weights, ids and loss_grad as the
+ * forward wrote them; grad_weights fp32 (tokens, top_k) or NULL, grad_loss
+ * one fp32 on the device or NULL (a NULL gradient is zero). grad_logits
+ * (tokens, experts), row-major, of the logits' type. */
+int moe_route_backward(const void *logits, int32_t dtype, int64_t tokens, int64_t experts, int64_t row_stride,
+                       const uint8_t *valid, int32_t top_k, int32_t renormalize, const float *weights,
+                       const int32_t *ids, const float *loss_grad, const float *grad_weights, const float *grad_loss,
+                       void *grad_logits, cudaStream_t stream);
+
+/* Order by expert of `entries` expert ids (a (tokens, top_k) array, row-major):
+ * pos[i] = number of entries of smaller experts plus earlier entries of the
+ * same expert, offs (experts) the group ends that the grouped GEMMs take. A
+ * negative id is dropped (pos -1); an id >= experts is dropped too and
+ * recorded as MXQ_ERR_BAD_INDEX in the device status. experts <= 1024.
+ * workspace: moe_dispatch_plan_workspace_bytes() bytes (NULL when 0), not
+ * shared by calls that overlap on the GPU. */
+size_t moe_dispatch_plan_workspace_bytes(int64_t entries, int64_t experts);
+int moe_dispatch_plan(const int32_t *ids, int64_t entries, int64_t experts, int32_t *pos, int32_t *offs,
+                      void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* out[pos[t][j]] = x[t] for every slot with pos >= 0; the rows of out from
+ * offs[num_groups - 1] to out_rows are zero. x (tokens, cols) with row_stride
+ * elements between rows, out (out_rows, cols) row-major. A pos >= out_rows is
+ * skipped and recorded as MXQ_ERR_BAD_INDEX. top_k <= 32. */
+int moe_dispatch(const void *x, int32_t dtype, int64_t tokens, int64_t cols, int64_t row_stride, const int32_t *pos,
+                 int32_t top_k, const int32_t *offs, int32_t num_groups, void *out, int64_t out_rows,
+                 cudaStream_t stream);
+
+/* out[t] = sum_j weights[t][j] * y[pos[t][j]] over the slots with pos >= 0
+ * (weights NULL: ones), slots in order, fp32, rounded once. y (rows, cols)
+ * with row_stride, out (tokens, cols) row-major. Also the gradient of
+ * moe_dispatch by x, with weights NULL. A pos >= rows is skipped and recorded
+ * as MXQ_ERR_BAD_INDEX. */
+int moe_combine(const void *y, int32_t dtype, int64_t rows, int64_t cols, int64_t row_stride, const int32_t *pos,
+                const float *weights, int64_t tokens, int32_t top_k, void *out, cudaStream_t stream);
+
+/* Gradient of moe_combine: grad_y[pos[t][j]] = weights[t][j] * grad_out[t]
+ * (rows from offs[num_groups - 1] on zero) and grad_weights[t][j] = sum of
+ * grad_out[t] * y[pos[t][j]] (0 for a dropped slot). Either may be NULL; y is
+ * read for grad_weights only. */
+int moe_combine_backward(const void *grad_out, int64_t grad_row_stride, const void *y, int64_t row_stride,
+                         int32_t dtype, int64_t rows, int64_t cols, const int32_t *pos, const float *weights,
+                         int64_t tokens, int32_t top_k, const int32_t *offs, int32_t num_groups, void *grad_y,
+                         float *grad_weights, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ *
  * Status and housekeeping

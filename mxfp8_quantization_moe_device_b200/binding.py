@@ -16,7 +16,8 @@ LIB_PATH = os.path.join(_HERE, "libmxq.so")
 
 OK = 0
 ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_LAUNCH = 1, 2, 3, 4, 5
-ERR_BAD_OFFSETS, ERR_TIMEOUT, ERR_WORKSPACE, ERR_CUDA = 6, 7, 8, 9
+ERR_BAD_OFFSETS, ERR_TIMEOUT, ERR_WORKSPACE, ERR_CUDA, ERR_BAD_INDEX = 6, 7, 8, 9, 10
+BF16, FP32 = 0, 1
 FLOOR, RCEIL = 0, 1
 TESTING_WAIT_LIMIT_NS, TESTING_SKIP_ARRIVAL, TESTING_FORCE_PATH, TESTING_GEMM_TILE_N = 1, 2, 3, 4
 TESTING_BLOCKED_PATH = 5
@@ -58,6 +59,17 @@ SIGNATURES = {
     "mx_quant_jagged_rowwise_padded": (ctypes.c_int, [_vp, _i64, _i64, _i64, _i64, _vp, _i32, _i32, _vp, _i64,
                                                       _vp, _vp]),
     "mx_grouped_gemm_wgrad": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _i32, _vp, _vp]),
+    "moe_route_workspace_bytes": (_sz, [_i64, _i64]),
+    "moe_route": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                 _vp]),
+    "moe_route_backward": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                          _vp]),
+    "moe_dispatch_plan_workspace_bytes": (_sz, [_i64, _i64]),
+    "moe_dispatch_plan": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "moe_dispatch": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _i32, _vp, _i64, _vp]),
+    "moe_combine": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp]),
+    "moe_combine_backward": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _i32,
+                                            _vp, _vp, _vp]),
     "mxq_device_status": (ctypes.c_int, [_vp, ctypes.POINTER(_i32)]),
     "mxq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "mxq_version": (ctypes.c_int, []),
@@ -544,6 +556,197 @@ def mx_grouped_gemm_wgrad(a, sfa, b, sfb, offs, tokens, *, out=None):
     _call("mx_grouped_gemm_wgrad", dev, _ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), N, K, int(tokens), cap, _ptr(offs),
           G, _ptr(out))
     return out
+
+
+# ---------------------------------------------------------------- experts: router, order, rows
+
+_DTYPES = {torch.bfloat16: BF16, torch.float32: FP32}
+
+
+def _rows(t, name, dtype=None):
+    """A 2-D bf16 or fp32 CUDA tensor with contiguous rows that do not
+    overlap; returns (dtype code, rows, cols, row stride)."""
+    _cuda(t, name)
+    if t.dim() != 2 or t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be a 2-D {dtype or 'bfloat16 or float32'} tensor")
+    rows, cols = t.shape
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise TypeError(f"{name} must have contiguous rows that do not overlap")
+    return _DTYPES[t.dtype], rows, cols, (t.stride(0) if rows > 1 else cols)
+
+
+def _array(t, name, dtype, shape, dev):
+    """A contiguous input of this type and shape on `dev`."""
+    _cuda(t, name)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != dev:
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+    return t
+
+
+def _output(t, name, dtype, shape, dev):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    return _out_buffer(t, name, shape, dtype.itemsize, dev, dtype)
+
+
+def _valid(valid, tokens, dev):
+    if valid is None:
+        return None
+    if isinstance(valid, torch.Tensor) and valid.dtype == torch.uint8:
+        return _array(valid, "valid", torch.uint8, (tokens,), dev)
+    return _array(valid, "valid", torch.bool, (tokens,), dev)
+
+
+def _positions(pos, tokens, dev):
+    _cuda(pos, "pos")
+    if pos.dim() != 2:
+        raise TypeError("pos must be a (tokens, top_k) int32 tensor")
+    return _array(pos, "pos", torch.int32, (pos.shape[0] if tokens is None else tokens, pos.shape[1]), dev)
+
+
+def _workspace(nbytes, dev):
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+
+
+def moe_route(logits, top_k, *, valid=None, renormalize=False, weights=None, ids=None, counts=None, loss=None,
+              loss_grad=None):
+    """Router of logits (T, E) bf16 or fp32: softmax, the top_k largest (equal
+    ones by lowest index), counts and the balance loss E sum_e (counts[e] /
+    (top_k n)) mean_t p[t][e]. valid: (T,) bool, False marks padding. Returns
+    (weights (T, top_k) fp32, ids (T, top_k) int32, counts (E,) int32, loss ()
+    fp32); a slot without an expert (padding, experts at -inf) has id -1 and
+    weight 0; a row with a NaN or +inf has ids -1 and NaN weights, and makes
+    the loss NaN. loss_grad: optional (E,) fp32 buffer that receives d loss /
+    d p[t][e], for moe_route_backward."""
+    code, T, E, ld = _rows(logits, "logits")
+    dev = logits.device
+    k = int(top_k)
+    if not 1 <= k <= E:
+        raise ValueError("top_k must lie in [1, experts]")
+    valid = _valid(valid, T, dev)
+    weights = _output(weights, "weights", torch.float32, (T, k), dev)
+    ids = _output(ids, "ids", torch.int32, (T, k), dev)
+    counts = _output(counts, "counts", torch.int32, (E,), dev)
+    loss = _output(loss, "loss", torch.float32, (), dev)
+    if loss_grad is not None:
+        _out_buffer(loss_grad, "loss_grad", (E,), 4, dev, torch.float32)
+    with torch.cuda.device(dev):
+        ws = _workspace(lib().moe_route_workspace_bytes(T, E), dev)
+        _call("moe_route", dev, _ptr(logits), code, T, E, ld, _ptr(valid), k, 1 if renormalize else 0, _ptr(weights),
+              _ptr(ids), _ptr(counts), _ptr(loss), _ptr(loss_grad), _ptr(ws), ws.numel() if ws is not None else 0)
+    return weights, ids, counts, loss
+
+
+def moe_route_backward(logits, weights, ids, loss_grad, grad_weights, grad_loss, *, valid=None, renormalize=False,
+                       out=None):
+    """Gradient of moe_route by the logits, (T, E) of their type, from what
+    the forward returned and wrote (weights, ids, loss_grad) and the gradients
+    of weights (T, top_k) fp32 and of loss () fp32; either may be None."""
+    code, T, E, ld = _rows(logits, "logits")
+    dev = logits.device
+    _cuda(ids, "ids")
+    if ids.dim() != 2 or not 1 <= ids.shape[1] <= E:
+        raise TypeError("ids must be a (tokens, top_k) int32 tensor")
+    k = ids.shape[1]
+    _array(ids, "ids", torch.int32, (T, k), dev)
+    _array(weights, "weights", torch.float32, (T, k), dev)
+    if grad_weights is not None:
+        _array(grad_weights, "grad_weights", torch.float32, (T, k), dev)
+    if grad_loss is not None:
+        _array(grad_loss, "grad_loss", torch.float32, (), dev)
+        _array(loss_grad, "loss_grad", torch.float32, (E,), dev)
+    out = _output(out, "out", logits.dtype, (T, E), dev)
+    _call("moe_route_backward", dev, _ptr(logits), code, T, E, ld, _ptr(_valid(valid, T, dev)), k,
+          1 if renormalize else 0, _ptr(weights), _ptr(ids), _ptr(loss_grad), _ptr(grad_weights), _ptr(grad_loss),
+          _ptr(out))
+    return out
+
+
+def moe_dispatch_plan(ids, num_experts, *, pos=None, offs=None):
+    """The stable order by expert of ids (T, top_k) int32: returns (pos (T,
+    top_k) int32, the row of every entry among the sorted ones, -1 where the
+    id is negative; offs (num_experts,) int32, the group ends that the grouped
+    GEMMs take). An id >= num_experts is dropped and reported by
+    device_status."""
+    _cuda(ids, "ids")
+    if ids.dim() != 2:
+        raise TypeError("ids must be a (tokens, top_k) int32 tensor")
+    dev = ids.device
+    _array(ids, "ids", torch.int32, ids.shape, dev)
+    E = int(num_experts)
+    if E < 1:
+        raise ValueError("num_experts must be positive")
+    pos = _output(pos, "pos", torch.int32, ids.shape, dev)
+    offs = _output(offs, "offs", torch.int32, (E,), dev)
+    ws = _workspace(lib().moe_dispatch_plan_workspace_bytes(ids.numel(), E), dev)
+    _call("moe_dispatch_plan", dev, _ptr(ids), ids.numel(), E, _ptr(pos), _ptr(offs), _ptr(ws),
+          ws.numel() if ws is not None else 0)
+    return pos, offs
+
+
+def moe_dispatch_rows(entries):
+    """Rows of the dispatched tokens: the entries, up to a multiple of 16 (the
+    grouped GEMMs' token count)."""
+    return (entries + 15) // 16 * 16
+
+
+def moe_dispatch(x, pos, offs, *, out=None):
+    """Token rows in the order by expert: out[pos[t][j]] = x[t], the rows from
+    offs[-1] on zero. x (T, K) bf16 or fp32 with contiguous rows, pos and offs
+    from moe_dispatch_plan. Returns out (M, K) with M = moe_dispatch_rows(T *
+    top_k), or fills the given out (any number of rows)."""
+    code, T, K, ld = _rows(x, "x")
+    dev = x.device
+    _positions(pos, T, dev)
+    _offsets(offs, dev)
+    M = moe_dispatch_rows(pos.numel()) if out is None else out.shape[0]
+    out = _output(out, "out", x.dtype, (M, K), dev)
+    if pos.shape[1] == 0:
+        raise ValueError("pos must have at least one slot per token")
+    _call("moe_dispatch", dev, _ptr(x), code, T, K, ld, _ptr(pos), pos.shape[1], _ptr(offs), offs.numel(), _ptr(out),
+          M)
+    return out
+
+
+def moe_combine(y, pos, weights=None, *, out=None):
+    """The way back: out[t] = sum_j weights[t][j] * y[pos[t][j]] over the slots
+    with pos >= 0, in fp32, rounded once. y (M, K) bf16 or fp32 with
+    contiguous rows, weights (T, top_k) fp32 or None (ones). Returns out
+    (T, K); rows of y that no slot names are not read."""
+    code, M, K, ld = _rows(y, "y")
+    dev = y.device
+    _positions(pos, None, dev)
+    T, k = pos.shape
+    if k == 0:
+        raise ValueError("pos must have at least one slot per token")
+    if weights is not None:
+        _array(weights, "weights", torch.float32, (T, k), dev)
+    out = _output(out, "out", y.dtype, (T, K), dev)
+    _call("moe_combine", dev, _ptr(y), code, M, K, ld, _ptr(pos), _ptr(weights), T, k, _ptr(out))
+    return out
+
+
+def moe_combine_backward(grad_out, y, pos, weights, offs, *, need_y=True, need_weights=True, grad_y=None,
+                         grad_weights=None):
+    """Gradient of moe_combine: (grad_y (M, K) = weights[t][j] * grad_out[t] at
+    row pos[t][j], zero from offs[-1] on; grad_weights (T, top_k) fp32 =
+    <grad_out[t], y[pos[t][j]]>, 0 for a dropped slot). What is not needed is
+    returned as None."""
+    code, M, K, ld = _rows(y, "y")
+    dev = y.device
+    _, T, _, ldg = _rows(grad_out, "grad_out", y.dtype)
+    _positions(pos, T, dev)
+    k = pos.shape[1]
+    if grad_out.shape[1] != K or grad_out.device != dev or k == 0:
+        raise TypeError("shape mismatch between grad_out, y and pos")
+    _offsets(offs, dev)
+    if weights is not None:
+        _array(weights, "weights", torch.float32, (T, k), dev)
+    grad_y = _output(grad_y, "grad_y", y.dtype, (M, K), dev) if need_y else None
+    grad_weights = _output(grad_weights, "grad_weights", torch.float32, (T, k), dev) if need_weights else None
+    _call("moe_combine_backward", dev, _ptr(grad_out), ldg, _ptr(y), ld, code, M, K, _ptr(pos), _ptr(weights), T, k,
+          _ptr(offs), offs.numel(), _ptr(grad_y), _ptr(grad_weights))
+    return grad_y, grad_weights
 
 
 # ---------------------------------------------------------------- status

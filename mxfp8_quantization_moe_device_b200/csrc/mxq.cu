@@ -17,6 +17,7 @@
 #include "gemm_mx.cuh"
 #include "gemm2.cuh"
 #include "mxj.cuh"
+#include "moe.cuh"
 
 using namespace mxq;
 
@@ -177,6 +178,24 @@ int device_info(const DevInfo **out)
         di.ready = true;
     }
     *out = &di;
+    return MXQ_OK;
+}
+
+// let `kernel` use up to `bytes` of dynamic shared memory on the current
+// device; `set` (one per kernel) remembers the devices that have it
+template <typename... K> int allow_smem(void (*kernel)(K...), int bytes, std::atomic<uint64_t> (&set)[2])
+{
+    int d = 0;
+    if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= 128)
+        return MXQ_ERR_CUDA;
+    const uint64_t bit = uint64_t(1) << (d & 63);
+    if (set[d >> 6].load(std::memory_order_acquire) & bit)
+        return MXQ_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return MXQ_ERR_CUDA;
+    }
+    set[d >> 6].fetch_or(bit, std::memory_order_release);
     return MXQ_OK;
 }
 
@@ -1156,6 +1175,7 @@ const char *mxq_status_string(int status)
     case MXQ_ERR_TIMEOUT: return "device wait timed out";
     case MXQ_ERR_WORKSPACE: return "workspace missing or too small";
     case MXQ_ERR_CUDA: return "CUDA runtime error";
+    case MXQ_ERR_BAD_INDEX: return "index out of range";
     default: return "unknown status";
     }
 }
@@ -1192,3 +1212,5 @@ int mxq_testing_set(int32_t what, int64_t value)
 }
 
 } // extern "C"
+
+#include "moe_host.cuh"

@@ -336,3 +336,81 @@ def fp8_grouped_gemm_rowwise_wt(a: torch.Tensor, inv_a: torch.Tensor, wt: torch.
 @fp8_grouped_gemm_rowwise_wt.register_fake
 def _(a, inv_a, wt, inv_w, offs):
     return a.new_empty((a.shape[0], wt.shape[0]), dtype=torch.bfloat16)
+
+
+# ---------------------------------------------------------------- around the grouped products
+
+@torch.library.custom_op("mxq::moe_route", mutates_args=())
+def moe_route(logits: torch.Tensor, top_k: int, valid: torch.Tensor | None,
+              renormalize: bool) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Router: (weights (T, top_k) fp32, ids (T, top_k) int32, counts (E,)
+    int32, balance loss () fp32, loss_grad (E,) fp32 for moe_route_backward)."""
+    loss_grad = torch.empty((logits.shape[1],), dtype=torch.float32, device=logits.device)
+    return *_b.moe_route(logits, top_k, valid=valid, renormalize=renormalize, loss_grad=loss_grad), loss_grad
+
+
+@moe_route.register_fake
+def _(logits, top_k, valid, renormalize):
+    T, E = logits.shape
+    return (logits.new_empty((T, top_k), dtype=torch.float32), logits.new_empty((T, top_k), dtype=torch.int32),
+            logits.new_empty((E,), dtype=torch.int32), logits.new_empty((), dtype=torch.float32),
+            logits.new_empty((E,), dtype=torch.float32))
+
+
+@torch.library.custom_op("mxq::moe_route_backward", mutates_args=())
+def moe_route_backward(logits: torch.Tensor, weights: torch.Tensor, ids: torch.Tensor, loss_grad: torch.Tensor,
+                       grad_weights: torch.Tensor | None, grad_loss: torch.Tensor | None,
+                       valid: torch.Tensor | None, renormalize: bool) -> torch.Tensor:
+    """Gradient of moe_route by the logits, (T, E) of their type."""
+    return _b.moe_route_backward(logits, weights, ids, loss_grad, grad_weights, grad_loss, valid=valid,
+                                 renormalize=renormalize)
+
+
+@moe_route_backward.register_fake
+def _(logits, weights, ids, loss_grad, grad_weights, grad_loss, valid, renormalize):
+    return logits.new_empty(logits.shape)
+
+
+@torch.library.custom_op("mxq::moe_dispatch_plan", mutates_args=())
+def moe_dispatch_plan(ids: torch.Tensor, num_experts: int) -> tuple[torch.Tensor, torch.Tensor]:
+    """Stable order by expert: (pos of ids' shape int32, group ends (num_experts,) int32)."""
+    return _b.moe_dispatch_plan(ids, num_experts)
+
+
+@moe_dispatch_plan.register_fake
+def _(ids, num_experts):
+    return ids.new_empty(ids.shape), ids.new_empty((num_experts,))
+
+
+@torch.library.custom_op("mxq::moe_dispatch", mutates_args=())
+def moe_dispatch(x: torch.Tensor, pos: torch.Tensor, offs: torch.Tensor) -> torch.Tensor:
+    """Token rows by expert, (T * top_k up to a multiple of 16, K); rows past offs[-1] are zero."""
+    return _b.moe_dispatch(x, pos, offs)
+
+
+@moe_dispatch.register_fake
+def _(x, pos, offs):
+    return x.new_empty(((pos.shape[0] * pos.shape[1] + 15) // 16 * 16, x.shape[1]))
+
+
+@torch.library.custom_op("mxq::moe_combine", mutates_args=())
+def moe_combine(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor | None) -> torch.Tensor:
+    """Weighted sum of every token's rows, (T, K)."""
+    return _b.moe_combine(y, pos, weights)
+
+
+@moe_combine.register_fake
+def _(y, pos, weights):
+    return y.new_empty((pos.shape[0], y.shape[1]))
+
+
+@torch.library.custom_op("mxq::moe_combine_backward", mutates_args=())
+def moe_combine_backward(grad_out: torch.Tensor, y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor | None,
+                         offs: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gradient of moe_combine: (grad_y (M, K), grad_weights (T, top_k) fp32)."""
+    return _b.moe_combine_backward(grad_out, y, pos, weights, offs)
+
+
+@moe_combine_backward.register_fake
+def _(grad_out, y, pos, weights, offs):
+    return y.new_empty(y.shape), y.new_empty(pos.shape, dtype=torch.float32)

@@ -1,0 +1,590 @@
+"""Router, order by expert, dispatch and combine, and their gradients, against
+plain implementations in 64 bits; refusals on the CPU, values on a GPU.
+
+Tolerances. Rounding to a type is off by at most eps / 2 of the value (U
+below). Weights and p: the argument l - max is exact to 2^-24 of itself, exp
+is good to 2 ulp and one division or product follows, so a weight is within
+(|l - max| + 8) 2^-23 of itself, below 2^-18 for |l - max| < 24; smaller p
+count only absolutely. Gradients of the logits are sums of a few products of
+such numbers: 2^-17 of the sum of the terms' absolute values. Rows: dispatch
+copies; a combine of k terms is within (k + 1) 2^-24 of the sum of absolute
+values before its one rounding; a dot of K terms in fp32 within K 2^-24 of the
+sum of absolute values (the true error is far smaller, 32 lanes share it).
+"""
+import math
+
+import pytest
+import torch
+
+from mxfp8_quantization_moe_device_b200 import autograd, binding as mxq
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+DEV = "cuda"
+
+
+# ------------------------------------------------------------ plain forms
+def ref_route(logits, k, valid=None, renorm=False, gw=None, gl=None):
+    """64-bit router: weights, ids, counts, loss and, with gw and gl, the
+    gradient and the sum of its terms' absolute values. Rows one by one."""
+    T, E = logits.shape
+    l = logits.double().cpu()
+    ok = torch.ones(T, dtype=torch.bool) if valid is None else valid.cpu().bool()
+    w, ids = torch.zeros(T, k, dtype=torch.float64), torch.full((T, k), -1, dtype=torch.int32)
+    p, S = torch.zeros(T, E, dtype=torch.float64), torch.zeros(T, dtype=torch.float64)
+    bad = torch.zeros(T, dtype=torch.bool)
+    for t in range(T):
+        if not ok[t]:
+            continue
+        row = l[t].tolist()
+        if any(math.isnan(v) or v == math.inf for v in row):
+            bad[t] = True
+            p[t], w[t] = math.nan, math.nan
+            continue
+        live = [e for e in range(E) if row[e] > -math.inf]
+        if not live:
+            continue
+        m = max(row)
+        p[t] = torch.tensor([math.exp(v - m) for v in row], dtype=torch.float64)
+        p[t] /= p[t].sum()
+        best = sorted(live, key=lambda e: (-row[e], e))[:k]
+        ids[t, :len(best)] = torch.tensor(best, dtype=torch.int32)
+        w[t, :len(best)] = p[t, best]
+        S[t] = w[t].sum()
+        if renorm:
+            w[t] /= S[t]
+    counts = torch.tensor([int((ids == e).sum()) for e in range(E)], dtype=torch.int32)
+    n = int(ok.sum())
+    hb = counts.double() * E / (k * n * n) if n else torch.zeros(E, dtype=torch.float64)
+    loss = (hb * p.sum(0)).sum()
+    if gw is None and gl is None:
+        return w, ids, counts, loss
+    gw = torch.zeros(T, k, dtype=torch.float64) if gw is None else gw.double().cpu()
+    hb = hb * (0.0 if gl is None else float(gl))
+    d, mag = torch.zeros(T, E, dtype=torch.float64), torch.zeros(T, E, dtype=torch.float64)
+    for t in range(T):
+        if bad[t]:
+            d[t] = math.nan
+            continue
+        h, ha = hb.clone(), hb.abs()
+        u = gw[t] * (ids[t] >= 0)
+        if renorm and S[t] > 0:
+            um = (u.abs() + (u * w[t]).abs().sum()) / S[t]
+            u = (u - (u * w[t]).sum()) / S[t]
+        else:
+            um = u.abs()
+        for j in range(k):
+            if ids[t, j] >= 0:
+                h[ids[t, j]] += u[j]
+                ha[ids[t, j]] += um[j]
+        d[t] = p[t] * (h - (h * p[t]).sum())
+        mag[t] = p[t] * (ha + (ha * p[t]).sum())
+    return w, ids, counts, loss, d, mag
+
+
+def ref_plan(ids, E):
+    flat = ids.reshape(-1).tolist()
+    order = sorted((e, i) for i, e in enumerate(flat) if 0 <= e < E)
+    pos = torch.full((len(flat),), -1, dtype=torch.int32)
+    for r, (_, i) in enumerate(order):
+        pos[i] = r
+    ends, c = [], 0
+    for e in range(E):
+        c += sum(1 for x in flat if x == e)
+        ends.append(c)
+    return pos.reshape(ids.shape), torch.tensor(ends, dtype=torch.int32)
+
+
+def logits_of(T, E, dtype, seed, closed=0, ties=False):
+    g = torch.Generator().manual_seed(seed)
+    l = torch.randn(T, E, generator=g) * 2.0
+    if ties:
+        l = (l * 2).round() / 2
+        l[l == 0] *= -1.0  # both zeros, equal to each other
+    if closed:
+        l[:, torch.randperm(E, generator=g)[:closed]] = -math.inf
+    return l.to(dtype)
+
+
+def ids_of(T, E, k, seed, dropped=0.0):
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.stack([torch.randperm(max(E, k), generator=g)[:k] % E for _ in range(T)]).to(torch.int32) \
+        if T else torch.zeros(0, k, dtype=torch.int32)
+    ids[torch.rand(T, k, generator=g) < dropped] = -1
+    return ids
+
+
+def near(got, want, tol, what):
+    got, want, tol = got.detach().double().cpu(), want.double(), torch.as_tensor(tol, dtype=torch.float64)
+    assert got.shape == want.shape, what
+    nan = want.isnan()
+    assert torch.equal(got.isnan(), nan), f"{what}: NaN in other places"
+    over = ((got - want).abs() > tol)[~nan] if tol.dim() else ((got - want).abs()[~nan] > tol)
+    assert not bool(over.any()), f"{what}: off by {float((got - want).abs()[~nan].max())}"
+
+
+# ------------------------------------------------------------ refusals (CPU)
+def test_host_checks():
+    L = mxq.lib()
+    p = 256  # a non-null pointer that is never followed: the checks come first
+    assert L.moe_route(p, 0, 4, 0, 0, None, 1, 0, p, p, p, p, None, p, 1 << 20, None) == mxq.ERR_SHAPE
+    assert L.moe_route(p, 0, 4, 8, 7, None, 1, 0, p, p, p, p, None, p, 1 << 20, None) == mxq.ERR_SHAPE
+    assert L.moe_route(p, 0, 4, 8, 8, None, 9, 0, p, p, p, p, None, p, 1 << 20, None) == mxq.ERR_SHAPE
+    assert L.moe_route(p, 0, 4, 8, 8, None, 0, 0, p, p, p, p, None, p, 1 << 20, None) == mxq.ERR_SHAPE
+    assert L.moe_route(p, 2, 4, 8, 8, None, 2, 0, p, p, p, p, None, p, 1 << 20, None) == mxq.ERR_UNSUPPORTED
+    assert L.moe_route(p, 0, 4, 1025, 1025, None, 2, 0, p, p, p, p, None, p, 1 << 20, None) == mxq.ERR_UNSUPPORTED
+    assert L.moe_route(p, 0, 4, 64, 64, None, 33, 0, p, p, p, p, None, p, 1 << 20, None) == mxq.ERR_UNSUPPORTED
+    assert L.moe_route(None, 0, 4, 8, 8, None, 2, 0, p, p, p, p, None, p, 1 << 20, None) == mxq.ERR_NULL
+    assert L.moe_route(p, 0, 4, 8, 8, None, 2, 0, p, None, p, p, None, p, 1 << 20, None) == mxq.ERR_NULL
+    assert L.moe_route(p + 1, 0, 4, 8, 8, None, 2, 0, p, p, p, p, None, p, 1 << 20, None) == mxq.ERR_ALIGN
+    assert L.moe_route_backward(p, 0, 4, 8, 8, None, 2, 0, p, p, None, p, p, p, None) == mxq.ERR_NULL
+    assert L.moe_route_backward(p, 1, 4, 8, 8, None, 2, 0, p, p, p, p, p, None, None) == mxq.ERR_NULL
+    assert L.moe_route_backward(p + 2, 1, 4, 8, 8, None, 2, 0, p, p, p, p, p, p, None) == mxq.ERR_ALIGN
+    assert L.moe_route_backward(None, 0, 0, 8, 8, None, 2, 0, None, None, None, None, None, None, None) == mxq.OK
+    assert L.moe_dispatch_plan(p, -1, 8, p, p, None, 0, None) == mxq.ERR_SHAPE
+    assert L.moe_dispatch_plan(p, 8, 1025, p, p, None, 0, None) == mxq.ERR_UNSUPPORTED
+    assert L.moe_dispatch_plan(p, 1 << 31, 8, p, p, None, 0, None) == mxq.ERR_UNSUPPORTED
+    assert L.moe_dispatch_plan(p, 8, 8, None, p, None, 0, None) == mxq.ERR_NULL
+    assert L.moe_dispatch_plan(p, 100000, 8, p, p, None, 0, None) == mxq.ERR_WORKSPACE
+    assert L.moe_dispatch(p, 0, 4, 64, 63, p, 2, p, 4, p, 16, None) == mxq.ERR_SHAPE
+    assert L.moe_dispatch(p, 0, 4, 64, 64, p, 33, p, 4, p, 16, None) == mxq.ERR_UNSUPPORTED
+    assert L.moe_dispatch(p, 0, 4, 64, 64, p, 2, None, 4, p, 16, None) == mxq.ERR_NULL
+    assert L.moe_dispatch(p, 1, 4, 64, 64, p, 2, p, 4, p + 2, 16, None) == mxq.ERR_ALIGN
+    assert L.moe_dispatch(None, 0, 0, 64, 64, None, 2, None, 4, None, 0, None) == mxq.OK
+    assert L.moe_combine(p, 0, 16, 64, 60, p, p, 4, 2, p, None) == mxq.ERR_SHAPE
+    assert L.moe_combine(p, 0, 16, 64, 64, p, p, 4, 0, p, None) == mxq.ERR_SHAPE
+    assert L.moe_combine(p, 0, 16, 64, 64, None, p, 4, 2, p, None) == mxq.ERR_NULL
+    assert L.moe_combine(None, 0, 0, 64, 64, None, None, 0, 2, None, None) == mxq.OK
+    assert L.moe_combine_backward(p, 64, p, 64, 0, 16, 64, p, p, 4, 2, None, 4, p, p, None) == mxq.ERR_NULL
+    assert L.moe_combine_backward(p, 60, p, 64, 0, 16, 64, p, p, 4, 2, p, 4, p, p, None) == mxq.ERR_SHAPE
+    assert L.mxq_status_string(mxq.ERR_BAD_INDEX) == b"index out of range"
+
+
+def test_workspace_sizes():
+    L = mxq.lib()
+    assert L.moe_dispatch_plan_workspace_bytes(8192, 64) == 0
+    assert L.moe_dispatch_plan_workspace_bytes(8193, 64) == 2 * 64 * 4
+    assert L.moe_dispatch_plan_workspace_bytes(64 * 8192 + 1, 64) == 33 * 64 * 4
+    assert L.moe_route_workspace_bytes(-1, 64) == 0 and L.moe_route_workspace_bytes(16, 2000) == 0
+
+
+def test_cpu_tensors_are_refused():
+    x = torch.zeros(4, 8)
+    ids = torch.zeros(4, 2, dtype=torch.int32)
+    for call in (lambda: mxq.moe_route(x, 2), lambda: mxq.moe_dispatch_plan(ids, 4),
+                 lambda: mxq.moe_dispatch(x, ids, ids[0]), lambda: mxq.moe_combine(x, ids),
+                 lambda: mxq.moe_combine_backward(x, x, ids, None, ids[0])):
+        with pytest.raises(TypeError):
+            call()
+
+
+def test_fake_shapes():
+    import mxfp8_quantization_moe_device_b200.ops  # noqa: F401
+    o = torch.ops.mxq
+    x = torch.empty(30, 24, dtype=torch.bfloat16, device="meta")
+    w, ids, counts, loss, lg = o.moe_route(x, 3, None, True)
+    assert w.shape == ids.shape == (30, 3) and counts.shape == lg.shape == (24,) and loss.shape == ()
+    assert w.dtype == torch.float32 and ids.dtype == counts.dtype == torch.int32
+    d = o.moe_route_backward(x, w, ids, lg, w, loss, None, True)
+    assert d.shape == x.shape and d.dtype == x.dtype
+    pos, offs = o.moe_dispatch_plan(ids, 24)
+    assert pos.shape == (30, 3) and offs.shape == (24,) and offs.dtype == torch.int32
+    xs = o.moe_dispatch(x, pos, offs)
+    assert xs.shape == (96, 24) and xs.dtype == x.dtype
+    assert o.moe_combine(xs, pos, w).shape == (30, 24)
+    dy, dw = o.moe_combine_backward(x, xs, pos, w, offs)
+    assert dy.shape == (96, 24) and dw.shape == (30, 3) and dw.dtype == torch.float32
+
+
+@pytest.mark.gpu
+def test_registered_ops():
+    import mxfp8_quantization_moe_device_b200.ops  # noqa: F401
+    o = torch.ops.mxq
+    x = torch.randn(30, 24, device=DEV).bfloat16()
+    valid = torch.ones(30, dtype=torch.bool, device=DEV)
+    w, ids, counts, loss, lg = o.moe_route(x, 3, valid, True)
+    pos, offs = o.moe_dispatch_plan(ids, 24)
+    xs = o.moe_dispatch(x, pos, offs)
+    g = torch.ones((), device=DEV)
+    for a, b in zip((w, ids, counts, loss), mxq.moe_route(x, 3, renormalize=True)):
+        assert torch.equal(a, b)
+    for op, args in ((o.moe_route, (x, 3, valid, True)), (o.moe_route, (x, 2, None, False)),
+                     (o.moe_route_backward, (x, w, ids, lg, w, g, valid, True)), (o.moe_dispatch_plan, (ids, 24)),
+                     (o.moe_dispatch, (x, pos, offs)), (o.moe_combine, (xs, pos, w)),
+                     (o.moe_combine_backward, (x, xs, pos, w, offs))):
+        torch.library.opcheck(op, args, test_utils=("test_schema", "test_faketensor"))
+
+
+# ------------------------------------------------------------ router
+ROUTE = [(1, 1, 1), (1, 4, 4), (3, 7, 2), (33, 8, 3), (40, 16, 1), (65, 24, 5), (130, 60, 4), (70, 64, 8),
+         (257, 100, 6), (64, 128, 32), (300, 256, 8), (50, 257, 3), (41, 512, 10), (9, 700, 32), (21, 1024, 16)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", ROUTE)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_and_gradient(T, E, k, dtype, renorm):
+    l = logits_of(T, E, dtype, T + E, closed=1 if E > 4 else 0, ties=T % 2 == 0)
+    g = torch.Generator().manual_seed(7)
+    valid = (torch.rand(T, generator=g) < 0.8) if T > 2 else None
+    gw, gl = torch.randn(T, k, generator=g), torch.tensor(3.0)
+    w, ids, counts, loss, d, mag = ref_route(l, k, valid, renorm, gw, gl)
+    x = l.to(DEV).requires_grad_(True)
+    v = valid.to(DEV) if valid is not None else None
+    gotw, goti, gotc, gotl = autograd.moe_route(x, k, valid=v, renormalize=renorm)
+    assert torch.equal(goti.cpu(), ids) and torch.equal(gotc.cpu(), counts)
+    near(gotw, w, 2.0 ** -18 * w + 1e-12, "weights")
+    near(gotl, loss, 2.0 ** -18 * float(loss) + 1e-30, "loss")
+    (gd,) = torch.autograd.grad((gotw, gotl), (x,), (gw.to(DEV), gl.to(DEV)))
+    assert gd.dtype == dtype
+    near(gd, d, U[dtype] * d.abs() + 2.0 ** -17 * mag + 1e-12, "gradient")
+    # each gradient alone, and the forward without autograd
+    only = ref_route(l, k, valid, renorm, gw, None)
+    (gd,) = torch.autograd.grad(autograd.moe_route(x, k, valid=v, renormalize=renorm)[0], x, gw.to(DEV))
+    near(gd, only[4], U[dtype] * only[4].abs() + 2.0 ** -17 * only[5] + 1e-12, "gradient of the weights")
+    only = ref_route(l, k, valid, renorm, None, gl)
+    (gd,) = torch.autograd.grad(autograd.moe_route(x, k, valid=v, renormalize=renorm)[3], x, gl.to(DEV))
+    near(gd, only[4], U[dtype] * only[4].abs() + 2.0 ** -17 * only[5] + 1e-12, "gradient of the loss")
+    again = mxq.moe_route(x.detach(), k, valid=v, renormalize=renorm)
+    for a, b in zip(again, (gotw, goti, gotc, gotl)):
+        assert torch.equal(a, b.detach())
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_route_gradient_against_differences():
+    # central differences in 64 bits of the definition's value, h = 1e-5: the
+    # quotient's own error is below 1e-8
+    T, E, k, h = 5, 12, 3, 1e-5
+    l = logits_of(T, E, torch.float32, 3)
+    g = torch.Generator().manual_seed(1)
+    gw = torch.randn(T, k, generator=g, dtype=torch.float64)
+
+    def value(x):
+        w, _, _, loss = ref_route(x, k, None, True)
+        return float((w * gw).sum() + 2.0 * loss)
+
+    x = l.to(DEV).requires_grad_(True)
+    w, _, _, loss = autograd.moe_route(x, k, renormalize=True)
+    (d,) = torch.autograd.grad((w, loss), x, (gw.float().to(DEV), torch.tensor(2.0, device=DEV)))
+    for t in range(T):
+        for e in range(E):
+            up, dn = l.double(), l.double()
+            up[t, e] += h
+            dn[t, e] -= h
+            num = (value(up) - value(dn)) / (2 * h)
+            assert abs(num - float(d[t, e])) <= 1e-5 * (1.0 + abs(num))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_route_rows_that_choose_nothing(dtype):
+    T, E, k = 40, 20, 4
+    l = logits_of(T, E, dtype, 11)
+    l[0] = -math.inf                       # no expert left
+    l[1] = torch.finfo(dtype).min          # the type's lowest value: choosable
+    l[2, 2:] = -math.inf                   # fewer experts than slots
+    l[3] = torch.finfo(dtype).max
+    l[4, 1:] = torch.finfo(dtype).min
+    valid = torch.ones(T, dtype=torch.bool)
+    valid[5:9] = False
+    l[6] = math.nan                        # in a padded row: not looked at
+    l[7] = math.inf
+    gw = torch.ones(T, k)
+    w, ids, counts, loss, d, mag = ref_route(l, k, valid, True, gw, torch.tensor(1.0))
+    x = l.to(DEV).requires_grad_(True)
+    gotw, goti, gotc, gotl = autograd.moe_route(x, k, valid=valid.to(DEV), renormalize=True)
+    assert torch.equal(goti.cpu(), ids) and torch.equal(gotc.cpu(), counts)
+    near(gotw, w, 2.0 ** -18 * w + 1e-12, "weights")
+    near(gotl, loss, 2.0 ** -18 * float(loss), "loss")
+    (gd,) = torch.autograd.grad((gotw, gotl), x, (gw.to(DEV), torch.tensor(1.0, device=DEV)))
+    near(gd, d, U[dtype] * d.abs() + 2.0 ** -17 * mag + 1e-12, "gradient")
+    # a NaN or +inf in a row that counts shows in its weights and in the loss
+    l[10, 3] = math.nan
+    l[11, 4] = math.inf
+    w, ids, counts, loss, d, mag = ref_route(l, k, valid, False, gw, torch.tensor(1.0))
+    x = l.to(DEV).requires_grad_(True)
+    gotw, goti, gotc, gotl = autograd.moe_route(x, k, valid=valid.to(DEV))
+    assert torch.equal(goti.cpu(), ids) and torch.equal(gotc.cpu(), counts) and bool(gotl.isnan())
+    near(gotw, w, 2.0 ** -18 * w.nan_to_num() + 1e-12, "weights")
+    (gd,) = torch.autograd.grad(gotw, x, gw.to(DEV))
+    assert bool(gd[10].isnan().all()) and bool(gd[11].isnan().all()) and not bool(gd[12:].isnan().any())
+    # all tokens padded
+    out = mxq.moe_route(x.detach(), k, valid=torch.zeros(T, dtype=torch.bool, device=DEV))
+    assert float(out[3]) == 0.0 and int(out[2].sum()) == 0 and bool((out[1] == -1).all())
+
+
+@pytest.mark.gpu
+def test_route_no_tokens_strides_and_many_tokens():
+    out = mxq.moe_route(torch.zeros(0, 8, device=DEV), 2)
+    assert out[0].shape == (0, 2) and float(out[3]) == 0.0 and int(out[2].abs().sum()) == 0
+    # rows inside a wider buffer, an odd first element
+    buf = torch.randn(3000, 70, device=DEV).bfloat16()
+    for view in (buf[:, :64], buf[:, 3:67], buf[::2, 1:61]):
+        a, b = mxq.moe_route(view, 4, renormalize=True), mxq.moe_route(view.contiguous(), 4, renormalize=True)
+        for p, q in zip(a, b):
+            assert torch.equal(p, q)
+    # more tokens than the grid takes at once: against torch in 64 bits
+    T, E, k = 70001, 64, 6
+    l = torch.randn(T, E, device=DEV)
+    w, ids, counts, loss = mxq.moe_route(l, k)
+    p = torch.softmax(l.double(), 1)
+    ri = torch.sort(l, dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(ids.long(), ri)
+    rc = torch.bincount(ri.reshape(-1), minlength=E)
+    assert torch.equal(counts.long(), rc)
+    rl = E * float((rc.double() / (k * T) * p.mean(0)).sum())
+    assert abs(float(loss) - rl) <= 2.0 ** -18 * rl
+    near(w, p.gather(1, ri).cpu(), 2.0 ** -18 * p.gather(1, ri).cpu(), "weights")
+    for _ in range(3):
+        again = mxq.moe_route(l, k)
+        assert all(torch.equal(a, b) for a, b in zip(again, (w, ids, counts, loss)))
+
+
+# ------------------------------------------------------------ order by expert
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", [(0, 5, 2), (1, 1, 1), (5, 3, 2), (100, 16, 4), (1024, 60, 8), (1025, 64, 8),
+                                   (3000, 7, 6), (2000, 1024, 32), (300, 1000, 5)])
+@pytest.mark.parametrize("dropped", [0.0, 0.3])
+def test_plan(T, E, k, dropped):
+    ids = ids_of(T, E, k, T + E + k, dropped)
+    pos, offs = mxq.moe_dispatch_plan(ids.to(DEV), E)
+    rp, ro = ref_plan(ids, E)
+    assert torch.equal(pos.cpu(), rp) and torch.equal(offs.cpu(), ro)
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_plan_many_entries_one_expert_and_bad_ids():
+    # several tiles per chunk, against a stable sort
+    T, E, k = 90001, 37, 8
+    ids = torch.randint(0, E, (T, k), device=DEV, dtype=torch.int32)
+    ids[torch.rand(T, k, device=DEV) < 0.1] = -1
+    for x in (ids, torch.full_like(ids, 36), torch.full_like(ids, -5)):
+        pos, offs = mxq.moe_dispatch_plan(x, E)
+        flat = x.reshape(-1).long()
+        key = torch.where(flat < 0, E, flat)
+        order = torch.sort(key, stable=True).indices
+        want = torch.empty_like(flat)
+        want[order] = torch.arange(flat.numel(), device=DEV)
+        want[flat < 0] = -1
+        assert torch.equal(pos.reshape(-1).long(), want)
+        assert torch.equal(offs.long(), torch.cumsum(torch.bincount(key, minlength=E + 1)[:E], 0))
+    # the same expert twice in a token: two rows, the first slot first
+    pos, offs = mxq.moe_dispatch_plan(torch.tensor([[2, 2], [0, 2]], dtype=torch.int32, device=DEV), 3)
+    assert pos.tolist() == [[1, 2], [0, 3]] and offs.tolist() == [1, 1, 4]
+    # an id past the experts is dropped and reported
+    pos, offs = mxq.moe_dispatch_plan(torch.tensor([[3, 1], [0, 9]], dtype=torch.int32, device=DEV), 3)
+    assert pos.tolist() == [[-1, 1], [0, -1]] and offs.tolist() == [1, 2, 2]
+    assert mxq.device_status() == mxq.ERR_BAD_INDEX and mxq.device_status() == 0
+
+
+# ------------------------------------------------------------ rows
+ROWS = [(0, 4, 2, 64), (1, 3, 1, 1), (3, 4, 2, 8), (17, 5, 3, 63), (50, 16, 2, 2048), (33, 60, 6, 1419),
+        (129, 8, 8, 514), (20, 40, 32, 100), (7, 4, 2, 7168), (260, 4, 4, 130)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k,K", ROWS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dropped", [0.0, 0.25, 1.0])
+def test_dispatch_combine_and_gradients(T, E, k, K, dtype, dropped):
+    g = torch.Generator().manual_seed(T + K)
+    ids = ids_of(T, E, k, 5 * T + k, dropped)
+    x = torch.randn(T, K, generator=g).to(dtype)
+    w = torch.randn(T, k, generator=g)
+    xd, wd = x.to(DEV).requires_grad_(True), w.to(DEV).requires_grad_(True)
+    xs, pos, offs = autograd.moe_dispatch(xd, ids.to(DEV), E)
+    M = mxq.moe_dispatch_rows(T * k)
+    rp, ro = ref_plan(ids, E)
+    assert torch.equal(pos.cpu(), rp) and torch.equal(offs.cpu(), ro) and xs.shape == (M, K)
+    want = torch.zeros(M, K, dtype=dtype)
+    for t in range(T):
+        for j in range(k):
+            if rp[t, j] >= 0:
+                want[rp[t, j]] = x[t]
+    assert torch.equal(xs.detach().cpu(), want)
+    gxs = torch.randn(M, K, generator=g).to(dtype)
+    (dx,) = torch.autograd.grad(xs, xd, gxs.to(DEV))
+    live = (rp >= 0)[..., None].double()
+    rows = gxs.double()[rp.clamp(min=0).long().reshape(-1)].reshape(T, k, K) * live if M else torch.zeros(T, k, K)
+    ref, mag = rows.sum(1), rows.abs().sum(1)
+    near(dx, ref, U[dtype] * ref.abs() + (k + 1) * 2.0 ** -24 * mag, "gradient of dispatch")
+    # combine
+    y = torch.randn(M, K, generator=g).to(dtype)
+    yd = y.to(DEV).requires_grad_(True)
+    out = autograd.moe_combine(yd, pos, wd, offs)
+    rows = y.double()[rp.clamp(min=0).long().reshape(-1)].reshape(T, k, K) if M else torch.zeros(T, k, K)
+    terms = rows * w.double()[..., None] * live
+    near(out, terms.sum(1), U[dtype] * terms.sum(1).abs() + (k + 1) * 2.0 ** -24 * terms.abs().sum(1), "combine")
+    dout = torch.randn(T, K, generator=g).to(dtype)
+    dy, dw = torch.autograd.grad(out, (yd, wd), dout.to(DEV))
+    ref = torch.zeros(M, K, dtype=torch.float64)
+    for t in range(T):
+        for j in range(k):
+            if rp[t, j] >= 0:
+                ref[rp[t, j]] = w[t, j].double() * dout[t].double()
+    near(dy, ref, U[dtype] * ref.abs() + 2.0 ** -24 * ref.abs(), "gradient of combine by rows")
+    dots = rows * dout.double()[:, None, :] * live
+    near(dw, dots.sum(2), (K + 1) * 2.0 ** -24 * dots.abs().sum(2), "gradient of combine by weights")
+    # no weights: ones
+    ones = mxq.moe_combine(yd.detach(), pos)
+    assert torch.equal(ones, mxq.moe_combine(yd.detach(), pos, torch.ones(T, k, device=DEV)))
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_strides_offsets_and_poison(dtype):
+    T, E, k = 37, 6, 3
+    ids = ids_of(T, E, k, 1, 0.2).to(DEV)
+    pos, offs = mxq.moe_dispatch_plan(ids, E)
+    M, n = mxq.moe_dispatch_rows(T * k), int(offs[-1])
+    w = torch.rand(T, k, device=DEV)
+    buf = torch.randn(T, 300, device=DEV).to(dtype)
+    for lo, hi in ((0, 256), (8, 264), (2, 258), (1, 258), (4, 260)):
+        v = buf[:, lo:hi]
+        xs = mxq.moe_dispatch(v, pos, offs)
+        assert torch.equal(xs, mxq.moe_dispatch(v.contiguous(), pos, offs))
+        wide = torch.full((M, 300), math.nan, device=DEV).to(dtype)
+        wide[:, lo:hi] = xs
+        y = wide[:, lo:hi]
+        y[n:] = math.nan  # rows behind the last group are not read
+        assert torch.equal(mxq.moe_combine(y, pos, w), mxq.moe_combine(y.contiguous(), pos, w))
+        assert not bool(mxq.moe_combine(y, pos, w).isnan().any())
+        a = mxq.moe_combine_backward(v, y, pos, w, offs)
+        b = mxq.moe_combine_backward(v.contiguous(), y.contiguous(), pos, w, offs)
+        assert torch.equal(a[0], b[0])
+        # rows on other boundaries move in other vectors, so a dot's terms are
+        # added in another order: two sums of K terms, each within K 2^-24 of
+        # the sum of absolute values
+        K = hi - lo
+        mag = (v.double().abs() @ torch.nan_to_num(y.double()).abs().t()).gather(1, pos.clamp(min=0).long())
+        near(a[1], b[1].cpu(), 2 * K * 2.0 ** -24 * mag.cpu(), "dots of strided rows")
+        assert bool((a[0][n:] == 0).all()) and not bool(a[1].isnan().any())
+        only_y = mxq.moe_combine_backward(v, y, pos, w, offs, need_weights=False)
+        only_w = mxq.moe_combine_backward(v, y, pos, w, offs, need_y=False)
+        assert only_y[1] is None and only_w[0] is None
+        assert torch.equal(only_y[0], a[0]) and torch.equal(only_w[1], a[1])
+    # a place past the rows is skipped and reported; fewer rows than places
+    short = mxq.moe_dispatch(buf, pos, offs, out=torch.empty(16, 300, dtype=dtype, device=DEV))
+    assert torch.equal(short, mxq.moe_dispatch(buf, pos, offs)[:16]) and mxq.device_status() == mxq.ERR_BAD_INDEX
+    mxq.moe_combine(torch.zeros(16, 300, dtype=dtype, device=DEV), pos, w)
+    assert mxq.device_status() == mxq.ERR_BAD_INDEX and mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_refusals_of_the_binding():
+    x = torch.randn(8, 64, device=DEV).bfloat16()
+    ids = torch.zeros(8, 2, dtype=torch.int32, device=DEV)
+    pos, offs = mxq.moe_dispatch_plan(ids, 4)
+    w = torch.ones(8, 2, device=DEV)
+    bad = [lambda: mxq.moe_route(x.half(), 2), lambda: mxq.moe_route(x.t(), 2), lambda: mxq.moe_route(x[0], 2),
+           lambda: mxq.moe_route(x[:1].expand(8, 64), 2), lambda: mxq.moe_route(x, 2, valid=w[:, 0]),
+           lambda: mxq.moe_route(x, 2, valid=torch.ones(7, dtype=torch.bool, device=DEV)),
+           lambda: mxq.moe_route(x, 2, ids=ids.long()), lambda: mxq.moe_dispatch_plan(ids.long(), 4),
+           lambda: mxq.moe_dispatch_plan(ids.t(), 4), lambda: mxq.moe_dispatch(x, pos[:7], offs),
+           lambda: mxq.moe_dispatch(x, pos, offs.long()), lambda: mxq.moe_dispatch(x.t(), pos, offs),
+           lambda: mxq.moe_dispatch(x, pos, offs, out=torch.empty(16, 63, device=DEV).bfloat16()),
+           lambda: mxq.moe_combine(x, pos, w.double()), lambda: mxq.moe_combine(x, pos, w[:, :1]),
+           lambda: mxq.moe_combine(x, pos.long(), w), lambda: mxq.moe_combine_backward(x.float(), x, pos, w, offs),
+           lambda: mxq.moe_combine_backward(x[:, :32], x, pos, w, offs),
+           lambda: mxq.moe_route_backward(x, w, ids.long(), None, w, None),
+           lambda: mxq.moe_route_backward(x, w, ids, None, w, w[0, 0])]
+    for call in bad:
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: mxq.moe_route(x, 0), lambda: mxq.moe_route(x, 65), lambda: mxq.moe_dispatch_plan(ids, 0),
+                 lambda: mxq.moe_combine(x, pos[:, :0])):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(mxq.MXQError):
+        mxq.moe_route(x, 33)
+    assert mxq.device_status() == 0
+
+
+# ------------------------------------------------------------ together
+def _layer(x, wr, we, k, offs_check=None):
+    logits = x @ wr
+    w, ids, counts, loss = autograd.moe_route(logits, k, renormalize=True)
+    xs, pos, offs = autograd.moe_dispatch(x, ids, we.shape[0])
+    y = autograd.fp8_grouped_mm(xs, we, offs)
+    return autograd.moe_combine(y, pos, w, offs), counts, offs, loss
+
+
+@pytest.mark.gpu
+def test_layer_forward_and_backward():
+    """Router, dispatch, the FP8 grouped product and combine as one layer,
+    against the same layer with exact products: an e4m3 operand is off by up
+    to 2^-4 of its value, about 0.026 in the mean square, so a product of two
+    is off by about 0.037 of its norm, and a gradient by the router on top of
+    it stays below 0.08 (the bound of the grouped product's own tests)."""
+    T, E, k, K, N = 200, 6, 2, 256, 128
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(T, K, generator=g, device=DEV).bfloat16().requires_grad_(True)
+    wr = (torch.randn(K, E, generator=g, device=DEV) * 0.1).bfloat16().requires_grad_(True)
+    we = (torch.randn(E, N, K, generator=g, device=DEV) * 0.05).bfloat16().requires_grad_(True)
+    dout = torch.randn(T, N, generator=g, device=DEV).bfloat16()
+    out, counts, offs, loss = _layer(x, wr, we, k)
+    assert torch.equal(torch.cumsum(counts, 0).int(), offs)
+    grads = torch.autograd.grad((out, loss), (x, wr, we), (dout, torch.tensor(0.5, device=DEV)))
+    # the same in 64 bits with the logits' bf16 rounding kept
+    xr, wrr, wer = (t.detach().double().requires_grad_(True) for t in (x, wr, we))
+    lg = xr @ wrr
+    lg = lg + ((x.detach() @ wr.detach()).double() - lg).detach()
+    p = torch.softmax(lg, 1)
+    ids = torch.sort(lg.detach(), dim=1, descending=True, stable=True).indices[:, :k]
+    w = p.gather(1, ids)
+    w = w / w.sum(1, keepdim=True)
+    ref = sum(w[:, j:j + 1] * torch.einsum("tk,tnk->tn", xr, wer[ids[:, j]]) for j in range(k))
+    f = torch.bincount(ids.reshape(-1), minlength=E).double() / (k * T)
+    rl = E * (f * p.mean(0)).sum()
+    want = torch.autograd.grad((ref, rl), (xr, wrr, wer), (dout.double(), torch.tensor(0.5, device=DEV).double()))
+    assert abs(float(loss.detach()) - float(rl.detach())) <= 2.0 ** -17 * float(rl.detach())
+    for got, r, name in zip((out, *grads), (ref, *want), ("out", "dx", "dwr", "dwe")):
+        assert torch.linalg.norm(got.detach().double() - r.detach()) <= 0.08 * torch.linalg.norm(r.detach()), name
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_streams_graphs_and_calls_at_once():
+    T, E, k, K = 20000, 64, 4, 256
+    l = torch.randn(T, E, device=DEV).bfloat16()
+    x = torch.randn(T, K, device=DEV).bfloat16()
+
+    def step():
+        w, ids, counts, loss = mxq.moe_route(l, k, renormalize=True)
+        pos, offs = mxq.moe_dispatch_plan(ids, E)
+        xs = mxq.moe_dispatch(x, pos, offs)
+        return [w, ids, counts, loss, pos, offs, xs, mxq.moe_combine(xs, pos, w),
+                *mxq.moe_combine_backward(x, xs, pos, w, offs)]
+
+    want = step()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append(step())
+    torch.cuda.synchronize()
+    for r in got:
+        assert all(torch.equal(a, b) for a, b in zip(r, want))
+    # two graphs of the same step on new inputs, replayed at once on two streams
+    graphs = []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            graphs.append((gr, step()))
+    l.copy_(torch.randn(T, E, device=DEV))
+    x.copy_(torch.randn(T, K, device=DEV))
+    torch.cuda.synchronize()
+    for (gr, _), s in zip([g for g in graphs], streams):
+        with torch.cuda.stream(s):
+            gr.replay()
+    torch.cuda.synchronize()
+    want = step()
+    torch.cuda.synchronize()
+    for _, out in graphs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert mxq.device_status() == 0

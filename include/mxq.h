@@ -526,6 +526,25 @@ int moe_combine_backward(const void *grad_out, int64_t grad_row_stride, const vo
                          float *grad_weights, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ *
+ * Orthogonalisation of weight updates by Newton-Schulz products. For every
+ * matrix G of g (batch, rows, cols), bf16 or fp32, row-major:
+ *   X = G / (|G|_F + eps), transposed when rows > cols; then `steps` times,
+ *   with (a, b, c) = coefficients[3 s], [3 s + 1], [3 s + 2] (host memory):
+ *   A = X X^T;  X = a X + (b A + c A A) X
+ * out (batch, rows, cols) bf16, row-major. The products run in fp16 with fp32
+ * sums on X held in 22 bits; singular values should stay below 4 on the way
+ * (they do for the usual coefficients) and coefficients within [-16, 16]. A
+ * matrix of zeros gives zeros; a NaN or infinity makes its own matrix NaN and
+ * no other. rows, cols <= 65536, batch <= 65535, steps <= 64. workspace:
+ * newton_schulz_workspace_bytes() bytes, 256-byte aligned, not shared by
+ * calls that overlap on the GPU.
+ * ------------------------------------------------------------------------ */
+size_t newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, int32_t steps);
+int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols, int32_t steps,
+                  const float *coefficients, double eps, void *out, void *workspace, size_t workspace_bytes,
+                  cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ *
  * Status and housekeeping
  * ------------------------------------------------------------------------ */
 

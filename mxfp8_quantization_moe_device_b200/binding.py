@@ -70,6 +70,9 @@ SIGNATURES = {
     "moe_combine": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp]),
     "moe_combine_backward": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _i32,
                                             _vp, _vp, _vp]),
+    "newton_schulz_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
+    "newton_schulz": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i64, _i32, ctypes.POINTER(ctypes.c_float),
+                                     ctypes.c_double, _vp, _vp, _sz, _vp]),
     "mxq_device_status": (ctypes.c_int, [_vp, ctypes.POINTER(_i32)]),
     "mxq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "mxq_version": (ctypes.c_int, []),
@@ -747,6 +750,34 @@ def moe_combine_backward(grad_out, y, pos, weights, offs, *, need_y=True, need_w
     _call("moe_combine_backward", dev, _ptr(grad_out), ldg, _ptr(y), ld, code, M, K, _ptr(pos), _ptr(weights), T, k,
           _ptr(offs), offs.numel(), _ptr(grad_y), _ptr(grad_weights))
     return grad_y, grad_weights
+
+
+# ---------------------------------------------------------------- orthogonalisation
+
+def newton_schulz(g, *, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, out=None):
+    """Orthogonalise every matrix of g (E, N, K) (or one, (N, K)) bf16 or fp32
+    by Newton-Schulz products: X = G / (|G|_F + eps), then steps times A = X
+    X^T, X = a X + (b A + c A A) X (on the transpose when N > K).
+    coefficients: one (a, b, c) for all steps or one per step. Returns bf16 of
+    g's shape. Takes the expert weight gradients (or their momentum) that the
+    weight-gradient GEMMs return."""
+    _cuda(g, "g")
+    if g.dim() not in (2, 3) or g.dtype not in _DTYPES or not g.is_contiguous():
+        raise TypeError("g must be a contiguous (E, N, K) or (N, K) bfloat16 or float32 tensor")
+    steps = int(steps)
+    if not 1 <= steps <= 64:
+        raise ValueError("steps must lie in [1, 64]")
+    rows = [coefficients] * steps if not hasattr(coefficients[0], "__len__") else list(coefficients)
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError("coefficients must be one (a, b, c), or one per step")
+    co = (ctypes.c_float * (3 * steps))(*(float(v) for r in rows for v in r))
+    dev = g.device
+    E, N, K = g.shape if g.dim() == 3 else (1, *g.shape)
+    out = _output(out, "out", torch.bfloat16, g.shape, dev)
+    ws = _workspace(lib().newton_schulz_workspace_bytes(E, N, K, steps), dev)
+    _call("newton_schulz", dev, _ptr(g), _DTYPES[g.dtype], E, N, K, steps, co, float(eps), _ptr(out), _ptr(ws),
+          ws.numel() if ws is not None else 0)
+    return out
 
 
 # ---------------------------------------------------------------- status

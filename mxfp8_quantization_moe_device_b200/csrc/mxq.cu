@@ -18,6 +18,7 @@
 #include "gemm2.cuh"
 #include "mxj.cuh"
 #include "moe.cuh"
+#include "ns.cuh"
 
 using namespace mxq;
 
@@ -1214,3 +1215,4 @@ int mxq_testing_set(int32_t what, int64_t value)
 } // extern "C"
 
 #include "moe_host.cuh"
+#include "ns_host.cuh"

@@ -414,3 +414,19 @@ def moe_combine_backward(grad_out: torch.Tensor, y: torch.Tensor, pos: torch.Ten
 @moe_combine_backward.register_fake
 def _(grad_out, y, pos, weights, offs):
     return y.new_empty(y.shape), y.new_empty(pos.shape, dtype=torch.float32)
+
+
+# ---------------------------------------------------------------- orthogonalisation
+
+@torch.library.custom_op("mxq::newton_schulz", mutates_args=())
+def newton_schulz(g: torch.Tensor, steps: int, coefficients: list[float], eps: float) -> torch.Tensor:
+    """Newton-Schulz orthogonalisation of every matrix of g (E, N, K) or (N,
+    K): bf16 of g's shape. coefficients: a, b, c of every step, one after
+    another, or one triple for all."""
+    co = [tuple(coefficients[i:i + 3]) for i in range(0, len(coefficients), 3)]
+    return _b.newton_schulz(g, steps=steps, coefficients=co[0] if len(co) == 1 else co, eps=eps)
+
+
+@newton_schulz.register_fake
+def _(g, steps, coefficients, eps):
+    return g.new_empty(g.shape, dtype=torch.bfloat16)

@@ -1,0 +1,242 @@
+"""Newton-Schulz orthogonalisation against the definition in 64 bits.
+
+Tolerance. `emulate` repeats the iteration in 64 bits with the roundings that
+the kernel's header states (X as hi + lo of fp16, the products on hi, A and B
+rounded once to fp16, the result to bf16); its distance from the exact
+iteration is what the scheme itself costs on that input. The kernel adds fp32
+sums: n terms, off by at most n 2^-24 of the sum of absolute values, which
+moves a result by far less than its fp16 rounding except where it flips one.
+So the kernel has to lie within 1.25 times the emulation's distance, in the
+Frobenius norm, plus 2^-20; and, for matrices of at least 16 rows and columns,
+within 2^-8 of the exact result's norm, bf16's own rounding bound. Below that
+size the second bound does not hold by arithmetic: with one singular value s
+the roundings of A and B (u = 2^-11 each) move a step's result by up to u (|B|
++ |b + 2 c s^2| s^2) s, which reaches 5.4 u, against a result of 0.7, so that
+already the last step can cost 2^-8, before bf16's rounding; in a matrix the
+entries' roundings are independent and average out.
+"""
+import ctypes
+
+import pytest
+import torch
+
+from mxfp8_quantization_moe_device_b200 import binding as mxq
+
+DEV = "cuda"
+COEF = (3.4445, -4.7750, 2.0315)
+
+
+def exact(g, coefs, eps=1e-7):
+    x = g.double()
+    x = x / (torch.linalg.vector_norm(x, dim=(-2, -1), keepdim=True) + eps)
+    t = x.shape[-2] > x.shape[-1]
+    x = x.mT if t else x
+    for a, b, c in coefs:
+        A = x @ x.mT
+        x = a * x + (b * A + c * (A @ A)) @ x
+    return x.mT if t else x
+
+
+def emulate(g, coefs, eps=1e-7):
+    def half(v, scale):
+        return (v * scale).half().double() / scale
+
+    x = g.double()
+    x = x / (torch.linalg.vector_norm(x, dim=(-2, -1), keepdim=True) + eps)
+    t = x.shape[-2] > x.shape[-1]
+    x = x.mT if t else x
+    for a, b, c in coefs:
+        hi = half(x, 256.0)
+        x = hi + half(x - hi, 256.0 * 2048.0)
+        A = half(hi @ hi.mT, 1024.0)
+        B = half(b * A + c * (A @ A), 1024.0)
+        x = a * x + B @ hi
+    x = x.mT if t else x
+    return x.bfloat16().double()
+
+
+def norm(x):
+    return torch.linalg.vector_norm(x, dim=(-2, -1))
+
+
+def matrices(E, N, K, dtype, seed, kind="gradient"):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn(E, N, K, generator=g, device=DEV)
+    if kind == "gradient":
+        r = max(1, min(N, K) // 16)
+        x = x + torch.randn(E, N, r, generator=g, device=DEV) @ torch.randn(E, r, K, generator=g, device=DEV) \
+            * (2.0 / r ** 0.5)
+        x = x * torch.exp(0.5 * torch.randn(E, N, 1, generator=g, device=DEV)) * 1e-3
+    elif kind == "decay":  # singular values from 1 down to 1e-4
+        u, s, v = torch.linalg.svd(x.double(), full_matrices=False)
+        x = (u * torch.logspace(0, -4, s.shape[-1], dtype=torch.float64, device=DEV)) @ v
+    return x.to(dtype)
+
+
+def check(got, g, coefs, eps=1e-7):
+    want = exact(g, coefs, eps)
+    assert got.shape == g.shape and got.dtype == torch.bfloat16
+    off, scheme, size = norm(got.double() - want), norm(emulate(g, coefs, eps) - want), norm(want)
+    assert bool((off <= 1.25 * scheme + 2.0 ** -20 * size).all()), (off / size, scheme / size)
+    if min(g.shape[-2:]) >= 16:
+        assert bool((off <= 2.0 ** -8 * size).all()), off / size
+
+
+# ------------------------------------------------------------ refusals (CPU)
+def test_host_checks():
+    L = mxq.lib()
+    p = 256
+    co = (ctypes.c_float * 3)(*COEF)
+    bad = (ctypes.c_float * 3)(3.0, -17.0, 2.0)
+    nan = (ctypes.c_float * 3)(3.0, float("nan"), 2.0)
+    big = 1 << 40
+    assert L.newton_schulz(p, 0, -1, 8, 8, 1, co, 1e-7, p, p, big, None) == mxq.ERR_SHAPE
+    assert L.newton_schulz(p, 0, 1, 8, 8, 0, co, 1e-7, p, p, big, None) == mxq.ERR_SHAPE
+    assert L.newton_schulz(p, 0, 1, 8, 8, 65, co, 1e-7, p, p, big, None) == mxq.ERR_UNSUPPORTED
+    assert L.newton_schulz(p, 0, 1, 65537, 8, 1, co, 1e-7, p, p, big, None) == mxq.ERR_UNSUPPORTED
+    assert L.newton_schulz(p, 3, 1, 8, 8, 1, co, 1e-7, p, p, big, None) == mxq.ERR_UNSUPPORTED
+    assert L.newton_schulz(p, 0, 1, 8, 8, 1, bad, 1e-7, p, p, big, None) == mxq.ERR_UNSUPPORTED
+    assert L.newton_schulz(p, 0, 1, 8, 8, 1, nan, 1e-7, p, p, big, None) == mxq.ERR_UNSUPPORTED
+    assert L.newton_schulz(p, 0, 1, 8, 8, 1, co, -1.0, p, p, big, None) == mxq.ERR_UNSUPPORTED
+    assert L.newton_schulz(p, 0, 1, 8, 8, 1, None, 1e-7, p, p, big, None) == mxq.ERR_NULL
+    assert L.newton_schulz(None, 0, 1, 8, 8, 1, co, 1e-7, p, p, big, None) == mxq.ERR_NULL
+    assert L.newton_schulz(p, 0, 1, 8, 8, 1, co, 1e-7, p + 1, p, big, None) == mxq.ERR_ALIGN
+    assert L.newton_schulz(p, 0, 1, 8, 8, 1, co, 1e-7, p, p + 16, big, None) == mxq.ERR_ALIGN
+    assert L.newton_schulz(p, 0, 1, 8, 8, 1, co, 1e-7, p, p, 100, None) == mxq.ERR_WORKSPACE
+    assert L.newton_schulz(p, 0, 0, 8, 8, 1, co, 1e-7, None, None, 0, None) == mxq.OK
+    assert L.newton_schulz(None, 0, 3, 0, 8, 1, co, 1e-7, None, None, 0, None) == mxq.OK
+    assert L.newton_schulz_workspace_bytes(0, 8, 8, 5) == 0
+    assert L.newton_schulz_workspace_bytes(2, 8, 8, 5) > 0
+
+
+def test_refusals_of_the_binding_and_fake_shape():
+    import mxfp8_quantization_moe_device_b200.ops  # noqa: F401
+    with pytest.raises(TypeError):
+        mxq.newton_schulz(torch.zeros(4, 4))
+    m = torch.empty(3, 20, 40, device="meta")
+    out = torch.ops.mxq.newton_schulz(m, 5, list(COEF), 1e-7)
+    assert out.shape == m.shape and out.dtype == torch.bfloat16
+
+
+# ------------------------------------------------------------ values
+SHAPES = [(1, 1, 1), (1, 1, 9), (2, 7, 1), (3, 16, 16), (2, 33, 65), (4, 96, 224), (2, 128, 128), (1, 129, 127),
+          (2, 256, 64), (3, 300, 260), (2, 257, 520), (1, 513, 511), (5, 64, 1000), (1, 1409, 577), (2, 768, 1280)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,N,K", SHAPES)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_newton_schulz(E, N, K, dtype):
+    g = matrices(E, N, K, dtype, E + N + K)
+    check(mxq.newton_schulz(g), g, [COEF] * 5)
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["noise", "decay"])
+@pytest.mark.parametrize("N,K", [(200, 500), (384, 256)])
+def test_spectra(kind, N, K):
+    g = matrices(2, N, K, torch.float32, 5, kind)
+    check(mxq.newton_schulz(g), g, [COEF] * 5)
+
+
+@pytest.mark.gpu
+def test_steps_coefficients_scale_and_shapes():
+    g = matrices(2, 130, 300, torch.float32, 9)
+    for steps in (1, 2, 7):
+        check(mxq.newton_schulz(g, steps=steps), g, [COEF] * steps)
+    co = [(4.0, -8.0, 5.0), (3.5, -5.0, 2.2), (1.875, -1.25, 0.375)]
+    check(mxq.newton_schulz(g, steps=3, coefficients=co), g, co)
+    # the norm is taken in 64 bits: scales whose squares leave fp32's range
+    for s in (1e-18, 1e-25, 1e25):
+        check(mxq.newton_schulz(g * s, eps=0.0), g * s, [COEF] * 5, eps=0.0)
+    two = matrices(1, 64, 96, torch.bfloat16, 2)
+    assert torch.equal(mxq.newton_schulz(two[0]), mxq.newton_schulz(two)[0])
+    out = torch.empty(1, 64, 96, dtype=torch.bfloat16, device=DEV)
+    assert mxq.newton_schulz(two, out=out) is out and torch.equal(out, mxq.newton_schulz(two))
+    assert mxq.newton_schulz(torch.empty(0, 4, 8, device=DEV)).shape == (0, 4, 8)
+    # an output that starts on a 2-byte boundary
+    buf = torch.empty(64 * 96 + 1, dtype=torch.bfloat16, device=DEV)
+    odd = buf[1:].view(1, 64, 96)
+    assert torch.equal(mxq.newton_schulz(two, out=odd), out)
+
+
+@pytest.mark.gpu
+def test_zeros_nan_and_neighbours():
+    g = matrices(5, 150, 270, torch.float32, 4)
+    want = mxq.newton_schulz(g)
+    g[1] = 0.0
+    g[2, 3, 4] = float("nan")
+    g[3, 149, 269] = float("inf")
+    got = mxq.newton_schulz(g)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[4], want[4])
+    assert bool((got[1] == 0).all()) and bool(got[2].isnan().all()) and bool(got[3].isnan().all())
+    assert bool((mxq.newton_schulz(g[1:2], eps=0.0) == 0).all())
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_gpu_refusals():
+    g = matrices(2, 64, 96, torch.float32, 4)
+    for call in (lambda: mxq.newton_schulz(g.half()), lambda: mxq.newton_schulz(g.mT), lambda: mxq.newton_schulz(g[0, 0]),
+                 lambda: mxq.newton_schulz(g, out=torch.empty_like(g))):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: mxq.newton_schulz(g, steps=0), lambda: mxq.newton_schulz(g, steps=65),
+                 lambda: mxq.newton_schulz(g, coefficients=[COEF] * 4), lambda: mxq.newton_schulz(g, coefficients=(1, 2))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: mxq.newton_schulz(g, coefficients=(20.0, 0.0, 0.0)), lambda: mxq.newton_schulz(g, eps=-1.0)):
+        with pytest.raises(mxq.MXQError):
+            call()
+    import mxfp8_quantization_moe_device_b200.ops  # noqa: F401
+    torch.library.opcheck(torch.ops.mxq.newton_schulz, (g, 5, list(COEF), 1e-7),
+                          test_utils=("test_schema", "test_faketensor"))
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_streams_graph_and_repeat():
+    g = matrices(3, 400, 700, torch.bfloat16, 8)
+    want = mxq.newton_schulz(g)
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(3):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            outs.append(mxq.newton_schulz(g))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    graphs = []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            graphs.append((gr, mxq.newton_schulz(g)))
+    g.copy_(matrices(3, 400, 700, torch.bfloat16, 18))
+    torch.cuda.synchronize()
+    for gr, _ in graphs:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            gr.replay()
+    torch.cuda.synchronize()
+    want = mxq.newton_schulz(g)
+    assert all(torch.equal(o, want) for _, o in graphs)
+    check(want, g, [COEF] * 5)
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_update_from_the_weight_gradient():
+    """The expert weight gradient of the FP8 grouped product, orthogonalised:
+    the singular values of the update lie where the polynomial takes those of
+    the normalised gradient."""
+    from mxfp8_quantization_moe_device_b200.autograd import fp8_grouped_mm
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(512, 256, generator=gen, device=DEV).bfloat16()
+    w = (torch.randn(3, 128, 256, generator=gen, device=DEV) * 0.05).bfloat16().requires_grad_(True)
+    offs = torch.tensor([160, 160, 512], dtype=torch.int32, device=DEV)
+    out = fp8_grouped_mm(x, w, offs)
+    (dw,) = torch.autograd.grad(out, w, torch.randn(512, 128, generator=gen, device=DEV).bfloat16())
+    up = mxq.newton_schulz(dw)
+    assert bool((up[1] == 0).all())  # the expert without tokens
+    check(up[[0, 2]], dw[[0, 2]], [COEF] * 5)

@@ -24,6 +24,15 @@
 // writes X^T too. A and A A are computed on and below the diagonal of tiles
 // and mirrored by the epilogue.
 //
+// Epilogue. A lane holds one row of the accumulator, so what it writes along
+// the row lands in 32 different lines per store and what it writes down a
+// column is one line for the warp. Everything that the epilogue reads or
+// writes directly is therefore laid out by columns: X^T (hi) and lo, and A and
+// B through their symmetry; the row-major copies that the products read go
+// through shared memory and a TMA store.
+// (Row-wise 16-byte accesses kept the load/store unit busy for 16 K cycles a
+// tile against 8 K of MMAs: 1393 us for B X at (16, 2048, 7168).)
+//
 // Kernel: the CTA-pair pipeline of gemm2.cuh (tcgen05.mma.cta_group::2, one
 // 256 x 256 tile per pair of SMs, six 32 KB stages of 64 fp16 columns, two
 // accumulators in TMEM); warps 0-7 epilogue (a warp takes 32 lanes and half
@@ -39,24 +48,27 @@
 namespace mxq {
 namespace ns {
 
-constexpr int HALF = 128;
-constexpr int TILE = 256;              // rows and columns of a pair's tile
+constexpr int HALF = 128;              // rows of one CTA
+constexpr int TILE = 2 * HALF;         // rows of a pair's tile; it has TN columns
 constexpr int BK = 64;                 // fp16 elements per 128-byte row
-constexpr int STAGES = 6;
-constexpr int OP_BYTES = HALF * 128;   // one operand, one stage, one CTA
+constexpr int OP_BYTES = HALF * 128;   // row operand, one stage, one CTA
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = (EPI_WARPS + 3) * 32;
 constexpr int ACC = 2;
-constexpr int TMEM_COLS = ACC * TILE;
+constexpr int CHUNK = 32;              // an epilogue step: 32 rows x 32 columns per warp
+constexpr int CHUNK_BYTES = CHUNK * CHUNK * 2;
 constexpr int MAX_PARTS = 64;          // partial sums of squares per matrix
 
 constexpr float SX = 256.0f;           // stored X  = X 2^8
 constexpr float SA = 1024.0f;          // stored A, B = A, B 2^10
 constexpr float SLO = 2048.0f;         // stored lo = (X 2^8 - hi) 2^11
 
-struct __align__(1024) Smem {
+template <int TN> struct __align__(1024) Smem {
+    static constexpr int STAGES = TN == 256 ? 6 : 8;
+    static constexpr int Q_BYTES = TN / 2 * 128; // column operand, one stage, one CTA
     uint8_t a[STAGES][OP_BYTES];
-    uint8_t b[STAGES][OP_BYTES];
+    uint8_t b[STAGES][Q_BYTES];
+    uint8_t stage[EPI_WARPS][2][CHUNK_BYTES]; // row-major chunks on their way out
     uint64_t full[STAGES];
     uint64_t ready[STAGES];
     uint64_t empty[STAGES];
@@ -66,30 +78,39 @@ struct __align__(1024) Smem {
     uint32_t tmem_base;
     int abort_flag;
 };
-constexpr size_t SMEM_BYTES = sizeof(Smem) + 1024;
+template <int TN> constexpr size_t smem_bytes() { return sizeof(Smem<TN>) + 1024; }
 
-// fp32 accumulator, f16 x f16, both K-major, N 256, M 256 (the pair)
-constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
+// fp32 accumulator, f16 x f16, both K-major, N = TN, M 256 (the pair)
+template <int TN> constexpr uint32_t idesc()
+{
+    return (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
+}
+
+// Programmatic launches: a kernel starts while the one before it finishes and
+// waits here for its results before it touches global memory.
+MXQ_DEV void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+MXQ_DEV void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 
 enum Mode { GRAM = 0, POLY = 1, STEP = 2, LAST = 3 };
 
 struct Args {
     int E, m, n;          // batch, X is (m, n)
-    int ldx, ldt;         // row lengths of X (n up to 8) and of X^T, A, B (m up to 8)
+    int ldt;              // row length of X^T, its state, A and B (m up to 8)
     float a, b, c;
-    __half *xh, *xl;      // (E, m, ldx)
-    __half *xt;           // (E, n, ldt): written by STEP
-    __half *A, *B;        // (E, m, ldt)
+    uint16_t *lo;         // (E, n, ldt): low words of X, by columns
+    const uint16_t *xt0;  // (E, n, ldt): high words of X by columns (X^T), read
+    uint16_t *xt;         // the new ones, written by STEP
+    uint16_t *A, *B;      // (E, m, ldt)
     uint16_t *out;        // LAST: bf16, (E, m, n) or, transposed, (E, n, m)
     int out_t, out_vec;
 };
 
-MXQ_DEV void mma_pair_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate)
+template <int TN> MXQ_DEV void mma_pair_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate)
 {
     asm volatile("{\n\t.reg .pred p;\n\t"
                  "setp.ne.b32 p, %3, 0;\n\t"
                  "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %4, p;\n\t}" ::"r"(d_tmem),
-                 "l"(adesc), "l"(bdesc), "r"(accumulate), "r"(IDESC)
+                 "l"(adesc), "l"(bdesc), "r"(accumulate), "r"(idesc<TN>())
                  : "memory");
 }
 
@@ -99,30 +120,98 @@ MXQ_DEV uint32_t pack_half2(float lo, float hi)
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+MXQ_DEV float half_value(uint16_t h) { return __half2float(__ushort_as_half(h)); }
 MXQ_DEV float2 unpack_half2(uint32_t w) { return __half22float2(*reinterpret_cast<__half2 *>(&w)); }
 
-MXQ_DEV float in_value(const uint16_t *p, int64_t i) { return __uint_as_float((uint32_t)p[i] << 16); }
-MXQ_DEV float in_value(const float *p, int64_t i) { return p[i]; }
-
-// sum of squares of a slice of matrix blockIdx.y, in 64 bits: squares of fp32
-// values leave fp32's range
-template <typename T>
-__global__ void __launch_bounds__(256) k_ns_sumsq(const T *__restrict__ g, int64_t size, double *__restrict__ part)
+// two neighbouring elements; `pair`: as one aligned word
+MXQ_DEV float2 in_pair(const uint16_t *p, bool pair, bool second)
 {
-    const T *p = g + (int64_t)blockIdx.y * size;
-    const int64_t per = (size + gridDim.x - 1) / gridDim.x;
-    const int64_t lo = blockIdx.x * per, hi = lo + per < size ? lo + per : size;
-    double s[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int64_t i = lo + threadIdx.x; i < hi; i += 4 * 256) {
-        float v[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            v[u] = i + u * 256 < hi ? in_value(p, i + u * 256) : 0.0f;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            s[u] = fma((double)v[u], (double)v[u], s[u]);
+    if (pair) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+        return make_float2(bf16_lo(w), bf16_hi(w));
     }
-    double t = (s[0] + s[1]) + (s[2] + s[3]);
+    return make_float2(__uint_as_float((uint32_t)p[0] << 16), second ? __uint_as_float((uint32_t)p[1] << 16) : 0.0f);
+}
+MXQ_DEV float2 in_pair(const float *p, bool pair, bool second)
+{
+    if (pair)
+        return *reinterpret_cast<const float2 *>(p);
+    return make_float2(p[0], second ? p[1] : 0.0f);
+}
+
+// the elements of one aligned 16-byte vector, eight (the last four zero for
+// fp32)
+MXQ_DEV void in_vec(const uint4 x, const uint16_t *, float (&v)[8])
+{
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+MXQ_DEV void in_vec(const uint4 x, const float *, float (&v)[8])
+{
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = __uint_as_float(w[i]);
+        v[4 + i] = 0.0f;
+    }
+}
+
+// Sum of squares of a slice of matrix blockIdx.y. Eight squares at a time are
+// added in fp32 and the sums in fp64; where the eight leave the range in which
+// fp32 squares are sound (values near 1e-18 or 1e19 and beyond) they are
+// squared in fp64. `vec`: every matrix is whole 16-byte vectors.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_ns_sumsq(const T *__restrict__ g, int64_t size, int vec, double *__restrict__ part)
+{
+    constexpr int V = 16 / sizeof(T);
+    let_next_kernel_start();
+    const T *p = g + (int64_t)blockIdx.y * size;
+    const int64_t per = ((size + gridDim.x - 1) / gridDim.x + 7) & ~int64_t(7);
+    const int64_t lo = blockIdx.x * per, hi = lo + per < size ? lo + per : size;
+    double t = 0.0;
+    auto add = [&](const float (&v)[8]) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            s = fmaf(v[i], v[i], s);
+        if (s > 0x1p-90f && s < 0x1p120f) {
+            t += (double)s;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                t = fma((double)v[i], (double)v[i], t);
+        }
+    };
+    if (vec) {
+        for (int64_t i = lo + V * threadIdx.x; i < hi; i += 4 * V * 256) {
+            uint4 x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                x[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (i + u * V * 256 < hi)
+                    x[u] = ld_stream_v4(p + i + u * V * 256);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float v[8];
+                in_vec(x[u], p, v);
+                add(v);
+            }
+        }
+    } else {
+        for (int64_t i = lo + threadIdx.x; i < hi; i += 8 * 256) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                v[u] = i + u * 256 < hi ? in_pair(p + i + u * 256, false, false).x : 0.0f;
+            add(v);
+        }
+    }
     __shared__ double w[8];
 #pragma unroll
     for (int o = 16; o; o >>= 1)
@@ -137,75 +226,119 @@ __global__ void __launch_bounds__(256) k_ns_sumsq(const T *__restrict__ g, int64
     }
 }
 
-// X0 from G (rows, cols), 64 x 64 tiles: hi and lo of X and hi of X^T. With
-// `tall` X is G^T, so the tile's transpose is X's and the tile itself X^T's.
+// X0 from G (rows, cols) in 64 x 64 tiles. X is G, or with `tall` G^T: the
+// tile as it is read goes to X (tall: to X^T and lo), its transpose to X^T and
+// lo (tall: to X). A thread moves pairs of neighbours.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    k_ns_init(const T *__restrict__ g, int rows, int cols, const double *__restrict__ part, int parts, double eps,
-              int tall, __half *__restrict__ xh, __half *__restrict__ xl, int ldx, __half *__restrict__ xt, int ldt)
+    k_ns_init(const T *__restrict__ g, int rows, int cols, int pair, const double *__restrict__ part, int parts,
+              double eps, int tall, uint16_t *__restrict__ xh, int ldx, uint16_t *__restrict__ xt,
+              uint16_t *__restrict__ xlo, int ldt)
 {
-    __shared__ __half sh[64][66], sl[64][66];
-    __shared__ double s_inv;
+    __shared__ uint32_t tile[64][65];
+    __shared__ float s_f[2];
     const int e = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-    if (threadIdx.x == 0) {
+    let_next_kernel_start();
+    wait_for_previous_kernel();
+    if (threadIdx.x < 32) {
         double s = 0.0;
-        for (int i = 0; i < parts; ++i)
+        for (int i = threadIdx.x; i < parts; i += 32)
             s += part[(size_t)e * parts + i];
-        const double norm = sqrt(s) + eps;
-        s_inv = norm > 0.0 ? (double)SX / norm : (norm == 0.0 ? 0.0 : norm);
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (threadIdx.x == 0) {
+            // 2^8 / (norm + eps) as two fp32 factors: either alone may leave
+            // fp32's range, g times the first does not where it matters
+            const double norm = sqrt(s) + eps;
+            const double inv = norm > 0.0 ? (double)SX / norm : (norm == 0.0 ? 0.0 : norm);
+            int ex = 0;
+            const double fr = frexp(inv, &ex);
+            const bool plain = inv == 0.0 || !(norm > 0.0) || isinf(norm);
+            s_f[0] = plain ? 1.0f : (float)ldexp(1.0, ex / 2);
+            s_f[1] = plain ? (float)inv : (float)ldexp(fr, ex - ex / 2);
+        }
     }
     __syncthreads();
-    const double inv = s_inv;
+    const float f0 = s_f[0], f1 = s_f[1];
     const T *p = g + (int64_t)e * rows * cols;
     const int64_t base_x = (int64_t)e * (tall ? cols : rows) * ldx;
     const int64_t base_t = (int64_t)e * (tall ? rows : cols) * ldt;
-    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-#pragma unroll 4
-    for (int r = ty; r < 64; r += 4) {
-        const int R = r0 + r, C = c0 + tx;
-        if (R < rows && C < cols) {
-            const float x = (float)((double)in_value(p, (int64_t)R * cols + C) * inv);
-            const __half h = __float2half_rn(x);
-            const __half l = __float2half_rn((x - __half2float(h)) * SLO);
-            sh[r][tx] = h;
-            sl[r][tx] = l;
+    const int tx = 2 * (threadIdx.x & 31), ty = threadIdx.x >> 5;
+    float2 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int R = r0 + ty + 8 * i, C = c0 + tx;
+        v[i] = R < rows && C < cols ? in_pair(p + (int64_t)R * cols + C, pair != 0, C + 1 < cols)
+                                    : make_float2(0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = ty + 8 * i, R = r0 + r, C = c0 + tx;
+        const float x = (v[i].x * f0) * f1, y = (v[i].y * f0) * f1;
+        const uint32_t h = pack_half2(x, y);
+        const float2 f = unpack_half2(h);
+        const uint32_t l = pack_half2((x - f.x) * SLO, (y - f.y) * SLO);
+        const uint32_t w0 = __byte_perm(h, l, 0x5410), w1 = __byte_perm(h, l, 0x7632);
+        tile[r][tx] = w0;
+        tile[r][tx + 1] = w1;
+        if (R < rows && C < cols) { // rows of the targets are padded to pairs
             if (tall) {
-                xt[base_t + (int64_t)R * ldt + C] = h;
+                *reinterpret_cast<uint32_t *>(xt + base_t + (int64_t)R * ldt + C) = h;
+                *reinterpret_cast<uint32_t *>(xlo + base_t + (int64_t)R * ldt + C) = l;
             } else {
-                xh[base_x + (int64_t)R * ldx + C] = h;
-                xl[base_x + (int64_t)R * ldx + C] = l;
+                *reinterpret_cast<uint32_t *>(xh + base_x + (int64_t)R * ldx + C) = h;
             }
         }
     }
     __syncthreads();
-#pragma unroll 4
-    for (int c = ty; c < 64; c += 4) {
-        const int C = c0 + c, R = r0 + tx;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int c = ty + 8 * i, C = c0 + c, R = r0 + tx;
         if (R < rows && C < cols) {
+            const uint32_t w0 = tile[tx][c], w1 = tile[tx + 1][c];
+            const uint32_t h = __byte_perm(w0, w1, 0x5410);
             if (tall) {
-                xh[base_x + (int64_t)C * ldx + R] = sh[tx][c];
-                xl[base_x + (int64_t)C * ldx + R] = sl[tx][c];
+                *reinterpret_cast<uint32_t *>(xh + base_x + (int64_t)C * ldx + R) = h;
             } else {
-                xt[base_t + (int64_t)C * ldt + R] = sh[tx][c];
+                *reinterpret_cast<uint32_t *>(xt + base_t + (int64_t)C * ldt + R) = h;
+                *reinterpret_cast<uint32_t *>(xlo + base_t + (int64_t)C * ldt + R) = __byte_perm(w0, w1, 0x7632);
             }
         }
     }
 }
 
+// tiles of one matrix: row tile i of a symmetric product needs the columns up
+// to its last row, of the others all
+template <bool SYM, int TN> __host__ __device__ inline int64_t sym_or_all_tiles(int m, int n)
+{
+    const int64_t tm = (m + TILE - 1) / TILE, tn = ((SYM ? m : n) + TN - 1) / TN;
+    if (!SYM)
+        return tm * tn;
+    // all but the last row tile end within the matrix
+    return (TILE / TN) * (tm * (tm - 1) / 2) + tn;
+}
+
 // D = P Q^T over K = 64 nkb columns for every matrix, with the epilogue of
-// MODE. Grid: an even number of CTAs in clusters of two.
-template <int MODE>
+// MODE. tm_o: the row-major copy of the result (X, A or B) in boxes of 32 x 32
+// with the 64-byte swizzle, unused by LAST. Grid: an even number of CTAs in
+// clusters of two.
+template <int MODE, int TN>
 __global__ void __launch_bounds__(THREADS, 1)
-    k_ns_gemm(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q, const Args q,
-              int nkb, uint64_t wait_ns)
+    k_ns_gemm(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
+              const __grid_constant__ CUtensorMap tm_o, const Args q, int nkb, uint64_t wait_ns)
 {
     constexpr bool SYM = MODE == GRAM || MODE == POLY;
+    constexpr int STAGES = Smem<TN>::STAGES;
+    constexpr int TMEM_COLS = ACC * TN;
+    constexpr int RATIO = TILE / TN; // column tiles per row tile
     extern __shared__ uint8_t smem_raw[];
-    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Smem<TN> &sm = *reinterpret_cast<Smem<TN> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = g2::cta_rank();
     const bool leader = rank == 0;
 
+    let_next_kernel_start();
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&sm.full[s], 1);
@@ -230,14 +363,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     g2::cluster_sync(); // barriers initialised and TMEM allocated in both CTAs
     gm::tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
+    wait_for_previous_kernel();
 
     const int64_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int tm = (q.m + TILE - 1) / TILE, tn = (q.n + TILE - 1) / TILE;
-    const int64_t per = SYM ? (int64_t)tm * (tm + 1) / 2 : (int64_t)tm * tn;
+    const int tm = (q.m + TILE - 1) / TILE, tn = ((SYM ? q.m : q.n) + TN - 1) / TN;
+    const int64_t per = sym_or_all_tiles<SYM, TN>(q.m, q.n);
     const int64_t total = per * q.E;
     // tile t of a matrix: row tile i, column tile j; symmetric products take
-    // j <= i, the others run down the row tiles first, so that the pairs at
-    // work share a column tile of X^T and all of B
+    // the column tiles up to the diagonal's, the others run down the row tiles
+    // first, so that the pairs at work share a column tile of X^T and all of B
     struct Item {
         int e, i, j;
     };
@@ -247,8 +381,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         int t = (int)(it - (int64_t)w.e * per);
         if (SYM) {
             w.i = 0;
-            while (t > w.i)
-                t -= ++w.i;
+            for (int c = min(RATIO, tn); t >= c; c = min(RATIO * (w.i + 1), tn)) {
+                t -= c;
+                ++w.i;
+            }
             w.j = t;
         } else {
             w.j = t / tm;
@@ -269,9 +405,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
                         break;
                     }
-                    mbar_arrive_expect_tx(&sm.full[s], 2 * OP_BYTES);
+                    mbar_arrive_expect_tx(&sm.full[s], OP_BYTES + Smem<TN>::Q_BYTES);
                     tma_load_3d(sm.a[s], &tm_p, &sm.full[s], kb * BK, w.i * TILE + (int)rank * HALF, w.e);
-                    tma_load_3d(sm.b[s], &tm_q, &sm.full[s], kb * BK, w.j * TILE + (int)rank * HALF, w.e);
+                    tma_load_3d(sm.b[s], &tm_q, &sm.full[s], kb * BK, w.j * TN + (int)rank * (TN / 2), w.e);
                 }
             }
             // drain: every issued fill has landed before the CTA leaves
@@ -313,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     break;
                 }
                 gm::tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(acc * TILE);
+                const uint32_t d = tmem + (uint32_t)(acc * TN);
                 // the next slot is waited on before this slot's last MMA, so
                 // that the wait overlaps MMAs already in the pipe
                 bool ok = mbar_wait(&sm.ready[s], ph, wait_ns);
@@ -323,12 +459,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const uint64_t bd = gm::smem_desc_k128(smem_u32(sm.b[s]));
 #pragma unroll
                     for (int k = 0; k < 3; ++k) // 16 columns per MMA: 32 bytes
-                        mma_pair_f16(d, ad + 2 * k, bd + 2 * k, (kb > 0 || k > 0) ? 1u : 0u);
+                        mma_pair_f16<TN>(d, ad + 2 * k, bd + 2 * k, (kb > 0 || k > 0) ? 1u : 0u);
                     const int s_next = s + 1 == STAGES ? 0 : s + 1;
                     const uint32_t ph_next = s + 1 == STAGES ? ph ^ 1u : ph;
                     if (kb + 1 < nkb)
                         ok = mbar_wait(&sm.ready[s_next], ph_next, wait_ns);
-                    mma_pair_f16(d, ad + 6, bd + 6, 1u);
+                    mma_pair_f16<TN>(d, ad + 6, bd + 6, 1u);
                     g2::commit_pair(&sm.empty[s], 0x3);
                     issued = true;
                     s = s_next;
@@ -350,10 +486,32 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ------------------------------------------------ epilogue (both CTAs)
         const uint32_t leader_acc_empty0 = g2::peer_addr(&sm.acc_empty[0], 0);
         const int quad = warp & 3, part = warp >> 2;
-        int t = 0;
+        int t = 0, buf = 0;
         for (int64_t it = pair; it < total; it += npairs, ++t) {
             const Item w = item(it);
             const int acc = t & 1;
+            const int r0 = w.i * TILE + (int)rank * HALF + 32 * quad; // the warp's rows, one per lane
+            const int r = r0 + lane;
+            const bool row_ok = r < q.m;
+            const int cols = SYM ? q.m : q.n;
+            // this lane's column-wise position: element c of the row is at
+            // at + c * ldt in X^T, lo, A and B alike
+            const int64_t at = (int64_t)w.e * cols * q.ldt + r;
+            // what the chunk adds to the product: X (hi and lo), or A
+            uint16_t old_h[CHUNK], old_l[MODE == POLY ? 1 : CHUNK];
+            auto load_old = [&](int c0) {
+                const int64_t o = at + (int64_t)c0 * q.ldt;
+                const uint16_t *ph = (MODE == POLY ? q.A : q.xt0) + o, *pl = q.lo + o;
+#pragma unroll
+                for (int k = 0; k < CHUNK; ++k, ph += q.ldt, pl += q.ldt) {
+                    const bool in = row_ok && c0 + k < cols;
+                    old_h[k] = in ? *ph : (uint16_t)0;
+                    if constexpr (MODE != POLY)
+                        old_l[k] = in ? *pl : (uint16_t)0;
+                }
+            };
+            if constexpr (MODE == STEP || MODE == LAST)
+                load_old(w.j * TN + CHUNK * part); // in flight while the product finishes
             bool ok = mbar_wait(&sm.acc_full[acc], (uint32_t)(t / ACC) & 1u, wait_ns);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || gm::aborted(&sm.abort_flag)) {
@@ -361,106 +519,103 @@ __global__ void __launch_bounds__(THREADS, 1)
                 break;
             }
             gm::tc_fence_after();
-            const int r = w.i * TILE + (int)rank * HALF + 32 * quad + lane; // this thread's row
-            const bool row_ok = r < q.m;
-            const int64_t row_t = ((int64_t)w.e * q.m + r) * q.ldt, row_x = ((int64_t)w.e * q.m + r) * q.ldx;
-            const int cols = SYM ? q.m : q.n, ld = SYM ? q.ldt : q.ldx;
 #pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
-                const int c0 = w.j * TILE + part * HALF + 32 * ch;
+            for (int ch = part; ch < TN / CHUNK; ch += 2) {
+                const int c0 = w.j * TN + CHUNK * ch;
                 if (c0 >= cols)
                     break; // the same in every lane
-                uint32_t d[32];
-                gm::tc_ld32(tmem + (uint32_t)(acc * TILE + part * HALF + 32 * ch) + ((uint32_t)(32 * quad) << 16), d);
-                uint32_t h[16]; // the chunk's result, two fp16 per word
+                if constexpr (MODE == POLY) // held only within the chunk: no registers for the next one's
+                    load_old(c0);
+                uint32_t d[CHUNK];
+                gm::tc_ld32(tmem + (uint32_t)(acc * TN + CHUNK * ch) + ((uint32_t)(32 * quad) << 16), d);
+                uint32_t h[CHUNK / 2], l[CHUNK / 2]; // pairs of the row, high and low words
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int c = c0 + 8 * g;
-                    const bool in = row_ok && c < ld;
-                    float v[8];
+                for (int k = 0; k < CHUNK / 2; ++k) {
+                    const float d0 = __uint_as_float(d[2 * k]), d1 = __uint_as_float(d[2 * k + 1]);
+                    float v0, v1;
                     if constexpr (MODE == GRAM) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            v[k] = __uint_as_float(d[8 * g + k]) * (SA / (SX * SX));
-                    } else if constexpr (MODE == POLY) {
-                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                        if (in)
-                            x = *reinterpret_cast<const uint4 *>(q.A + row_t + c);
-                        const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 f = unpack_half2(xw[k]);
-                            v[2 * k] = fmaf(q.c * (1.0f / SA), __uint_as_float(d[8 * g + 2 * k]), q.b * f.x);
-                            v[2 * k + 1] = fmaf(q.c * (1.0f / SA), __uint_as_float(d[8 * g + 2 * k + 1]), q.b * f.y);
-                        }
+                        v0 = d0 * (SA / (SX * SX));
+                        v1 = d1 * (SA / (SX * SX));
                     } else {
-                        uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-                        if (in) {
-                            x = *reinterpret_cast<const uint4 *>(q.xh + row_x + c);
-                            y = *reinterpret_cast<const uint4 *>(q.xl + row_x + c);
-                        }
-                        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 f = unpack_half2(xw[k]), l = unpack_half2(yw[k]);
-                            v[2 * k] = fmaf(q.a, fmaf(l.x, 1.0f / SLO, f.x),
-                                            __uint_as_float(d[8 * g + 2 * k]) * (1.0f / SA));
-                            v[2 * k + 1] = fmaf(q.a, fmaf(l.y, 1.0f / SLO, f.y),
-                                                __uint_as_float(d[8 * g + 2 * k + 1]) * (1.0f / SA));
+                        const float h0 = half_value(old_h[2 * k]), h1 = half_value(old_h[2 * k + 1]);
+                        if constexpr (MODE == POLY) {
+                            v0 = fmaf(q.c * (1.0f / SA), d0, q.b * h0);
+                            v1 = fmaf(q.c * (1.0f / SA), d1, q.b * h1);
+                        } else {
+                            v0 = fmaf(q.a, fmaf(half_value(old_l[2 * k]), 1.0f / SLO, h0), d0 * (1.0f / SA));
+                            v1 = fmaf(q.a, fmaf(half_value(old_l[2 * k + 1]), 1.0f / SLO, h1), d1 * (1.0f / SA));
                         }
                     }
                     if constexpr (MODE == LAST) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            h[4 * g + k] = gm::pack_bf16x2(v[2 * k] * (1.0f / SX), v[2 * k + 1] * (1.0f / SX));
+                        h[k] = gm::pack_bf16x2(v0 * (1.0f / SX), v1 * (1.0f / SX));
                     } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            h[4 * g + k] = pack_half2(v[2 * k], v[2 * k + 1]);
-                        if (in) {
-                            __half *dst = MODE == GRAM ? q.A + row_t + c : MODE == POLY ? q.B + row_t + c : q.xh + row_x + c;
-                            st_v4(dst, h[4 * g], h[4 * g + 1], h[4 * g + 2], h[4 * g + 3]);
-                            if constexpr (MODE == STEP) {
-                                uint32_t lo[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const float2 f = unpack_half2(h[4 * g + k]);
-                                    lo[k] = pack_half2((v[2 * k] - f.x) * SLO, (v[2 * k + 1] - f.y) * SLO);
-                                }
-                                st_v4(q.xl + row_x + c, lo[0], lo[1], lo[2], lo[3]);
-                            }
+                        h[k] = pack_half2(v0, v1);
+                        if constexpr (MODE == STEP) {
+                            const float2 f = unpack_half2(h[k]);
+                            l[k] = pack_half2((v0 - f.x) * SLO, (v1 - f.y) * SLO);
                         }
                     }
                 }
-                // the transpose: one column per store, neighbouring lanes
-                // hold neighbouring rows
-                if constexpr (MODE == LAST) {
-                    if (q.out_t) {
-                        uint16_t *dst = q.out + ((int64_t)w.e * q.n + c0) * q.m + r;
+                if constexpr (MODE == STEP || MODE == LAST) {
+                    if (ch + 2 < TN / CHUNK && c0 + 2 * CHUNK < cols)
+                        load_old(c0 + 2 * CHUNK);
+                }
+                // down the columns
+                if (MODE != LAST || q.out_t) {
+                    const int64_t ld = MODE == LAST ? q.m : q.ldt;
+                    const int64_t o = (MODE == LAST ? (int64_t)w.e * cols * q.m + r : at) + c0 * ld;
+                    uint16_t *dst = (MODE == GRAM ? q.A : MODE == POLY ? q.B : MODE == STEP ? q.xt : q.out) + o;
+                    uint16_t *dst_l = q.lo + o;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (row_ok && c0 + k < cols)
-                                dst[(int64_t)k * q.m] = (uint16_t)(k & 1 ? h[k >> 1] >> 16 : h[k >> 1]);
-                    } else if (row_ok) {
-                        uint16_t *dst = q.out + ((int64_t)w.e * q.m + r) * q.n + c0;
-                        if (q.out_vec && c0 + 32 <= cols) {
-#pragma unroll
-                            for (int g = 0; g < 4; ++g)
-                                st_v4(dst + 8 * g, h[4 * g], h[4 * g + 1], h[4 * g + 2], h[4 * g + 3]);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (c0 + k < cols)
-                                    dst[k] = (uint16_t)(k & 1 ? h[k >> 1] >> 16 : h[k >> 1]);
+                    for (int k = 0; k < CHUNK; ++k, dst += ld, dst_l += ld)
+                        if (row_ok && c0 + k < cols) {
+                            *dst = (uint16_t)(k & 1 ? h[k >> 1] >> 16 : h[k >> 1]);
+                            if constexpr (MODE == STEP)
+                                *dst_l = (uint16_t)(k & 1 ? l[k >> 1] >> 16 : l[k >> 1]);
                         }
+                }
+                // along the rows, through shared memory
+                const bool rows_too = MODE == LAST ? !q.out_t : !(SYM && w.j >= w.i * RATIO);
+                if (rows_too) {
+                    uint8_t *st = sm.stage[warp][buf];
+                    if constexpr (MODE != LAST) {
+                        if (lane == 0)
+                            bulk_wait_read<1>(); // the store before the last has read this buffer
+                        __syncwarp();
                     }
-                } else if (!SYM || w.i != w.j) {
-                    uint16_t *dst = reinterpret_cast<uint16_t *>(MODE == GRAM ? q.A : MODE == POLY ? q.B : q.xt) +
-                                    ((int64_t)w.e * cols + c0) * q.ldt + r;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (row_ok && c0 + k < cols)
-                            dst[(int64_t)k * q.ldt] = (uint16_t)(k & 1 ? h[k >> 1] >> 16 : h[k >> 1]);
+                    for (int g = 0; g < 4; ++g)
+                        sts_v4(smem_u32(st) + (uint32_t)(lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)),
+                               make_uint4(h[4 * g], h[4 * g + 1], h[4 * g + 2], h[4 * g + 3]));
+                    if constexpr (MODE != LAST) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && r0 < q.m) {
+                            tma_store_3d(&tm_o, st, c0, r0, w.e);
+                            bulk_commit();
+                        }
+                    } else {
+                        __syncwarp();
+                        uint16_t *dst = q.out + ((int64_t)w.e * q.m + r0) * q.n + c0;
+                        if (q.out_vec && c0 + CHUNK <= cols) { // eight rows at a time, four lanes each
+                            const int g = lane & 3;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int y = 8 * i + (lane >> 2);
+                                const uint4 x = *reinterpret_cast<const uint4 *>(st + y * 64 + ((g ^ ((y >> 1) & 3)) << 4));
+                                if (r0 + y < q.m)
+                                    st_v4(dst + (int64_t)y * q.n + 8 * g, x.x, x.y, x.z, x.w);
+                            }
+                        } else if (c0 + lane < cols) { // a row at a time, one element per lane
+#pragma unroll 8
+                            for (int y = 0; y < 32; ++y)
+                                if (r0 + y < q.m)
+                                    dst[(int64_t)y * q.n + lane] = *reinterpret_cast<const uint16_t *>(
+                                        st + y * 64 + (((lane >> 3) ^ ((y >> 1) & 3)) << 4) + (lane & 7) * 2);
+                        }
+                        __syncwarp();
+                    }
+                    buf ^= 1;
                 }
             }
             gm::tc_fence_before();
@@ -472,6 +627,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     g2::arrive_remote(leader_acc_empty0 + (uint32_t)(acc * sizeof(uint64_t)));
             }
         }
+        if (MODE != LAST && lane == 0)
+            bulk_wait<0>(); // the stores have left shared memory and are complete
     }
 
     __syncwarp(); // the cluster barrier below is warp-aligned

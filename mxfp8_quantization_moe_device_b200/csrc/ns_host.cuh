@@ -7,7 +7,7 @@ namespace {
 struct NsPlan {
     int64_t m, n, ldx, ldt;
     int tall, parts;
-    size_t xh, xl, xt[2], A, B, part, bytes;
+    size_t xh, lo, xt[2], A, B, part, bytes;
 };
 
 NsPlan ns_plan(int64_t E, int64_t rows, int64_t cols, int32_t steps)
@@ -18,7 +18,7 @@ NsPlan ns_plan(int64_t E, int64_t rows, int64_t cols, int32_t steps)
     p.n = std::max(rows, cols);
     p.ldx = (p.n + 7) / 8 * 8;
     p.ldt = (p.m + 7) / 8 * 8;
-    p.parts = (int)std::min<int64_t>(ns::MAX_PARTS, (rows * cols + 32767) / 32768);
+    p.parts = (int)std::min<int64_t>(ns::MAX_PARTS, (rows * cols + 4095) / 4096);
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;
@@ -26,7 +26,7 @@ NsPlan ns_plan(int64_t E, int64_t rows, int64_t cols, int32_t steps)
         return at;
     };
     p.xh = take((size_t)E * p.m * p.ldx * 2);
-    p.xl = take((size_t)E * p.m * p.ldx * 2);
+    p.lo = take((size_t)E * p.n * p.ldt * 2);
     p.xt[0] = take((size_t)E * p.n * p.ldt * 2);
     p.xt[1] = steps > 1 ? take((size_t)E * p.n * p.ldt * 2) : p.xt[0];
     p.A = take((size_t)E * p.m * p.ldt * 2);
@@ -45,37 +45,107 @@ int ns_check(int64_t E, int64_t rows, int64_t cols, int32_t steps)
     return MXQ_OK;
 }
 
-// map of one fp16 matrix per plane: boxes of 64 elements x 128 rows
-int ns_map(CUtensorMap *map, const void *p, int64_t inner, int64_t ld, int64_t rows, int64_t E)
+// map of one fp16 matrix per plane: boxes of 64 elements x `box_rows` rows for
+// the operands (128-byte swizzle), of 32 x 32 for the epilogue's stores
+int ns_map(CUtensorMap *map, const void *p, int64_t inner, int64_t ld, int64_t rows, int64_t E, int box_rows)
 {
+    const bool store = box_rows == ns::CHUNK;
     const uint64_t d[3] = {(uint64_t)inner, (uint64_t)rows, (uint64_t)E};
     const uint64_t s[2] = {(uint64_t)ld * 2, (uint64_t)ld * 2 * (uint64_t)rows};
-    const uint32_t box[3] = {ns::BK, ns::HALF, 1};
-    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, d, s, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    const uint32_t box[3] = {(uint32_t)(store ? ns::CHUNK : ns::BK), (uint32_t)box_rows, 1};
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, d, s, box,
+                    store ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int MODE>
-int ns_product(const CUtensorMap &p, const CUtensorMap &q, const ns::Args &a, int64_t K, cudaStream_t stream)
+// a launch that may begin while the kernel before it in the stream finishes
+// (the kernel waits for it before it touches global memory); pairs: clusters
+// of two CTAs
+template <typename... K, typename... A>
+int launch_chained(void (*kernel)(K...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool pairs,
+                   A &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pairs ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return MXQ_ERR_LAUNCH;
+    }
+    return MXQ_OK;
+}
+
+// the operands of one product: a matrix by rows, inner length and row length
+struct NsOperand {
+    const void *p;
+    int64_t inner, ld, rows;
+};
+
+// co-resident CTA pairs on the current device; the four products differ in
+// the epilogue's code alone
+template <int MODE, int TN> int ns_pairs(int *out)
 {
     static std::atomic<uint64_t> set[2];
-    const int rc = allow_smem(ns::k_ns_gemm<MODE>, (int)ns::SMEM_BYTES, set);
+    static std::atomic<int> pairs[128];
+    const int rc = allow_smem(ns::k_ns_gemm<MODE, TN>, (int)ns::smem_bytes<TN>(), set);
     if (rc != MXQ_OK)
         return rc;
-    static std::atomic<int> pairs[128]; // per device: co-resident CTA pairs
     int d = 0;
     if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= 128)
         return MXQ_ERR_CUDA;
     int np = pairs[d].load(std::memory_order_relaxed);
     if (np == 0) {
-        if (max_pairs(ns::k_ns_gemm<MODE>, dim3(ns::THREADS), ns::SMEM_BYTES, &np) != MXQ_OK || np < 1)
+        if (max_pairs(ns::k_ns_gemm<MODE, TN>, dim3(ns::THREADS), ns::smem_bytes<TN>(), &np) != MXQ_OK || np < 1)
             return MXQ_ERR_CUDA;
         pairs[d].store(np, std::memory_order_relaxed);
     }
-    const int64_t tm = (a.m + ns::TILE - 1) / ns::TILE, tn = (a.n + ns::TILE - 1) / ns::TILE;
-    const int64_t items = a.E * (MODE == ns::GRAM || MODE == ns::POLY ? tm * (tm + 1) / 2 : tm * tn);
-    const int64_t grid = std::min<int64_t>(items, np);
-    return launch_pairs(ns::k_ns_gemm<MODE>, dim3((unsigned)(2 * grid)), dim3(ns::THREADS), ns::SMEM_BYTES, stream, p, q,
-                        a, (int)((K + ns::BK - 1) / ns::BK), wait_ns());
+    *out = np;
+    return MXQ_OK;
+}
+
+template <int MODE, int TN>
+int ns_launch(const NsOperand &p, const NsOperand &q, const NsOperand &o, const ns::Args &a, int pairs,
+              cudaStream_t stream)
+{
+    CUtensorMap mp, mq, mo;
+    int rc;
+    if ((rc = ns_map(&mp, p.p, p.inner, p.ld, p.rows, a.E, ns::HALF)) != MXQ_OK ||
+        (rc = ns_map(&mq, q.p, q.inner, q.ld, q.rows, a.E, TN / 2)) != MXQ_OK ||
+        (rc = ns_map(&mo, o.p, o.inner, o.ld, o.rows, a.E, ns::CHUNK)) != MXQ_OK)
+        return rc;
+    constexpr bool sym = MODE == ns::GRAM || MODE == ns::POLY;
+    const int64_t grid = std::min<int64_t>(a.E * ns::sym_or_all_tiles<sym, TN>(a.m, a.n), pairs);
+    return launch_chained(ns::k_ns_gemm<MODE, TN>, dim3((unsigned)(2 * grid)), dim3(ns::THREADS), ns::smem_bytes<TN>(),
+                          stream, true, mp, mq, mo, a, (int)((p.inner + ns::BK - 1) / ns::BK), wait_ns());
+}
+
+// Tile width: a 256 x 128 tile takes 0.72 of a 256 x 256 tile's time (12.1 ms
+// against 8.4 for twice as many at (16, 2048, 7168)), so it is used where it
+// needs fewer than 1 / 0.72 as many rounds over the pairs: 269 us against 315
+// at (5, 1409, 577).
+template <int MODE>
+int ns_product(const NsOperand &p, const NsOperand &q, const NsOperand &o, const ns::Args &a, cudaStream_t stream)
+{
+    constexpr bool sym = MODE == ns::GRAM || MODE == ns::POLY;
+    int wide = 0, narrow = 0, rc;
+    if ((rc = ns_pairs<MODE, 256>(&wide)) != MXQ_OK || (rc = ns_pairs<MODE, 128>(&narrow)) != MXQ_OK)
+        return rc;
+    const int64_t rounds_w = (a.E * ns::sym_or_all_tiles<sym, 256>(a.m, a.n) + wide - 1) / wide;
+    const int64_t rounds_n = (a.E * ns::sym_or_all_tiles<sym, 128>(a.m, a.n) + narrow - 1) / narrow;
+    const int force = g_ns_tile.load();
+    if (force == 128 || (force == 0 && 18 * rounds_n < 25 * rounds_w))
+        return ns_launch<MODE, 128>(p, q, o, a, narrow, stream);
+    return ns_launch<MODE, 256>(p, q, o, a, wide, stream);
 }
 
 template <typename T>
@@ -84,13 +154,14 @@ int ns_start(const T *g, int64_t E, int64_t rows, int64_t cols, const NsPlan &p,
 {
     double *part = reinterpret_cast<double *>(ws + p.part);
     const int rc = launch(ns::k_ns_sumsq<T>, dim3((unsigned)p.parts, (unsigned)E), dim3(256), 0, stream, false, g,
-                          rows * cols, part);
+                          rows * cols, (int)(aligned(g, 16) && rows * cols * sizeof(T) % 16 == 0), part);
     if (rc != MXQ_OK)
         return rc;
-    return launch(ns::k_ns_init<T>, dim3((unsigned)((cols + 63) / 64), (unsigned)((rows + 63) / 64), (unsigned)E),
-                  dim3(256), 0, stream, false, g, (int)rows, (int)cols, (const double *)part, p.parts, eps, p.tall,
-                  reinterpret_cast<__half *>(ws + p.xh), reinterpret_cast<__half *>(ws + p.xl), (int)p.ldx,
-                  reinterpret_cast<__half *>(ws + p.xt[0]), (int)p.ldt);
+    return launch_chained(ns::k_ns_init<T>,
+                          dim3((unsigned)((cols + 63) / 64), (unsigned)((rows + 63) / 64), (unsigned)E), dim3(256), 0,
+                          stream, false, g, (int)rows, (int)cols, (int)(aligned(g, 2 * sizeof(T)) && cols % 2 == 0),
+                  (const double *)part, p.parts, eps, p.tall, reinterpret_cast<uint16_t *>(ws + p.xh), (int)p.ldx,
+                  reinterpret_cast<uint16_t *>(ws + p.xt[0]), reinterpret_cast<uint16_t *>(ws + p.lo), (int)p.ldt);
 }
 
 } // namespace
@@ -133,13 +204,8 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
     if (!aligned(workspace, 256))
         return MXQ_ERR_ALIGN;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    CUtensorMap mx, mt[2], ma, mb;
-    if ((rc = ns_map(&mx, ws + p.xh, p.n, p.ldx, p.m, batch)) != MXQ_OK ||
-        (rc = ns_map(&mt[0], ws + p.xt[0], p.m, p.ldt, p.n, batch)) != MXQ_OK ||
-        (rc = ns_map(&mt[1], ws + p.xt[1], p.m, p.ldt, p.n, batch)) != MXQ_OK ||
-        (rc = ns_map(&ma, ws + p.A, p.m, p.ldt, p.m, batch)) != MXQ_OK ||
-        (rc = ns_map(&mb, ws + p.B, p.m, p.ldt, p.m, batch)) != MXQ_OK)
-        return rc;
+    const NsOperand x = {ws + p.xh, p.n, p.ldx, p.m}, A = {ws + p.A, p.m, p.ldt, p.m}, B = {ws + p.B, p.m, p.ldt, p.m};
+    const NsOperand xt[2] = {{ws + p.xt[0], p.m, p.ldt, p.n}, {ws + p.xt[1], p.m, p.ldt, p.n}};
     rc = dtype == MXQ_BF16 ? ns_start(static_cast<const uint16_t *>(g), batch, rows, cols, p, eps, ws, stream)
                            : ns_start(static_cast<const float *>(g), batch, rows, cols, p, eps, ws, stream);
     if (rc != MXQ_OK)
@@ -148,12 +214,10 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
     a.E = (int)batch;
     a.m = (int)p.m;
     a.n = (int)p.n;
-    a.ldx = (int)p.ldx;
     a.ldt = (int)p.ldt;
-    a.xh = reinterpret_cast<__half *>(ws + p.xh);
-    a.xl = reinterpret_cast<__half *>(ws + p.xl);
-    a.A = reinterpret_cast<__half *>(ws + p.A);
-    a.B = reinterpret_cast<__half *>(ws + p.B);
+    a.lo = reinterpret_cast<uint16_t *>(ws + p.lo);
+    a.A = reinterpret_cast<uint16_t *>(ws + p.A);
+    a.B = reinterpret_cast<uint16_t *>(ws + p.B);
     a.out = static_cast<uint16_t *>(out);
     a.out_t = p.tall;
     a.out_vec = cols % 8 == 0 && aligned(out, 16);
@@ -161,11 +225,12 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
         a.a = coefficients[3 * s];
         a.b = coefficients[3 * s + 1];
         a.c = coefficients[3 * s + 2];
-        a.xt = reinterpret_cast<__half *>(ws + p.xt[(s + 1) & 1]);
-        if ((rc = ns_product<ns::GRAM>(mx, mx, a, p.n, stream)) != MXQ_OK ||
-            (rc = ns_product<ns::POLY>(ma, ma, a, p.m, stream)) != MXQ_OK ||
-            (rc = s + 1 < steps ? ns_product<ns::STEP>(mb, mt[s & 1], a, p.m, stream)
-                                : ns_product<ns::LAST>(mb, mt[s & 1], a, p.m, stream)) != MXQ_OK)
+        a.xt0 = reinterpret_cast<const uint16_t *>(ws + p.xt[s & 1]);
+        a.xt = reinterpret_cast<uint16_t *>(ws + p.xt[(s + 1) & 1]);
+        if ((rc = ns_product<ns::GRAM>(x, x, A, a, stream)) != MXQ_OK ||
+            (rc = ns_product<ns::POLY>(A, A, B, a, stream)) != MXQ_OK ||
+            (rc = s + 1 < steps ? ns_product<ns::STEP>(B, xt[s & 1], x, a, stream)
+                                : ns_product<ns::LAST>(B, xt[s & 1], x, a, stream)) != MXQ_OK)
             return rc;
     }
     return MXQ_OK;

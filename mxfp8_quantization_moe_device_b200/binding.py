@@ -113,8 +113,12 @@ def _check(fn, rc):
 def _call(name, dev, *args):
     """One library call with `dev` current (the kernels launch on the current
     device) on that device's current torch stream; raises on a non-OK status."""
+    fn = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        _check(name, fn(*args, torch._C._cuda_getCurrentRawStream(dev.index)))
+        return
     with torch.cuda.device(dev):
-        _check(name, getattr(lib(), name)(*args, _stream(dev)))
+        _check(name, fn(*args, torch._C._cuda_getCurrentRawStream(dev.index)))
 
 
 def _cuda(t, name):
@@ -128,7 +132,7 @@ def _stream(dev):
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
 
 
 def _mode(mode):
@@ -582,7 +586,7 @@ def _rows(t, name, dtype=None):
 def _array(t, name, dtype, shape, dev):
     """A contiguous input of this type and shape on `dev`."""
     _cuda(t, name)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != dev:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
         raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
     return t
 
@@ -606,6 +610,14 @@ def _positions(pos, tokens, dev):
     if pos.dim() != 2:
         raise TypeError("pos must be a (tokens, top_k) int32 tensor")
     return _array(pos, "pos", torch.int32, (pos.shape[0] if tokens is None else tokens, pos.shape[1]), dev)
+
+
+def _sized(name, dev, *args):
+    """A size that depends on the device, asked for with `dev` current."""
+    if dev.index == torch.cuda.current_device():
+        return getattr(lib(), name)(*args)
+    with torch.cuda.device(dev):
+        return getattr(lib(), name)(*args)
 
 
 def _workspace(nbytes, dev):
@@ -634,10 +646,9 @@ def moe_route(logits, top_k, *, valid=None, renormalize=False, weights=None, ids
     loss = _output(loss, "loss", torch.float32, (), dev)
     if loss_grad is not None:
         _out_buffer(loss_grad, "loss_grad", (E,), 4, dev, torch.float32)
-    with torch.cuda.device(dev):
-        ws = _workspace(lib().moe_route_workspace_bytes(T, E), dev)
-        _call("moe_route", dev, _ptr(logits), code, T, E, ld, _ptr(valid), k, 1 if renormalize else 0, _ptr(weights),
-              _ptr(ids), _ptr(counts), _ptr(loss), _ptr(loss_grad), _ptr(ws), ws.numel() if ws is not None else 0)
+    nbytes = _sized("moe_route_workspace_bytes", dev, T, E)
+    _call("moe_route", dev, _ptr(logits), code, T, E, ld, _ptr(valid), k, 1 if renormalize else 0, _ptr(weights),
+          _ptr(ids), _ptr(counts), _ptr(loss), _ptr(loss_grad), _ptr(_workspace(nbytes, dev)), nbytes)
     return weights, ids, counts, loss
 
 

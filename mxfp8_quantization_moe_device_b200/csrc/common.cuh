@@ -198,6 +198,12 @@ MXQ_DEV void red_release_gpu_add(int *p, int v)
     asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
+// ---------------------------------------------------------------- programmatic launches
+// A kernel launched so starts while the one before it in the stream finishes,
+// and waits here for its results before it touches global memory.
+MXQ_DEV void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+MXQ_DEV void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 // ---------------------------------------------------------------- numerics
 // bf16 is the upper half of an fp32 word: widening is exact bit placement.
 MXQ_DEV float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }

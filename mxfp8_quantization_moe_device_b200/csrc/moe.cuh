@@ -16,6 +16,8 @@
 // fixed order, so results do not change from run to run.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace mxq {
@@ -41,12 +43,42 @@ template <> struct Elem<float> {
     static MXQ_DEV float put(float f) { return f; }
 };
 
+MXQ_DEV uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 template <typename T, int V> struct alignas(sizeof(T) * V) Vec {
     T v[V];
 };
 
 template <typename T, int V> MXQ_DEV Vec<T, V> ld_vec(const T *p) { return *reinterpret_cast<const Vec<T, V> *>(p); }
 template <typename T, int V> MXQ_DEV void st_vec(T *p, const Vec<T, V> &x) { *reinterpret_cast<Vec<T, V> *>(p) = x; }
+
+// Load of one vector that stays where it is written: left to itself the
+// compiler moves a batch of loads down to their uses, one at a time.
+template <typename T, int V> MXQ_DEV Vec<T, V> ld_now(const T *p)
+{
+    Vec<T, V> x;
+    if constexpr (sizeof(T) * V == 16) {
+        const uint4 w = ld_stream_v4(p);
+        memcpy(&x, &w, 16);
+    } else if constexpr (sizeof(T) * V == 4) {
+        uint32_t w;
+        asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(w) : "l"(p));
+        memcpy(&x, &w, 4);
+    } else {
+        uint16_t w;
+        asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(w) : "l"(p));
+        memcpy(&x, &w, 2);
+    }
+    return x;
+}
+
+// the value, or zero whatever it is (a NaN times zero would stay)
+MXQ_DEV float keep_if(float v, uint32_t mask) { return __uint_as_float(__float_as_uint(v) & mask); }
 
 // unsigned key in the order of the float (-inf lowest; the caller has turned
 // -0 into +0 and has no NaN)
@@ -76,65 +108,103 @@ template <int LPT> MXQ_DEV float group_sum(float x)
     return x;
 }
 
-// a token's logits: lane i of its LPT lanes holds experts [i EPL, (i+1) EPL);
-// experts from E on read as -inf
-template <typename T, int EPL> MXQ_DEV void load_logits(const T *row, int e0, int E, bool vec, float (&v)[EPL])
-{
-    if (vec && e0 + EPL <= E) {
-        constexpr int V = 16 / sizeof(T);
-#pragma unroll
-        for (int i = 0; i < EPL; i += V) {
-            const Vec<T, V> x = ld_vec<T, V>(row + e0 + i);
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                v[i + j] = Elem<T>::get(x.v[j]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            v[i] = e0 + i < E ? Elem<T>::get(row[e0 + i]) : -INFINITY;
-    }
-}
+// A token's logits as raw words: lane i of its LPT lanes holds experts [i EPL,
+// (i + 1) EPL); experts from E on read as -inf.
+template <typename T, int EPL> struct Raw {
+    static constexpr int W = EPL * (int)sizeof(T) / 4;
+    static constexpr uint32_t NONE = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u; // -inf
+    uint32_t w[W];
 
-// softmax over the token's lanes: v becomes p, returns the largest logit.
-// A row of -inf alone has p = 0. A row with a NaN or +inf has p = NaN.
-// `bad` is the same in all lanes of the token.
-template <int LPT, int EPL> MXQ_DEV float softmax(float (&v)[EPL], bool live, bool &bad, float &rz)
-{
-    const int lane = threadIdx.x & 31;
-    float m = v[0];
-    bool odd = !(v[0] < INFINITY);
+    MXQ_DEV void none()
+    {
 #pragma unroll
-    for (int i = 1; i < EPL; ++i) {
-        m = fmaxf(m, v[i]);
-        odd |= !(v[i] < INFINITY);
+        for (int i = 0; i < W; ++i)
+            w[i] = NONE;
     }
-    const uint32_t group = LPT == 32 ? 0xffffffffu : ((1u << LPT) - 1u) << (lane & ~(LPT - 1));
-    // every lane takes part in the vote and in the maxima, whatever its row
-    const uint32_t odd_lanes = __ballot_sync(0xffffffffu, odd);
-    bad = live && (odd_lanes & group) != 0;
-    m = key_value(group_max<LPT>(order_key(m + 0.0f)));
-    const bool some = live && m > -INFINITY && !bad;
-    const float base = some ? m : 0.0f;
+    MXQ_DEV void load(const T *row, int e0, int E, bool vec)
+    {
+        if (vec && e0 + EPL <= E) {
+#pragma unroll
+            for (int i = 0; i < W; i += 4) {
+                const uint4 x = ld_stream_v4(reinterpret_cast<const uint32_t *>(row + e0) + i);
+                w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                if constexpr (sizeof(T) == 2) {
+                    const uint32_t h = e0 + i < E ? (uint32_t)row[e0 + i] : 0xFF80u;
+                    w[i >> 1] = i & 1 ? w[i >> 1] | (h << 16) : h;
+                } else {
+                    w[i] = e0 + i < E ? __float_as_uint(row[e0 + i]) : NONE;
+                }
+            }
+        }
+    }
+    MXQ_DEV float get(int i) const
+    {
+        if constexpr (sizeof(T) == 2)
+            return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+        else
+            return __uint_as_float(w[i]);
+    }
+};
+
+// p of a token from its logits v and their largest m, both in the token's
+// lanes: v becomes p. A row of -inf alone has p = 0; a row with a NaN or +inf
+// has p = NaN (m - m is NaN there) and returns true. base: what was taken off
+// the logits. exp by ex2.approx of x log2(e): off by (2 + 1.2 |x|) ulp, that is
+// least where p is largest.
+template <int LPT, int EPL> MXQ_DEV bool softmax(float (&v)[EPL], float m, float &base, float &rz)
+{
+    base = m == -INFINITY ? 0.0f : m;
     float z = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        v[i] = some ? expf(v[i] - base) : 0.0f;
+        v[i] = __expf(v[i] - base);
         z += v[i];
     }
     z = group_sum<LPT>(z);
-    rz = bad ? NAN : (some ? __fdiv_rn(1.0f, z) : 0.0f);
+    rz = z == 0.0f ? 0.0f : __fdiv_rn(1.0f, z);
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-        v[i] = bad ? NAN : v[i] * rz;
-    return m;
+        v[i] *= rz;
+    return !(z == z);
+}
+
+// Batcher's odd-even merge sort of N registers, descending: sort both halves,
+// then merge the elements R apart from LO on
+template <int LO, int N, int R, int S, typename K> MXQ_DEV void merge_descending(K (&c)[S])
+{
+    auto exchange = [&](int i, int j) {
+        const K a = c[i], b = c[j];
+        c[i] = a > b ? a : b;
+        c[j] = a > b ? b : a;
+    };
+    if constexpr (2 * R < N) {
+        merge_descending<LO, N, 2 * R>(c);
+        merge_descending<LO + R, N, 2 * R>(c);
+#pragma unroll
+        for (int i = LO + R; i + R < LO + N; i += 2 * R)
+            exchange(i, i + R);
+    } else {
+        exchange(LO, LO + R);
+    }
+}
+template <int LO, int N, int S, typename K> MXQ_DEV void sort_descending(K (&c)[S])
+{
+    if constexpr (N > 1) {
+        sort_descending<LO, N / 2>(c);
+        sort_descending<LO + N / 2, N / 2>(c);
+        merge_descending<LO, N, 1>(c);
+    }
 }
 
 constexpr int ROUTE_THREADS = 256;
 constexpr int ROUTE_WARPS = ROUTE_THREADS / 32;
 
-// bytes of the ids and weights that a CTA stages before it stores them
-__host__ __device__ constexpr size_t route_stage_bytes(int tpw, int k) { return (size_t)ROUTE_WARPS * tpw * k * 8; }
+// slots that a lane keeps: slot j of a token sits in its lane j % LPT
+template <int LPT, int EPL> constexpr int lane_slots() { return (LPT * EPL < MAX_K ? LPT * EPL : MAX_K) / LPT; }
 
 // what the CTAs leave for the finishing kernel: rows of E sums of p and of
 // choice counts per CTA, the valid tokens per CTA, partial losses, a ticket
@@ -153,7 +223,13 @@ MXQ_DEV double loss_factor(int E, int k, double n) { return n > 0.0 ? (double)E 
 } // namespace moe
 
 // Router forward: a token on LPT lanes with EPL experts each, 32 / LPT tokens
-// per warp at a time.
+// per warp at a time. A lane sorts its logits' keys once; the k best are then
+// the largest of the lanes' heads, k times, the winner's lane moving its list
+// up (a maximum over all of a lane's keys in every round cost three times the
+// instructions). Keys: the logit's order; 16-bit logits leave room for the
+// complement of the index below, so that one maximum gives value and index and
+// equal logits go to the lowest index; 32-bit ones carry it in a second word.
+// The next token's logits are loaded while this one is worked on.
 template <typename T, int LPT, int EPL>
 __global__ void __launch_bounds__(moe::ROUTE_THREADS)
     k_moe_route(const T *__restrict__ logits, int64_t tokens, int E, int64_t ld, const uint8_t *__restrict__ valid,
@@ -161,15 +237,16 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
                 moe::RoutePart part, int32_t *counts, float *loss, float *loss_grad)
 {
     using namespace moe;
-    constexpr int TPW = 32 / LPT;
+    using Key = std::conditional_t<sizeof(T) == 2, uint32_t, uint64_t>;
+    constexpr int TPW = 32 / LPT, SLOTS = lane_slots<LPT, EPL>();
+    constexpr uint32_t FIRST = 0x00800000u; // keys below belong to -inf
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sub = lane / LPT, li = lane % LPT, e0 = li * EPL;
-    int *s_ids = reinterpret_cast<int *>(smem) + (size_t)warp * TPW * k;
-    float *s_w = reinterpret_cast<float *>(smem + route_stage_bytes(TPW, k) / 2) + (size_t)warp * TPW * k;
-    float *s_p = reinterpret_cast<float *>(smem + route_stage_bytes(TPW, k)); // (warps, E)
-    int *s_c = reinterpret_cast<int *>(s_p + (size_t)ROUTE_WARPS * E);        // E
+    float *s_p = reinterpret_cast<float *>(smem);                      // (warps, E)
+    int *s_c = reinterpret_cast<int *>(s_p + (size_t)ROUTE_WARPS * E); // E
     __shared__ int s_n;
+    let_next_kernel_start();
     for (int e = tid; e < E; e += ROUTE_THREADS)
         s_c[e] = 0;
     if (tid == 0)
@@ -182,91 +259,110 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
         acc[i] = 0.0f;
     int nvalid = 0;
     const int64_t step = (int64_t)gridDim.x * ROUTE_WARPS * TPW;
-    for (int64_t t0 = ((int64_t)blockIdx.x * ROUTE_WARPS + warp) * TPW; t0 < tokens; t0 += step) {
-        const int64_t t = t0 + sub;
-        const bool in = t < tokens;
-        const bool live = in && (!valid || valid[t]);
+    int64_t t = ((int64_t)blockIdx.x * ROUTE_WARPS + warp) * TPW + sub; // this lane's token
+    Raw<T, EPL> next;
+    bool next_live = false;
+    auto fetch = [&](int64_t at) {
+        next.none();
+        next_live = false;
+        if (at < tokens) {
+            next.load(logits + at * ld, e0, E, vec);
+            next_live = !valid || valid[at] != 0;
+        }
+    };
+    fetch(t);
+    for (; t - sub < tokens; t += step) {
+        Raw<T, EPL> raw = next;
+        const bool live = next_live;
+        fetch(t + step);
+        if (!live)
+            raw.none();
         float v[EPL];
-        if (in)
-            load_logits<T, EPL>(logits + t * ld, e0, E, vec, v);
-        else
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                v[i] = -INFINITY;
-        // selection keys: the logit's order; for 16-bit logits the index in
-        // the low half, so that one maximum gives both
-        uint32_t c[EPL];
+        Key c[EPL];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const bool can = live && v[i] > -INFINITY;
+            v[i] = raw.get(i);
             const uint32_t key = order_key(v[i] + 0.0f);
-            c[i] = !can ? 0u : (sizeof(T) == 2 ? ((key & 0xFFFF0000u) | (0xFFFFu - (uint32_t)(e0 + i))) : key);
+            if constexpr (sizeof(T) == 2)
+                c[i] = (key & 0xFFFF0000u) | (0xFFFFu - (uint32_t)(e0 + i));
+            else
+                c[i] = ((uint64_t)key << 32) | (uint32_t)~(e0 + i);
         }
-        bool bad;
-        float rz;
-        const float m = softmax<LPT, EPL>(v, live, bad, rz);
+        sort_descending<0, EPL>(c);
+        uint32_t top; // the token's largest key, without the index
+        if constexpr (sizeof(T) == 2) {
+            top = group_max<LPT>(c[0]);
+            top = top & 0x80000000u ? top & 0xFFFF0000u : top | 0xFFFFu; // a negative value's key ends in ones
+        } else {
+            top = group_max<LPT>((uint32_t)(c[0] >> 32));
+        }
+        float base, rz;
+        const bool bad = softmax<LPT, EPL>(v, key_value(top), base, rz);
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
             acc[i] += v[i];
         nvalid += live && li == 0;
-        float ssum = 0.0f;
-        for (int j = 0; j < k; ++j) {
-            uint32_t best = c[0];
+
+        uint32_t best[SLOTS], who[SLOTS]; // this lane's slots: key and, for 32-bit logits, expert
 #pragma unroll
-            for (int i = 1; i < EPL; ++i)
-                best = max(best, c[i]);
-            uint32_t g = group_max<LPT>(best);
-            g = bad ? 0u : g;
-            int e = -1;
-            float val = 0.0f;
-            if (sizeof(T) == 2) {
-                if (g) {
-                    e = (int)(0xFFFFu - (g & 0xFFFFu));
-                    // a negative value's key has its cleared low half inverted
-                    val = key_value((g & 0x80000000u) ? (g & 0xFFFF0000u) : (g | 0xFFFFu));
+        for (int s = 0; s < SLOTS; ++s) {
+            best[s] = 0u;
+            who[s] = 0u;
+#pragma unroll 1
+            for (int jj = 0; jj < LPT; ++jj) {
+                if (s * LPT + jj >= k)
+                    break;
+                bool pop;
+                if constexpr (sizeof(T) == 2) {
+                    const uint32_t g = group_max<LPT>(c[0]);
+                    best[s] = li == jj ? g : best[s];
+                    pop = c[0] == g;
+                } else {
+                    // the first lane with the largest key: its experts come first
+                    const uint32_t head = (uint32_t)(c[0] >> 32);
+                    const uint32_t g = group_max<LPT>(head);
+                    const uint32_t group = LPT == 32 ? 0xffffffffu : ((1u << (LPT & 31)) - 1u) << (lane & ~(LPT - 1));
+                    const uint32_t eq = __ballot_sync(0xffffffffu, head == g) & group;
+                    const int src = __ffs(eq) - 1; // a lane of this token holds its maximum
+                    const uint32_t e = __shfl_sync(0xffffffffu, ~(uint32_t)c[0], src);
+                    best[s] = li == jj ? g : best[s];
+                    who[s] = li == jj ? e : who[s];
+                    pop = lane == src;
                 }
+                if (pop) {
 #pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    c[i] = c[i] == g ? 0u : c[i];
-            } else {
-                // the first lane with the largest key, then its first expert
-                const uint32_t group = LPT == 32 ? 0xffffffffu : ((1u << LPT) - 1u) << (lane & ~(LPT - 1));
-                const uint32_t who = __ballot_sync(0xffffffffu, best == g) & group;
-                const int src = __ffs(who) - 1;
-                int mine = 0;
-#pragma unroll
-                for (int i = EPL - 1; i >= 0; --i)
-                    mine = c[i] == g ? i : mine;
-                if (lane == src)
-#pragma unroll
-                    for (int i = 0; i < EPL; ++i)
-                        c[i] = i == mine ? 0u : c[i];
-                const int eo = __shfl_sync(0xffffffffu, e0 + mine, src < 0 ? lane : src);
-                if (g) {
-                    e = eo;
-                    val = key_value(g);
+                    for (int i = 0; i + 1 < EPL; ++i)
+                        c[i] = c[i + 1];
+                    c[EPL - 1] = 0;
                 }
             }
-            const float w = bad ? NAN : (e >= 0 ? expf(val - m) : 0.0f);
-            ssum += w;
-            if (li == 0) {
-                s_ids[sub * k + j] = e;
-                s_w[sub * k + j] = w;
-                if (e >= 0)
-                    atomicAdd(&s_c[e], 1);
+        }
+        float w[SLOTS], sum = 0.0f;
+        int id[SLOTS];
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+            const uint32_t g = best[s];
+            const bool got = !bad && g >= FIRST;
+            const uint32_t key = sizeof(T) == 4 ? g : (g & 0x80000000u ? g & 0xFFFF0000u : g | 0xFFFFu);
+            id[s] = !got ? -1 : (sizeof(T) == 2 ? (int)(0xFFFFu - (g & 0xFFFFu)) : (int)who[s]);
+            w[s] = got ? __expf(key_value(key) - base) : 0.0f;
+            sum += w[s];
+        }
+        float scale = rz;
+        if (renorm) {
+            sum = group_sum<LPT>(sum);
+            scale = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+        }
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+            const int j = s * LPT + li;
+            if (j < k && t < tokens) {
+                ids[t * k + j] = id[s];
+                weights[t * k + j] = bad ? NAN : w[s] * scale;
+                if (id[s] >= 0)
+                    atomicAdd(&s_c[id[s]], 1);
             }
         }
-        const float scale = renorm ? (ssum > 0.0f ? __fdiv_rn(1.0f, ssum) : (bad ? NAN : 0.0f)) : rz;
-        __syncwarp();
-        for (int j = li; j < k; j += LPT)
-            s_w[sub * k + j] *= scale;
-        __syncwarp();
-        const int64_t left = (tokens - t0 < TPW ? tokens - t0 : TPW) * k;
-        for (int i = lane; i < left; i += 32) {
-            ids[t0 * k + i] = s_ids[i];
-            weights[t0 * k + i] = s_w[i];
-        }
-        __syncwarp();
     }
     // the warp's tokens of one expert, then the CTA's warps in order
 #pragma unroll
@@ -329,8 +425,10 @@ __global__ void __launch_bounds__(1024)
     using namespace moe;
     __shared__ double s_p[32][33];
     __shared__ int s_c[32][33];
+    __shared__ long long s_n[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int e = blockIdx.x * 32 + lane;
+    wait_for_previous_kernel();
     double p = 0.0;
     int c = 0;
     if (e < E) {
@@ -340,14 +438,19 @@ __global__ void __launch_bounds__(1024)
             c += part.c[(size_t)r * E + e];
         }
     }
+    long long n = 0;
+    for (int r = threadIdx.x; r < R; r += 1024)
+        n += part.n[r];
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (lane == 0)
+        s_n[warp] = n;
     s_p[warp][lane] = p;
     s_c[warp][lane] = c;
     __syncthreads();
     if (warp)
         return;
-    long long n = 0;
-    for (int r = lane; r < R; r += 32)
-        n += part.n[r];
     p = 0.0;
     c = 0;
 #pragma unroll
@@ -355,6 +458,8 @@ __global__ void __launch_bounds__(1024)
         p += s_p[w][lane];
         c += s_c[w][lane];
     }
+    n = s_n[lane];
+#pragma unroll
     for (int o = 16; o; o >>= 1)
         n += __shfl_xor_sync(0xffffffffu, n, o);
     const double f = loss_factor(E, k, (double)n);
@@ -365,18 +470,23 @@ __global__ void __launch_bounds__(1024)
             loss_grad[e] = (float)(f * c);
         sum = p * c;
     }
+#pragma unroll
     for (int o = 16; o; o >>= 1)
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    int last = 0;
     if (lane == 0) {
         part.loss[blockIdx.x] = sum;
         __threadfence();
-        if (atomicAdd(part.ticket, 1) == (int)gridDim.x - 1) {
-            __threadfence();
-            double s = 0.0;
-            for (unsigned b = 0; b < gridDim.x; ++b)
-                s += reinterpret_cast<volatile double *>(part.loss)[b];
-            *loss = (float)(f * s);
-        }
+        last = atomicAdd(part.ticket, 1) == (int)gridDim.x - 1;
+        __threadfence();
+    }
+    if (__shfl_sync(0xffffffffu, last, 0)) { // at most 32 CTAs
+        sum = lane < (int)gridDim.x ? __ldcg(part.loss + lane) : 0.0;
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0)
+            *loss = (float)(f * sum);
     }
 }
 
@@ -391,51 +501,77 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
                     T *__restrict__ out)
 {
     using namespace moe;
-    constexpr int TPW = 32 / LPT;
+    constexpr int TPW = 32 / LPT, SLOTS = lane_slots<LPT, EPL>();
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sub = lane / LPT, li = lane % LPT, e0 = li * EPL;
+    // the token's row of terms at the chosen experts
     float *s_q = reinterpret_cast<float *>(smem) + (size_t)warp * 32 * EPL + sub * (LPT * EPL);
+    float4 *mine = reinterpret_cast<float4 *>(s_q + e0);
     float b[EPL];
     const float g_loss = gl ? *gl : 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
         b[i] = gl && e0 + i < E ? g_loss * loss_grad[e0 + i] : 0.0f;
     const int64_t step = (int64_t)gridDim.x * ROUTE_WARPS * TPW;
-    for (int64_t t0 = ((int64_t)blockIdx.x * ROUTE_WARPS + warp) * TPW; t0 < tokens; t0 += step) {
-        const int64_t t = t0 + sub;
-        const bool in = t < tokens;
-        const bool live = in && (!valid || valid[t]);
-        float v[EPL];
-        if (in)
-            load_logits<T, EPL>(logits + t * ld, e0, E, vec, v);
-        else
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                v[i] = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            s_q[e0 + i] = 0.0f;
-        __syncwarp();
-        bool bad;
-        float rz;
-        softmax<LPT, EPL>(v, live, bad, rz);
-        float G = 0.0f;
-        if (gw) {
-            if (live && !bad)
-                for (int j = li; j < k; j += LPT)
-                    if (ids[t * k + j] >= 0)
-                        G = fmaf(gw[t * k + j], weights[t * k + j], G);
-            G = group_sum<LPT>(G);
-            if (live && !bad)
-                for (int j = li; j < k; j += LPT) {
-                    const int e = ids[t * k + j];
-                    if (e >= 0 && e < E) {
-                        const float g = gw[t * k + j];
-                        atomicAdd(&s_q[e], weights[t * k + j] * (renorm ? g - G : g));
-                    }
-                }
+    int64_t t = ((int64_t)blockIdx.x * ROUTE_WARPS + warp) * TPW + sub;
+    Raw<T, EPL> next;
+    bool next_live = false;
+    int next_id[SLOTS];
+    float next_w[SLOTS], next_g[SLOTS];
+    auto fetch = [&](int64_t at) {
+        next.none();
+        next_live = false;
+        const bool in = at < tokens;
+        if (in) {
+            next.load(logits + at * ld, e0, E, vec);
+            next_live = !valid || valid[at] != 0;
         }
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+            const int j = s * LPT + li;
+            const bool slot = in && gw && j < k;
+            next_id[s] = slot ? ids[at * k + j] : -1;
+            next_w[s] = slot ? weights[at * k + j] : 0.0f;
+            next_g[s] = slot ? gw[at * k + j] : 0.0f;
+        }
+    };
+    fetch(t);
+    for (; t - sub < tokens; t += step) {
+        Raw<T, EPL> raw = next;
+        const bool live = next_live;
+        int id[SLOTS];
+        float w[SLOTS], g[SLOTS], G = 0.0f;
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+            id[s] = live && next_id[s] < E ? next_id[s] : -1;
+            w[s] = next_w[s];
+            g[s] = next_g[s];
+            G = id[s] >= 0 ? fmaf(g[s], w[s], G) : G;
+        }
+        fetch(t + step);
+        if (!live)
+            raw.none();
+#pragma unroll
+        for (int i = 0; i < EPL / 4; ++i)
+            mine[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float v[EPL];
+        v[0] = raw.get(0);
+        float m = v[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) {
+            v[i] = raw.get(i);
+            m = fmaxf(m, v[i]); // a NaN shows in the sum of the exponentials
+        }
+        m = key_value(group_max<LPT>(order_key(m)));
+        float base, rz;
+        softmax<LPT, EPL>(v, m, base, rz);
+        G = group_sum<LPT>(G);
+        __syncwarp();
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+            if (id[s] >= 0) // a token's experts are distinct
+                s_q[id[s]] = w[s] * (renorm ? g[s] - G : g[s]);
         __syncwarp();
         float pb = 0.0f;
 #pragma unroll
@@ -444,19 +580,28 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
         pb = group_sum<LPT>(pb) + (renorm ? 0.0f : G);
         float d[EPL];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            d[i] = fmaf(v[i], b[i] - pb, s_q[e0 + i]);
-        if (in) {
+        for (int i = 0; i < EPL / 4; ++i) {
+            const float4 q = mine[i];
+            d[4 * i] = fmaf(v[4 * i], b[4 * i] - pb, q.x);
+            d[4 * i + 1] = fmaf(v[4 * i + 1], b[4 * i + 1] - pb, q.y);
+            d[4 * i + 2] = fmaf(v[4 * i + 2], b[4 * i + 2] - pb, q.z);
+            d[4 * i + 3] = fmaf(v[4 * i + 3], b[4 * i + 3] - pb, q.w);
+        }
+        if (!live) // padding, whatever the incoming gradients hold
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                d[i] = 0.0f;
+        if (t < tokens) {
             T *row = out + t * E;
             if (vec && e0 + EPL <= E) {
-                constexpr int V = 16 / sizeof(T);
 #pragma unroll
-                for (int i = 0; i < EPL; i += V) {
-                    Vec<T, V> x;
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        x.v[j] = Elem<T>::put(d[i + j]);
-                    st_vec<T, V>(row + e0 + i, x);
+                for (int i = 0; i < EPL; i += 16 / (int)sizeof(T)) {
+                    if constexpr (sizeof(T) == 2)
+                        st_v4(row + e0 + i, pack_bf16(d[i], d[i + 1]), pack_bf16(d[i + 2], d[i + 3]),
+                              pack_bf16(d[i + 4], d[i + 5]), pack_bf16(d[i + 6], d[i + 7]));
+                    else
+                        st_v4(row + e0 + i, __float_as_uint(d[i]), __float_as_uint(d[i + 1]),
+                              __float_as_uint(d[i + 2]), __float_as_uint(d[i + 3]));
                 }
             } else {
 #pragma unroll
@@ -472,16 +617,22 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
 // ---------------------------------------------------------------------------
 // Order by expert. The n = tokens * k entries are cut into C chunks of whole
 // tiles; pass 1 counts each chunk's entries per expert, pass 2 adds the counts
-// of smaller experts and of earlier chunks and ranks the chunk's entries:
-// a warp owns a run of a tile's entries, ranks 32 of them at a time among
-// their equals (match.any), and the warps' counters are then summed in order.
-// One chunk needs no pass 1. No atomics across CTAs, nothing to clear.
+// of smaller experts and of earlier chunks and ranks the chunk's entries: a
+// warp owns a run of a tile's entries, ranks 32 of them at a time among their
+// equals (match.any), and the warps' counters are then summed in order. One
+// tile needs no pass 1. No atomics across CTAs, nothing to clear. match.any
+// bounds the ranking, so tiles are small and spread over the SMs: 131072
+// entries took 10.8 us in tiles of 8192.
 namespace moe {
-constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_THREADS = 512;
 constexpr int PLAN_WARPS = PLAN_THREADS / 32;
-constexpr int PLAN_R = 8;                                // entries per thread and tile
-constexpr int PLAN_TILE = PLAN_THREADS * PLAN_R;         // 8192
-constexpr int PLAN_MAX_CHUNKS = 64;
+constexpr int PLAN_R = 4;                                // entries per thread and tile
+constexpr int PLAN_TILE = PLAN_THREADS * PLAN_R;         // 2048
+constexpr int PLAN_MAX_CHUNKS = 128;
+
+// dynamic shared memory of the ranking kernel: first positions, sums over the
+// chunks, and the warps' counters
+__host__ __device__ constexpr size_t plan_smem(int E) { return (size_t)E * 12 + (size_t)PLAN_WARPS * E * 2; }
 
 // expert of entry i: -1 outside [0, E) and behind the end
 MXQ_DEV int entry_expert(const int32_t *ids, int64_t i, int64_t end, int E)
@@ -500,6 +651,7 @@ __global__ void __launch_bounds__(moe::PLAN_THREADS)
 {
     using namespace moe;
     extern __shared__ int s_h[];
+    let_next_kernel_start();
     for (int e = threadIdx.x; e < E; e += PLAN_THREADS)
         s_h[e] = 0;
     __syncthreads();
@@ -526,16 +678,18 @@ __global__ void __launch_bounds__(moe::PLAN_THREADS)
 {
     using namespace moe;
     extern __shared__ int smem_i[];
-    int *base = smem_i;                                              // E: next position of each expert
-    uint16_t *cnt = reinterpret_cast<uint16_t *>(smem_i + MAX_E);    // (warps, E)
+    int *base = smem_i;                                         // E: next position of each expert
+    int *total = smem_i + E, *before = smem_i + 2 * E;          // E each: all chunks', earlier chunks' counts
+    uint16_t *cnt = reinterpret_cast<uint16_t *>(smem_i + 3 * E); // (warps, E)
     __shared__ int s_scan[PLAN_WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t lo = blockIdx.x * chunk, hi = lo + chunk < n ? lo + chunk : n;
 
-    // exclusive sum over the experts of `total`, plus `before`; the last
-    // thread's inclusive sums are the group ends
-    auto set_base = [&](int total, int before) {
-        int x = total;
+    // base from `total` and `before`: an exclusive sum over the experts, two
+    // neighbours per thread (E <= 1024); the inclusive sums are the group ends
+    auto set_base = [&]() {
+        const int a = 2 * tid < E ? total[2 * tid] : 0, b = 2 * tid + 1 < E ? total[2 * tid + 1] : 0;
+        int x = a + b;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -545,37 +699,45 @@ __global__ void __launch_bounds__(moe::PLAN_THREADS)
         if (lane == 31)
             s_scan[warp] = x;
         __syncthreads();
-        if (warp == 0) {
-            int s = s_scan[lane];
+        for (int w = 0; w < warp; ++w)
+            x += s_scan[w];
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o)
-                    s += y;
+        for (int i = 0; i < 2; ++i) {
+            const int e = 2 * tid + i, end = i ? x : x - b;
+            if (e < E) {
+                base[e] = end - (i ? b : a) + before[e];
+                if (blockIdx.x == 0)
+                    offs[e] = end;
             }
-            s_scan[lane] = s;
-        }
-        __syncthreads();
-        x += warp ? s_scan[warp - 1] : 0;
-        if (tid < E) {
-            base[tid] = x - total + before;
-            if (blockIdx.x == 0)
-                offs[tid] = x;
         }
         __syncthreads();
     };
 
+    for (int e = tid; e < E; e += PLAN_THREADS) {
+        total[e] = 0;
+        before[e] = 0;
+    }
+    __syncthreads();
     if (hist) {
-        int total = 0, before = 0;
-        if (tid < E) {
+        wait_for_previous_kernel();
+        // the chunks' rows, 32 experts per warp at a time
+        const int groups = (E + 31) / 32;
+        for (int u = warp; u < groups * 4; u += PLAN_WARPS) { // a quarter of the chunks each
+            const int e = (u >> 2) * 32 + lane, c0 = (u & 3) * ((C + 3) / 4), c1 = min(C, c0 + (C + 3) / 4);
+            int all = 0, early = 0;
+            if (e < E) {
 #pragma unroll 16
-            for (int c = 0; c < C; ++c) {
-                const int h = hist[(size_t)c * E + tid];
-                total += h;
-                before += c < (int)blockIdx.x ? h : 0;
+                for (int c = c0; c < c1; ++c) {
+                    const int h = hist[(size_t)c * E + e];
+                    all += h;
+                    early += c < (int)blockIdx.x ? h : 0;
+                }
+                atomicAdd(&total[e], all); // integers: the order does not matter
+                atomicAdd(&before[e], early);
             }
         }
-        set_base(total, before);
+        __syncthreads();
+        set_base();
     }
     for (int64_t i0 = lo; i0 < hi || i0 == 0; i0 += PLAN_TILE) {
         for (int e = tid; e < PLAN_WARPS * E; e += PLAN_THREADS)
@@ -589,27 +751,28 @@ __global__ void __launch_bounds__(moe::PLAN_THREADS)
 #pragma unroll
         for (int r = 0; r < PLAN_R; ++r) {
             const uint32_t peers = __match_any_sync(0xffffffffu, e[r]);
-            const int before = e[r] >= 0 ? mine[e[r]] : 0;
-            rank[r] = before + __popc(peers & ((1u << lane) - 1u));
+            const int earlier = e[r] >= 0 ? mine[e[r]] : 0;
+            rank[r] = earlier + __popc(peers & ((1u << lane) - 1u));
             __syncwarp();
             if (e[r] >= 0 && lane == __ffs(peers) - 1)
-                mine[e[r]] = (uint16_t)(before + __popc(peers));
+                mine[e[r]] = (uint16_t)(earlier + __popc(peers));
             __syncwarp();
         }
         __syncthreads();
         // the warps' counters become each warp's first rank within the tile
-        int tile_total = 0;
-        if (tid < E) {
-#pragma unroll 8
+        for (int x = tid; x < E; x += PLAN_THREADS) {
+            int sum = 0;
+#pragma unroll
             for (int w = 0; w < PLAN_WARPS; ++w) {
-                const int c = cnt[(size_t)w * E + tid];
-                cnt[(size_t)w * E + tid] = (uint16_t)tile_total;
-                tile_total += c;
+                const int c = cnt[(size_t)w * E + x];
+                cnt[(size_t)w * E + x] = (uint16_t)sum;
+                sum += c;
             }
+            total[x] = sum; // from here on the tile's counts
         }
-        if (!hist)
-            set_base(tile_total, 0); // the only tile
         __syncthreads();
+        if (!hist)
+            set_base(); // the only tile
 #pragma unroll
         for (int r = 0; r < PLAN_R; ++r) {
             const int64_t i = i0 + (int64_t)warp * (32 * PLAN_R) + r * 32 + lane;
@@ -617,8 +780,8 @@ __global__ void __launch_bounds__(moe::PLAN_THREADS)
                 pos[i] = e[r] >= 0 ? base[e[r]] + mine[e[r]] + rank[r] : -1;
         }
         __syncthreads();
-        if (tid < E)
-            base[tid] += tile_total;
+        for (int x = tid; x < E; x += PLAN_THREADS)
+            base[x] += total[x];
     }
 }
 
@@ -680,59 +843,78 @@ __global__ void __launch_bounds__(moe::ROW_THREADS)
     }
 }
 
-// out[t] = sum_j w[t][j] y[pos[t][j]] (w NULL: ones), slots in order, fp32
-template <typename T, int V, int U>
-__global__ void __launch_bounds__(moe::ROW_THREADS)
+// out[t] = sum_j w[t][j] y[pos[t][j]] (w NULL: ones), slots in order, fp32. A
+// warp takes one of `parts` runs of `run` vectors of a token's row and walks it
+// 32 * U vectors at a time (one run per row when there are tokens enough: the
+// slots are then looked up once a row). The loads of J slots are issued
+// together, without a branch or predicate between them: a dropped slot reads
+// the token's first row that is there and what it read is cleared, a lane
+// behind the run's end reads the run's last vector and stores nothing.
+template <typename T, int V, int U, int J>
+__global__ void __launch_bounds__(moe::ROW_THREADS, 4)
     k_moe_combine(const T *__restrict__ y, int64_t M, int64_t K, int64_t ld, const int32_t *__restrict__ pos,
-                  const float *__restrict__ weights, int64_t tokens, int k, T *__restrict__ out)
+                  const float *__restrict__ weights, uint32_t tokens, uint32_t parts, uint32_t run, int k,
+                  T *__restrict__ out)
 {
     using namespace moe;
     const int lane = threadIdx.x & 31;
-    const int64_t nvec = K / V, segs = (nvec + 32 * U - 1) / (32 * U), all = tokens * segs;
-    for (int64_t w = (int64_t)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5); w < all;
-         w += (int64_t)gridDim.x * ROW_WARPS) {
-        const int64_t t = w / segs, v0 = (w - t * segs) * (32 * U) + lane;
-        const int64_t row = lane < k ? slot_row(pos, t * k + lane, M) : -1;
-        const float wl = lane < k ? (weights ? weights[t * k + lane] : 1.0f) : 0.0f;
-        float acc[U][V];
+    const uint32_t nvec = (uint32_t)(K / V), all = tokens * parts, stride = gridDim.x * ROW_WARPS;
+    for (uint32_t w = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5); w < all; w += stride) {
+        const uint32_t t = w / parts, v_lo = (w - t * parts) * run, v_hi = min(v_lo + run, nvec);
+        int64_t row = -1; // lane j: slot j's row and weight
+        float wl = 0.0f;
+        if (lane < k) {
+            const int64_t i = (int64_t)t * k + lane;
+            row = slot_row(pos, i, M);
+            wl = row < 0 ? 0.0f : (weights ? weights[i] : 1.0f);
+        }
+        const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
+        const int64_t any = __shfl_sync(0xffffffffu, row, there ? __ffs(there) - 1 : 0);
+        T *dst = out + (int64_t)t * K;
+#pragma unroll 1
+        for (uint32_t v0 = v_lo + lane; v0 - lane < v_hi; v0 += 32 * U) {
+            float acc[U][V];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                acc[u][i] = 0.0f;
-        for (int j0 = 0; j0 < k; j0 += 4) {
-            Vec<T, V> r[4][U];
-            int64_t s[4];
-            float wj[4];
+                for (int i = 0; i < V; ++i)
+                    acc[u][i] = 0.0f;
+            uint32_t at[U];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) { // lanes from k on hold -1
-                s[j] = __shfl_sync(0xffffffffu, row, (j0 + j) & 31);
-                wj[j] = __shfl_sync(0xffffffffu, wl, (j0 + j) & 31);
-                if (j0 + j >= k)
-                    s[j] = -1;
+            for (int u = 0; u < U; ++u)
+                at[u] = min(v0 + 32 * u, v_hi - 1) * V;
+#pragma unroll 1
+            for (int j0 = 0; j0 < k && there; j0 += J) {
+                Vec<T, V> r[J][U];
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (s[j] >= 0 && v0 + 32 * u < nvec)
-                        r[j][u] = ld_vec<T, V>(y + s[j] * ld + (v0 + 32 * u) * V);
-            }
+                for (int j = 0; j < J; ++j) {
+                    const int64_t s = __shfl_sync(0xffffffffu, row, (j0 + j) & 31);
+                    const T *p = y + (s >= 0 ? s : any) * ld;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (s[j] >= 0)
+                    for (int u = 0; u < U; ++u)
+                        r[j][u] = ld_now<T, V>(p + at[u]);
+                }
+#pragma unroll
+                for (int j = 0; j < J; ++j) { // lanes from k on hold no slot
+                    const float wj = __shfl_sync(0xffffffffu, wl, (j0 + j) & 31);
+                    const uint32_t mask = (there >> ((j0 + j) & 31)) & 1u ? 0xffffffffu : 0u;
 #pragma unroll
                     for (int u = 0; u < U; ++u)
 #pragma unroll
                         for (int i = 0; i < V; ++i)
-                            acc[u][i] = fmaf(wj[j], Elem<T>::get(r[j][u].v[i]), acc[u][i]);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (v0 + 32 * u < nvec) {
-                Vec<T, V> o;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    o.v[i] = Elem<T>::put(acc[u][i]);
-                st_vec<T, V>(out + t * K + (v0 + 32 * u) * V, o);
+                            acc[u][i] = fmaf(wj, keep_if(Elem<T>::get(r[j][u].v[i]), mask), acc[u][i]);
+                }
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (v0 + 32 * u < v_hi) {
+                    Vec<T, V> o;
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        o.v[i] = Elem<T>::put(acc[u][i]);
+                    st_vec<T, V>(dst + (int64_t)(v0 + 32 * u) * V, o);
+                }
+        }
     }
 }
 
@@ -747,16 +929,16 @@ __global__ void __launch_bounds__(moe::ROW_THREADS)
 {
     using namespace moe;
     const int lane = threadIdx.x & 31;
-    const int64_t nvec = K / V, n = tokens * k;
-    const int64_t end = max(0, offs[E - 1]);
+    const uint32_t nvec = (uint32_t)(K / V);
+    const int64_t n = tokens * k, end = max(0, offs[E - 1]);
     const int64_t all = n + (dy && end < M ? M - end : 0);
     for (int64_t w = (int64_t)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5); w < all;
          w += (int64_t)gridDim.x * ROW_WARPS) {
         if (w >= n) {
             Vec<T, V> zero = {};
             T *d = dy + (end + w - n) * K;
-            for (int64_t v = lane; v < nvec; v += 32)
-                st_vec<T, V>(d + v * V, zero);
+            for (uint32_t v = lane; v < nvec; v += 32)
+                st_vec<T, V>(d + (int64_t)v * V, zero);
             continue;
         }
         const int64_t s = slot_row(pos, w, M);
@@ -768,15 +950,17 @@ __global__ void __launch_bounds__(moe::ROW_THREADS)
         const T *g = dout + (w / k) * ldd;
         const float wt = weights ? weights[w] : 1.0f;
         float acc = 0.0f;
-        for (int64_t v0 = lane; v0 < nvec; v0 += 32 * U) {
+        const T *yr = y + s * ldy;
+#pragma unroll 1
+        for (uint32_t v0 = lane; v0 - lane < nvec; v0 += 32 * U) {
             Vec<T, V> a[U], b[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (v0 + 32 * u < nvec) {
-                    a[u] = ld_vec<T, V>(g + (v0 + 32 * u) * V);
-                    if (dw)
-                        b[u] = ld_vec<T, V>(y + s * ldy + (v0 + 32 * u) * V);
-                }
+            for (int u = 0; u < U; ++u) { // behind the end: the last vector, unused
+                const uint32_t at = min(v0 + 32 * u, nvec - 1) * V;
+                a[u] = ld_now<T, V>(g + at);
+                if (dw)
+                    b[u] = ld_now<T, V>(yr + at);
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (v0 + 32 * u < nvec) {
@@ -789,7 +973,7 @@ __global__ void __launch_bounds__(moe::ROW_THREADS)
                         o.v[i] = Elem<T>::put(wt * f);
                     }
                     if (dy)
-                        st_vec<T, V>(dy + s * K + (v0 + 32 * u) * V, o);
+                        st_vec<T, V>(dy + s * K + (int64_t)(v0 + 32 * u) * V, o);
                 }
         }
         if (dw) {

@@ -76,8 +76,8 @@ int route_forward(const void *logits, int64_t tokens, int64_t E, int64_t ld, con
                   float *loss, float *loss_grad, cudaStream_t stream)
 {
     const RouteShape s = route_shape(E);
-    // at most 39 KB (1024 experts), below what needs a function attribute
-    const size_t smem = moe::route_stage_bytes(32 / s.lpt, k) + (size_t)moe::ROUTE_WARPS * E * 4 + (size_t)E * 4;
+    // at most 36 KB (1024 experts), below what needs a function attribute
+    const size_t smem = (size_t)(moe::ROUTE_WARPS + 1) * E * 4;
     const int vec = E % (16 / sizeof(T)) == 0 && rows_vec16(logits, ld, sizeof(T));
     const T *l = static_cast<const T *>(logits);
 #define MXQ_ROUTE_CASE(TT, LPT, EPL)                                                                                 \
@@ -138,8 +138,12 @@ int row_vector(std::initializer_list<RowOperand> ops, int64_t K, int size)
     return 1;
 }
 
-// vectors of V elements, U of them per lane: at least 64 bytes per lane
-#define MXQ_ROW_VARIANTS(X) X(MXQ_BF16, uint16_t, 8, 4) X(MXQ_BF16, uint16_t, 2, 8) X(MXQ_BF16, uint16_t, 1, 8) X(MXQ_FP32, float, 4, 4) X(MXQ_FP32, float, 1, 8)
+// Vectors of V elements, and how many of them a lane has in flight: U of one
+// row where one row is read, U4 of each of up to four slots, U8 of each of J8
+// slots where there are more (more in flight costs residency: at 16384 x 4 rows
+// of 7168 bf16, U4 = 2 with four CTAs per SM sums in 190 us, with two CTAs and
+// twice the loads in 197).
+#define MXQ_ROW_VARIANTS(X) X(MXQ_BF16, uint16_t, 8, 4, 2, 8, 1) X(MXQ_BF16, uint16_t, 2, 8, 4, 4, 4) X(MXQ_BF16, uint16_t, 1, 8, 4, 4, 4) X(MXQ_FP32, float, 4, 4, 2, 8, 1) X(MXQ_FP32, float, 1, 8, 4, 4, 4)
 
 unsigned row_grid(int64_t warps, int sms)
 {
@@ -151,7 +155,8 @@ int rows_check(int32_t dtype, int64_t T, int32_t k, int64_t K, int64_t M, int64_
 {
     if (T < 0 || K < 0 || M < 0 || k < 1 || ld < K)
         return MXQ_ERR_SHAPE;
-    if (!dtype_ok(dtype) || k > moe::MAX_K || M >= (int64_t(1) << 31) || T >= (int64_t(1) << 31) / k)
+    if (!dtype_ok(dtype) || k > moe::MAX_K || K >= (int64_t(1) << 31) || M >= (int64_t(1) << 31) ||
+        T >= (int64_t(1) << 31) / k)
         return MXQ_ERR_UNSUPPORTED;
     return MXQ_OK;
 }
@@ -200,8 +205,8 @@ int moe_route(const void *logits, int32_t dtype, int64_t tokens, int64_t experts
                                     part, R, counts, loss, loss_grad, stream);
     if (rc != MXQ_OK || R == 1)
         return rc;
-    return launch(k_moe_route_finish, dim3((unsigned)((experts + 31) / 32)), dim3(1024), 0, stream, false, part,
-                  (int)R, (int)experts, (int)top_k, counts, loss, loss_grad);
+    return launch_chained(k_moe_route_finish, dim3((unsigned)((experts + 31) / 32)), dim3(1024), 0, stream, false,
+                          part, (int)R, (int)experts, (int)top_k, counts, loss, loss_grad);
 }
 
 int moe_route_backward(const void *logits, int32_t dtype, int64_t tokens, int64_t experts, int64_t row_stride,
@@ -265,13 +270,14 @@ int moe_dispatch_plan(const int32_t *ids, int64_t entries, int64_t experts, int3
         if (rc != MXQ_OK)
             return rc;
     }
-    static std::atomic<uint64_t> set[2];
-    const int rc = allow_smem(k_moe_plan_rank, moe::MAX_E * 4 + moe::PLAN_WARPS * moe::MAX_E * 2, set);
-    if (rc != MXQ_OK)
-        return rc;
-    return launch(k_moe_plan_rank, dim3((unsigned)chunks), dim3(moe::PLAN_THREADS),
-                  moe::MAX_E * 4 + (size_t)moe::PLAN_WARPS * experts * 2, stream, false, ids, entries, (int)experts,
-                  chunk, static_cast<const int *>(hist), (int)chunks, pos, offs);
+    // at most 44 KB (1024 experts), below what needs a function attribute
+    const size_t smem = moe::plan_smem((int)experts);
+    const dim3 grid((unsigned)chunks), block(moe::PLAN_THREADS);
+    if (!hist)
+        return launch(k_moe_plan_rank, grid, block, smem, stream, false, ids, entries, (int)experts, chunk,
+                      (const int *)nullptr, (int)chunks, pos, offs);
+    return launch_chained(k_moe_plan_rank, grid, block, smem, stream, false, ids, entries, (int)experts, chunk,
+                          (const int *)hist, (int)chunks, pos, offs);
 }
 
 int moe_dispatch(const void *x, int32_t dtype, int64_t tokens, int64_t cols, int64_t row_stride, const int32_t *pos,
@@ -295,7 +301,7 @@ int moe_dispatch(const void *x, int32_t dtype, int64_t tokens, int64_t cols, int
     if (rc != MXQ_OK)
         return rc;
     const int v = row_vector({{x, row_stride}, {out, cols}}, cols, size);
-#define MXQ_ROW_CASE(D, T, V, U)                                                                                     \
+#define MXQ_ROW_CASE(D, T, V, U, U4, J8, U8)                                                                         \
     if (dtype == D && v == V) {                                                                                      \
         const int64_t segs = (cols / V + 32 * U - 1) / (32 * U);                                                     \
         return launch(k_moe_dispatch<T, V, U>, dim3(row_grid((tokens + 16) * segs, di->sms)),                        \
@@ -325,15 +331,24 @@ int moe_combine(const void *y, int32_t dtype, int64_t rows, int64_t cols, int64_
     if (rc != MXQ_OK)
         return rc;
     const int v = row_vector({{y, row_stride}, {out, cols}}, cols, size);
-#define MXQ_ROW_CASE(D, T, V, U)                                                                                     \
-    if (dtype == D && v == V) {                                                                                      \
-        const int64_t segs = (cols / V + 16 * U - 1) / (16 * U);                                                     \
-        return launch(k_moe_combine<T, V, U / 2>, dim3(row_grid(tokens * segs, di->sms)), dim3(moe::ROW_THREADS), 0, \
-                      stream, false, static_cast<const T *>(y), rows, cols, row_stride, pos, weights, tokens,        \
-                      (int)top_k, static_cast<T *>(out));                                                            \
+    // runs of a row: one when the tokens alone give every resident warp eight
+    const int64_t want = std::max<int64_t>(1, (int64_t)di->sms * 32 * 8 / tokens);
+#define MXQ_ROW_LAUNCH(T, V, U, J)                                                                                   \
+    {                                                                                                                \
+        const int64_t width = 32 * U, steps = (cols / V + width - 1) / width, split = std::min(steps, want);         \
+        const int64_t run = (steps + split - 1) / split * width, parts = (cols / V + run - 1) / run;                 \
+        return launch(k_moe_combine<T, V, U, J>, dim3(row_grid(tokens * parts, di->sms)), dim3(moe::ROW_THREADS), 0, \
+                      stream, false, static_cast<const T *>(y), rows, cols, row_stride, pos, weights,                \
+                      (uint32_t)tokens, (uint32_t)parts, (uint32_t)run, (int)top_k, static_cast<T *>(out));          \
     }
+#define MXQ_ROW_CASE(D, T, V, U, U4, J8, U8)                                                                         \
+    if (dtype == D && v == V && top_k <= 4)                                                                          \
+        MXQ_ROW_LAUNCH(T, V, U4, 4)                                                                                  \
+    if (dtype == D && v == V)                                                                                        \
+        MXQ_ROW_LAUNCH(T, V, U8, J8)
     MXQ_ROW_VARIANTS(MXQ_ROW_CASE)
 #undef MXQ_ROW_CASE
+#undef MXQ_ROW_LAUNCH
     return MXQ_ERR_UNSUPPORTED;
 }
 
@@ -362,7 +377,7 @@ int moe_combine_backward(const void *grad_out, int64_t grad_row_stride, const vo
     const int v = row_vector({{grad_out, grad_row_stride}, {grad_weights ? y : nullptr, grad_weights ? row_stride : 0},
                               {grad_y, cols}},
                              cols, size);
-#define MXQ_ROW_CASE(D, T, V, U)                                                                                     \
+#define MXQ_ROW_CASE(D, T, V, U, U4, J8, U8)                                                                         \
     if (dtype == D && v == V)                                                                                        \
         return launch(k_moe_combine_bwd<T, V, U>, dim3(row_grid(tokens * top_k + 16, di->sms)),                      \
                       dim3(moe::ROW_THREADS), 0, stream, false, static_cast<const T *>(grad_out), grad_row_stride,   \

@@ -252,6 +252,34 @@ int launch_pairs(void (*kernel)(K...), dim3 grid, dim3 block, size_t smem, cudaS
 }
 
 
+// a launch that may begin while the kernel before it in the stream finishes
+// (the kernel waits for it before it touches global memory); pairs: clusters
+// of two CTAs
+template <typename... K, typename... A>
+int launch_chained(void (*kernel)(K...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool pairs,
+                   A &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pairs ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return MXQ_ERR_LAUNCH;
+    }
+    return MXQ_OK;
+}
+
 // ------------------------------------------------------------ jagged plan
 struct JaggedPlan {
     bool twopass = false;     // k_jagged_amax + k_jagged_cast

@@ -86,11 +86,6 @@ template <int TN> constexpr uint32_t idesc()
     return (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
 }
 
-// Programmatic launches: a kernel starts while the one before it finishes and
-// waits here for its results before it touches global memory.
-MXQ_DEV void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-MXQ_DEV void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;"); }
-
 enum Mode { GRAM = 0, POLY = 1, STEP = 2, LAST = 3 };
 
 struct Args {

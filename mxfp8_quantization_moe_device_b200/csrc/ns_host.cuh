@@ -57,34 +57,6 @@ int ns_map(CUtensorMap *map, const void *p, int64_t inner, int64_t ld, int64_t r
                     store ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// a launch that may begin while the kernel before it in the stream finishes
-// (the kernel waits for it before it touches global memory); pairs: clusters
-// of two CTAs
-template <typename... K, typename... A>
-int launch_chained(void (*kernel)(K...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool pairs,
-                   A &&...args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = pairs ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return MXQ_ERR_LAUNCH;
-    }
-    return MXQ_OK;
-}
-
 // the operands of one product: a matrix by rows, inner length and row length
 struct NsOperand {
     const void *p;

@@ -161,9 +161,9 @@ def test_host_checks():
 
 def test_workspace_sizes():
     L = mxq.lib()
-    assert L.moe_dispatch_plan_workspace_bytes(8192, 64) == 0
-    assert L.moe_dispatch_plan_workspace_bytes(8193, 64) == 2 * 64 * 4
-    assert L.moe_dispatch_plan_workspace_bytes(64 * 8192 + 1, 64) == 33 * 64 * 4
+    assert L.moe_dispatch_plan_workspace_bytes(2048, 64) == 0
+    assert L.moe_dispatch_plan_workspace_bytes(2049, 64) == 2 * 64 * 4
+    assert L.moe_dispatch_plan_workspace_bytes(128 * 2048 + 1, 64) == 65 * 64 * 4
     assert L.moe_route_workspace_bytes(-1, 64) == 0 and L.moe_route_workspace_bytes(16, 2000) == 0
 
 
@@ -381,7 +381,7 @@ def test_plan_many_entries_one_expert_and_bad_ids():
 
 # ------------------------------------------------------------ rows
 ROWS = [(0, 4, 2, 64), (1, 3, 1, 1), (3, 4, 2, 8), (17, 5, 3, 63), (50, 16, 2, 2048), (33, 60, 6, 1419),
-        (129, 8, 8, 514), (20, 40, 32, 100), (7, 4, 2, 7168), (260, 4, 4, 130)]
+        (129, 8, 8, 514), (20, 40, 32, 100), (7, 4, 2, 7168), (260, 4, 4, 130), (11, 6, 5, 31), (40, 12, 5, 37), (6, 3, 2, 33)]
 
 
 @pytest.mark.gpu

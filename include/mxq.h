@@ -536,8 +536,8 @@ int moe_combine_backward(const void *grad_out, int64_t grad_row_stride, const vo
  * (they do for the usual coefficients) and coefficients within [-16, 16]. A
  * matrix of zeros gives zeros; a NaN or infinity makes its own matrix NaN and
  * no other. rows, cols <= 65536, batch <= 65535, steps <= 64. workspace:
- * newton_schulz_workspace_bytes() bytes, 256-byte aligned, not shared by
- * calls that overlap on the GPU.
+ * newton_schulz_workspace_bytes() bytes (NULL when 0), 256-byte aligned, not
+ * shared by calls that overlap on the GPU.
  * ------------------------------------------------------------------------ */
 size_t newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, int32_t steps);
 int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols, int32_t steps,
@@ -582,9 +582,10 @@ int mxq_version(void);
  *                              (CTA pairs with 256 x 256 tiles when N and
  *                              K are multiples of 256), 1 the one-SM
  *                              kernel.
- *   MXQ_TESTING_NS_TILE        newton_schulz: 0 automatic (the tile width
- *                              with the shorter estimated time), 128 or 256
- *                              columns forced. */
+ *   MXQ_TESTING_NS_TILE        newton_schulz: 0 automatic (one launch for
+ *                              small matrices, else the tile width with the
+ *                              shorter estimated time), 128 or 256 columns
+ *                              forced. */
 #define MXQ_TESTING_WAIT_LIMIT_NS 1
 #define MXQ_TESTING_SKIP_ARRIVAL 2
 #define MXQ_TESTING_FORCE_PATH 3

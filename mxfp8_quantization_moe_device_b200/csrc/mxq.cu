@@ -19,6 +19,7 @@
 #include "mxj.cuh"
 #include "moe.cuh"
 #include "ns.cuh"
+#include "ns_small.cuh"
 
 using namespace mxq;
 

@@ -118,6 +118,46 @@ MXQ_DEV uint32_t pack_half2(float lo, float hi)
 MXQ_DEV float half_value(uint16_t h) { return __half2float(__ushort_as_half(h)); }
 MXQ_DEV float2 unpack_half2(uint32_t w) { return __half22float2(*reinterpret_cast<__half2 *>(&w)); }
 
+// A warp's 32 x 32 chunk of 16-bit values, one row per lane (two columns per
+// word), to shared memory: rows of 64 bytes, 16-byte pieces swizzled by the
+// row as the 64-byte TMA swizzle does, so that no two lanes' stores share banks
+MXQ_DEV void chunk_to_smem(uint8_t *st, const uint32_t (&h)[16])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+        sts_v4(smem_u32(st) + (uint32_t)(lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)),
+               make_uint4(h[4 * g], h[4 * g + 1], h[4 * g + 2], h[4 * g + 3]));
+}
+
+// The chunk to rows of a row-major matrix (dst: its first element, n per row;
+// `rows` and `cols` of it exist) through shared memory, so that a store covers
+// whole lines: eight rows of four 16-byte pieces at a time with `vec`, else a
+// row at a time, one element per lane.
+MXQ_DEV void rows_out(uint8_t *st, const uint32_t (&h)[16], uint16_t *dst, int64_t n, int rows, int cols, int vec)
+{
+    const int lane = threadIdx.x & 31;
+    chunk_to_smem(st, h);
+    __syncwarp();
+    if (vec && cols >= CHUNK) {
+        const int g = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int y = 8 * i + (lane >> 2);
+            const uint4 x = *reinterpret_cast<const uint4 *>(st + y * 64 + ((g ^ ((y >> 1) & 3)) << 4));
+            if (y < rows)
+                st_v4(dst + y * n + 8 * g, x.x, x.y, x.z, x.w);
+        }
+    } else if (lane < cols) {
+#pragma unroll 8
+        for (int y = 0; y < 32; ++y)
+            if (y < rows)
+                dst[y * n + lane] =
+                    *reinterpret_cast<const uint16_t *>(st + y * 64 + (((lane >> 3) ^ ((y >> 1) & 3)) << 4) + (lane & 7) * 2);
+    }
+    __syncwarp();
+}
+
 // two neighbouring elements; `pair`: as one aligned word
 MXQ_DEV float2 in_pair(const uint16_t *p, bool pair, bool second)
 {
@@ -221,6 +261,19 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// 2^8 / norm as two fp32 factors, to be multiplied one after the other: either
+// alone may leave fp32's range, an element times the first does not where it
+// matters. A norm of zero gives zeros, NaN gives NaN.
+MXQ_DEV void scale_factors(double norm, float &f0, float &f1)
+{
+    const double inv = norm > 0.0 ? (double)SX / norm : (norm == 0.0 ? 0.0 : norm);
+    int ex = 0;
+    const double fr = frexp(inv, &ex);
+    const bool plain = inv == 0.0 || !(norm > 0.0) || isinf(norm);
+    f0 = plain ? 1.0f : (float)ldexp(1.0, ex / 2);
+    f1 = plain ? (float)inv : (float)ldexp(fr, ex - ex / 2);
+}
+
 // X0 from G (rows, cols) in 64 x 64 tiles. X is G, or with `tall` G^T: the
 // tile as it is read goes to X (tall: to X^T and lo), its transpose to X^T and
 // lo (tall: to X). A thread moves pairs of neighbours.
@@ -243,15 +296,7 @@ __global__ void __launch_bounds__(256)
         for (int o = 16; o; o >>= 1)
             s += __shfl_xor_sync(0xffffffffu, s, o);
         if (threadIdx.x == 0) {
-            // 2^8 / (norm + eps) as two fp32 factors: either alone may leave
-            // fp32's range, g times the first does not where it matters
-            const double norm = sqrt(s) + eps;
-            const double inv = norm > 0.0 ? (double)SX / norm : (norm == 0.0 ? 0.0 : norm);
-            int ex = 0;
-            const double fr = frexp(inv, &ex);
-            const bool plain = inv == 0.0 || !(norm > 0.0) || isinf(norm);
-            s_f[0] = plain ? 1.0f : (float)ldexp(1.0, ex / 2);
-            s_f[1] = plain ? (float)inv : (float)ldexp(fr, ex - ex / 2);
+            scale_factors(sqrt(s) + eps, s_f[0], s_f[1]);
         }
     }
     __syncthreads();
@@ -578,11 +623,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                             bulk_wait_read<1>(); // the store before the last has read this buffer
                         __syncwarp();
                     }
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        sts_v4(smem_u32(st) + (uint32_t)(lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)),
-                               make_uint4(h[4 * g], h[4 * g + 1], h[4 * g + 2], h[4 * g + 3]));
                     if constexpr (MODE != LAST) {
+                        chunk_to_smem(st, h);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0 && r0 < q.m) {
@@ -590,25 +632,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                             bulk_commit();
                         }
                     } else {
-                        __syncwarp();
-                        uint16_t *dst = q.out + ((int64_t)w.e * q.m + r0) * q.n + c0;
-                        if (q.out_vec && c0 + CHUNK <= cols) { // eight rows at a time, four lanes each
-                            const int g = lane & 3;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int y = 8 * i + (lane >> 2);
-                                const uint4 x = *reinterpret_cast<const uint4 *>(st + y * 64 + ((g ^ ((y >> 1) & 3)) << 4));
-                                if (r0 + y < q.m)
-                                    st_v4(dst + (int64_t)y * q.n + 8 * g, x.x, x.y, x.z, x.w);
-                            }
-                        } else if (c0 + lane < cols) { // a row at a time, one element per lane
-#pragma unroll 8
-                            for (int y = 0; y < 32; ++y)
-                                if (r0 + y < q.m)
-                                    dst[(int64_t)y * q.n + lane] = *reinterpret_cast<const uint16_t *>(
-                                        st + y * 64 + (((lane >> 3) ^ ((y >> 1) & 3)) << 4) + (lane & 7) * 2);
-                        }
-                        __syncwarp();
+                        rows_out(st, h, q.out + ((int64_t)w.e * q.m + r0) * q.n + c0, q.n, q.m - r0, cols - c0,
+                                 q.out_vec);
                     }
                     buf ^= 1;
                 }

@@ -136,13 +136,52 @@ int ns_start(const T *g, int64_t E, int64_t rows, int64_t cols, const NsPlan &p,
                   reinterpret_cast<uint16_t *>(ws + p.xt[0]), reinterpret_cast<uint16_t *>(ws + p.lo), (int)p.ldt);
 }
 
+// one launch for all steps: the smaller side fits a tile, the larger a cluster
+bool ns_is_small(int64_t rows, int64_t cols)
+{
+    return g_ns_tile.load() == 0 && std::min(rows, cols) <= ns::SM_M &&
+           std::max(rows, cols) <= ns::SM_SLAB * ns::SM_MAX_CTAS;
+}
+
+template <typename T>
+int ns_small(const T *g, int64_t E, int64_t rows, int64_t cols, int32_t steps, const float *coefficients, double eps,
+             uint16_t *out, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> set[2];
+    const int rc = allow_smem(ns::k_ns_small<T>, (int)ns::small_smem_bytes(true), set);
+    if (rc != MXQ_OK)
+        return rc;
+    ns::Coefs co;
+    std::memcpy(co.v, coefficients, sizeof(float) * 3 * (size_t)steps);
+    const int ctas = (int)((std::max(rows, cols) + ns::SM_SLAB - 1) / ns::SM_SLAB);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(E * ctas));
+    cfg.blockDim = dim3(ns::SM_THREADS);
+    cfg.dynamicSmemBytes = ns::small_smem_bytes(ctas > 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, ns::k_ns_small<T>, g, (int)rows, (int)cols, ctas, (int)(rows > cols), (int)steps, co,
+                           eps, out, (int)(cols % 8 == 0 && aligned(out, 16)), wait_ns()) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return MXQ_ERR_LAUNCH;
+    }
+    return MXQ_OK;
+}
+
 } // namespace
 
 extern "C" {
 
 size_t newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, int32_t steps)
 {
-    if (ns_check(batch, rows, cols, steps) != MXQ_OK || batch == 0 || rows == 0 || cols == 0)
+    if (ns_check(batch, rows, cols, steps) != MXQ_OK || batch == 0 || rows == 0 || cols == 0 ||
+        ns_is_small(rows, cols))
         return 0;
     return ns_plan(batch, rows, cols, steps).bytes;
 }
@@ -170,6 +209,11 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
         return MXQ_ERR_NULL;
     if (!aligned(g, dtype_size(dtype)) || !aligned(out, 2))
         return MXQ_ERR_ALIGN;
+    if (ns_is_small(rows, cols))
+        return dtype == MXQ_BF16 ? ns_small(static_cast<const uint16_t *>(g), batch, rows, cols, steps, coefficients, eps,
+                                            static_cast<uint16_t *>(out), stream)
+                                 : ns_small(static_cast<const float *>(g), batch, rows, cols, steps, coefficients, eps,
+                                            static_cast<uint16_t *>(out), stream);
     const NsPlan p = ns_plan(batch, rows, cols, steps);
     if (!workspace || workspace_bytes < p.bytes)
         return MXQ_ERR_WORKSPACE;

@@ -1,0 +1,411 @@
+// ns_small.cuh - newton_schulz (see ns.cuh) for matrices whose smaller side is
+// at most 128: all steps of a matrix in one launch, on chip.
+//
+// A CTA holds a slab of up to 256 columns of X (m <= 128 rows): hi of X and of
+// X^T as fp16 in shared memory in the layout that tcgen05.mma reads, X itself
+// in fp32 in TMEM, as the accumulator of the step's last product: a X is
+// written there and B X added to it by the tensor core, so X is never rounded.
+// A matrix with more columns takes a cluster of up to eight CTAs: each
+// multiplies its slab with itself, the partial 128 x 128 products are summed
+// over distributed shared memory in rank order (every CTA sums some rows and
+// sends them to all), and the rest is local to the slab.
+//
+// Per step: three products (K = 256, 128, 128; about 1.4 us of tensor time),
+// three drains of TMEM by sixteen warps, two cluster barriers. What bounds it is
+// the chain of barriers, TMEM loads and shared-memory stores, not bandwidth or
+// the tensor pipe; against the general kernels' three launches per step it
+// saves their launch, fill and drain (about 8 us each).
+#pragma once
+
+#include <cstddef>
+
+#include "ns.cuh"
+
+namespace mxq {
+namespace ns {
+
+constexpr int SM_M = 128;              // rows of X, at most
+constexpr int SM_SLAB = 256;           // columns of X per CTA
+constexpr int SM_MAX_CTAS = 8;         // CTAs per matrix
+constexpr int SM_THREADS = 512;        // four warps per 32 rows, a quarter of the columns each
+constexpr int MAX_STEPS = 64;
+
+struct Coefs {
+    float v[3 * MAX_STEPS];
+};
+
+struct __align__(1024) SmallSmem {
+    uint8_t xh[SM_SLAB / 64][SM_M * 128];  // X: blocks of 64 columns, 128-byte rows
+    uint8_t xt[SM_M / 64][SM_SLAB * 128];  // X^T: blocks of 64 rows of X
+    uint8_t ab[SM_M / 64][SM_M * 128];     // A, then B
+    double sums[SM_MAX_CTAS];              // every CTA's sum of squares
+    double warp_sum[SM_THREADS / 32];
+    uint64_t bar;
+    uint32_t tmem_base;
+    float factor[2];
+    alignas(16) float part[SM_M * SM_M];   // fp32 A of this slab (clusters only)
+};
+// one CTA per matrix needs no room for partial products
+constexpr size_t small_smem_bytes(bool cluster)
+{
+    return (cluster ? sizeof(SmallSmem) : offsetof(SmallSmem, part)) + 1024;
+}
+
+// fp32 accumulator, f16 x f16, both K-major, M 128, N n (a multiple of 16)
+MXQ_DEV uint32_t small_idesc(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(SM_M >> 4) << 24); }
+
+MXQ_DEV void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// 32 lanes x 32 columns of fp32 to TMEM
+MXQ_DEV void tc_st32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+                 "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+                 "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+                 : "memory");
+}
+MXQ_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// generic-proxy writes of shared memory, also by other CTAs of the cluster,
+// before the async proxy (the tensor core's operand reads)
+MXQ_DEV void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+MXQ_DEV float4 ld_cluster_v4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+MXQ_DEV void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b)
+{
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+MXQ_DEV void st_cluster_f64(uint32_t addr, double v)
+{
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+
+// byte of column byte `b` (of 128) of row `r` in a block of 128-byte rows with
+// the 128-byte swizzle
+MXQ_DEV uint32_t swz(int r, int b) { return (uint32_t)(r * 128 + (b ^ ((r & 7) << 4))); }
+
+// Grid: E * ctas CTAs in clusters of `ctas`. g (E, rows, cols); X = G, or with
+// `tall` G^T.
+template <typename T>
+__global__ void __launch_bounds__(SM_THREADS, 1)
+    k_ns_small(const T *__restrict__ g, int rows, int cols, int ctas, int tall, int steps,
+               const __grid_constant__ Coefs co, double eps, uint16_t *__restrict__ out, int out_vec,
+               uint64_t wait_ns)
+{
+    extern __shared__ uint8_t smem_raw[];
+    SmallSmem &sm = *reinterpret_cast<SmallSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int quad = warp & 3, part = warp >> 2;
+    const int rank = (int)g2::cta_rank(), e = blockIdx.x / ctas;
+    const int m = tall ? cols : rows, n = tall ? rows : cols;
+    const int c_base = rank * SM_SLAB, ncol = min(SM_SLAB, n - c_base); // this slab's columns, at least one
+    const int m16 = (m + 15) & ~15, n16 = (ncol + 15) & ~15;
+    const int r = 32 * quad + lane;         // this thread's row of X
+    const bool active = 32 * quad < m16;    // the warp has rows that a product reads
+
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                     "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        mbar_init(&sm.bar, 1);
+        fence_mbar_init();
+    }
+    gm::tc_fence_before();
+    __syncthreads();
+    gm::tc_fence_after();
+    const uint32_t lanes = sm.tmem_base + ((uint32_t)(32 * quad) << 16);
+    const uint32_t d_x = 0, d_a = SM_SLAB, d_b = SM_SLAB + SM_M; // TMEM columns of X, A, A A
+
+    // ---- G into TMEM, its sum of squares
+    double sq = 0.0;
+    if (active) {
+        const T *p = g + (int64_t)e * rows * cols;
+#pragma unroll 1
+        for (int ch = part; 32 * ch < n16; ch += 4) {
+            uint32_t v[32];
+            float f[32];
+            const int c0 = c_base + 32 * ch;
+            if (tall) { // X(r, c) is G[c][r]: neighbouring lanes, neighbouring elements
+                const T *q = p + (int64_t)c0 * cols + r;
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    f[k] = r < m && 32 * ch + k < ncol ? in_pair(q + (int64_t)k * cols, false, false).x : 0.0f;
+            } else { // a row at a time, turned over where X and X^T will be
+                const T *q = p + (int64_t)(32 * quad) * cols + c0 + lane;
+                const bool in = 32 * ch + lane < ncol;
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    f[k] = in && 32 * quad + k < m ? in_pair(q + (int64_t)k * cols, false, false).x : 0.0f;
+                float *st = reinterpret_cast<float *>(sm.xh[0]) + warp * (32 * 33);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    st[k * 33 + lane] = f[k];
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    f[k] = st[lane * 33 + k];
+                __syncwarp();
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    s = fmaf(f[k + i], f[k + i], s);
+                if (s > 0x1p-90f && s < 0x1p120f) {
+                    sq += (double)s;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        sq = fma((double)f[k + i], (double)f[k + i], sq);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                v[k] = __float_as_uint(f[k]);
+            tc_st32(lanes + d_x + 32 * ch, v);
+        }
+        tc_wait_st();
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    if (lane == 0)
+        sm.warp_sum[warp] = sq;
+    __syncwarp();
+    g2::cluster_sync(); // every CTA of the cluster runs and has its sums
+    // rows and columns that are never written stay zero
+    for (int i = tid; i < (int)(sizeof(sm.xh) + sizeof(sm.xt) + sizeof(sm.ab)) / 16; i += SM_THREADS)
+        reinterpret_cast<uint4 *>(sm.xh)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < ctas) {
+        double s = 0.0;
+        for (int w = 0; w < SM_THREADS / 32; ++w)
+            s += sm.warp_sum[w];
+        st_cluster_f64(g2::peer_addr(&sm.sums[rank], (uint32_t)tid), s);
+    }
+    __syncwarp(); // the cluster barrier is warp-aligned
+    g2::cluster_sync();
+    if (tid == 0) {
+        double s = 0.0;
+        for (int p = 0; p < ctas; ++p)
+            s += sm.sums[p];
+        scale_factors(sqrt(s) + eps, sm.factor[0], sm.factor[1]);
+    }
+    __syncthreads();
+
+    // X of a chunk, times 2^8, to its places: hi to xh and xt
+    auto put_x = [&](int c0, const float (&x)[32]) {
+        uint32_t h[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            h[k] = pack_half2(x[2 * k], x[2 * k + 1]);
+        uint8_t *row = sm.xh[c0 >> 6];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            sts_v4(smem_u32(row) + swz(r, (c0 & 32) * 2 + 16 * q),
+                   make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]));
+        uint8_t *colp = sm.xt[r >> 6];
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            *reinterpret_cast<uint16_t *>(colp + swz(c0 + k, (r & 63) * 2)) =
+                (uint16_t)(k & 1 ? h[k >> 1] >> 16 : h[k >> 1]);
+    };
+    if (active) {
+        const float f0 = sm.factor[0], f1 = sm.factor[1], a0 = co.v[0] * SA;
+#pragma unroll 1
+        for (int ch = part; 32 * ch < n16; ch += 4) {
+            uint32_t v[32];
+            float x[32];
+            gm::tc_ld32(lanes + d_x + 32 * ch, v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                x[k] = (__uint_as_float(v[k]) * f0) * f1;
+                v[k] = __float_as_uint(a0 * x[k]);
+            }
+            put_x(32 * ch, x);
+            tc_st32(lanes + d_x + 32 * ch, v);
+        }
+        tc_wait_st();
+    }
+
+    uint32_t phase = 0;
+    // everything that the tensor core will read is written: then one thread
+    // multiplies P (128 x 16 ks) by Q^T (N rows) into TMEM column d
+    auto product = [&](uint32_t d, const uint8_t *P, const uint8_t *Q, int q_block, int N, int K, bool add) {
+        fence_proxy_async_all();
+        gm::tc_fence_before();
+        __syncthreads();
+        if (tid == 0) {
+            gm::tc_fence_after();
+            const uint32_t id = small_idesc(N);
+            for (int k = 0; k < K; k += 16) {
+                const uint64_t ad = gm::smem_desc_k128(smem_u32(P) + (k >> 6) * SM_M * 128) + 2 * ((k >> 4) & 3);
+                const uint64_t bd = gm::smem_desc_k128(smem_u32(Q) + (k >> 6) * q_block) + 2 * ((k >> 4) & 3);
+                mma_f16(sm.tmem_base + d, ad, bd, id, add || k > 0 ? 1u : 0u);
+            }
+            gm::tc_commit(&sm.bar);
+        }
+        __syncwarp();
+        mbar_wait(&sm.bar, phase, wait_ns); // a wait that runs out is in the status; no CTA leaves the cluster
+        phase ^= 1u;
+        gm::tc_fence_after();
+    };
+
+#pragma unroll 1
+    for (int s = 0; s < steps; ++s) {
+        const float cb = co.v[3 * s + 1], cc = co.v[3 * s + 2];
+        // ---- A = X X^T
+        product(d_a, sm.xh[0], sm.xh[0], SM_M * 128, m16, n16, false);
+        if (active) {
+#pragma unroll 1
+            for (int ch = part; 32 * ch < m16; ch += 4) {
+                uint32_t v[32];
+                gm::tc_ld32(lanes + d_a + 32 * ch, v);
+                if (ctas == 1) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (32 * ch + 8 * q < m16) {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                h[k] = pack_half2(__uint_as_float(v[8 * q + 2 * k]) * (SA / (SX * SX)),
+                                                  __uint_as_float(v[8 * q + 2 * k + 1]) * (SA / (SX * SX)));
+                            sts_v4(smem_u32(sm.ab[ch >> 1]) + swz(r, (ch & 1) * 64 + 16 * q),
+                                   make_uint4(h[0], h[1], h[2], h[3]));
+                        }
+                } else {
+                    // 16-byte chunks, swizzled by the row so that 32 rows'
+                    // stores fall into different banks
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        sts_v4(smem_u32(sm.part) + (uint32_t)(r * 512 + (((8 * ch + q) ^ lane) << 4)),
+                               make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+                }
+            }
+        }
+        if (ctas > 1) {
+            __syncwarp();
+            g2::cluster_sync(); // every slab's product is in its CTA's shared memory
+            const int per = (m16 + ctas - 1) / ctas, r0 = rank * per, nr = min(per, m16 - r0);
+            for (int i = tid; i < nr * 32; i += SM_THREADS) {
+                const int row = r0 + (i >> 5), ch = i & 31;
+                if (4 * ch >= m16)
+                    continue;
+                const uint32_t at = (uint32_t)(row * 512 + ((ch ^ (row & 31)) << 4));
+                float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float4 b[SM_MAX_CTAS]; // all loads in flight, then the sum in rank order
+#pragma unroll
+                for (int p = 0; p < SM_MAX_CTAS; ++p)
+                    if (p < ctas)
+                        b[p] = ld_cluster_v4(g2::peer_addr(sm.part, (uint32_t)p) + at);
+#pragma unroll
+                for (int p = 0; p < SM_MAX_CTAS; ++p)
+                    if (p < ctas)
+                        a.x += b[p].x, a.y += b[p].y, a.z += b[p].z, a.w += b[p].w;
+                constexpr float F = SA / (SX * SX);
+                const uint32_t h0 = pack_half2(a.x * F, a.y * F), h1 = pack_half2(a.z * F, a.w * F);
+                const uint32_t to = (uint32_t)((ch >> 4) * SM_M * 128) + swz(row, (ch & 15) * 8);
+                for (int p = 0; p < ctas; ++p)
+                    st_cluster_v2(g2::peer_addr(sm.ab[0], (uint32_t)p) + to, h0, h1);
+            }
+            fence_proxy_async_all();
+            __syncwarp();
+            g2::cluster_sync(); // A is whole in every CTA
+        }
+        // ---- B = b A + c A A, in A's place
+        product(d_b, sm.ab[0], sm.ab[0], SM_M * 128, m16, m16, false);
+        if (active) {
+#pragma unroll 1
+            for (int ch = part; 32 * ch < m16; ch += 4) {
+                uint32_t v[32];
+                gm::tc_ld32(lanes + d_b + 32 * ch, v);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (32 * ch + 8 * q < m16) {
+                        uint8_t *p = sm.ab[ch >> 1] + swz(r, (ch & 1) * 64 + 16 * q);
+                        const uint4 a = *reinterpret_cast<const uint4 *>(p);
+                        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+                        uint32_t h[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = unpack_half2(w[k]);
+                            h[k] = pack_half2(fmaf(cc * (1.0f / SA), __uint_as_float(v[8 * q + 2 * k]), cb * f.x),
+                                              fmaf(cc * (1.0f / SA), __uint_as_float(v[8 * q + 2 * k + 1]), cb * f.y));
+                        }
+                        *reinterpret_cast<uint4 *>(p) = make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+            }
+        }
+        // ---- X = a X + B X, added in TMEM; its columns hold a X 2^18
+        product(d_x, sm.ab[0], sm.xt[0], SM_SLAB * 128, n16, m16, true);
+        if (active) {
+            const float a_next = s + 1 < steps ? co.v[3 * (s + 1)] : 0.0f;
+#pragma unroll 1
+            for (int ch = part; 32 * ch < n16; ch += 4) {
+                uint32_t v[32];
+                float x[32];
+                gm::tc_ld32(lanes + d_x + 32 * ch, v);
+                const int c0 = 32 * ch;
+                if (s + 1 < steps) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        x[k] = __uint_as_float(v[k]) * (1.0f / SA);
+                        v[k] = __float_as_uint(a_next * __uint_as_float(v[k]));
+                    }
+                    put_x(c0, x);
+                    tc_st32(lanes + d_x + c0, v);
+                } else {
+                    uint32_t h[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        h[k] = gm::pack_bf16x2(__uint_as_float(v[2 * k]) * (1.0f / (SA * SX)),
+                                               __uint_as_float(v[2 * k + 1]) * (1.0f / (SA * SX)));
+                    uint16_t *dst = out + (int64_t)e * rows * cols;
+                    if (tall) {
+                        dst += (int64_t)(c_base + c0) * m + r;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (r < m && c0 + k < ncol)
+                                dst[(int64_t)k * m] = (uint16_t)(k & 1 ? h[k >> 1] >> 16 : h[k >> 1]);
+                    } else { // turned over where X^T was: its last product is done
+                        rows_out(sm.xt[0] + warp * CHUNK_BYTES, h, dst + (int64_t)(32 * quad) * n + c_base + c0, n,
+                                 m - 32 * quad, ncol - c0, out_vec);
+                    }
+                }
+            }
+            tc_wait_st();
+        }
+    }
+
+    __syncwarp();
+    gm::tc_fence_before();
+    g2::cluster_sync(); // no CTA's shared memory goes while another may read it
+    gm::tc_fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sm.tmem_base), "r"(512u) : "memory");
+}
+
+} // namespace ns
+} // namespace mxq

@@ -101,12 +101,14 @@ def test_host_checks():
     assert L.newton_schulz(p, 0, 1, 8, 8, 1, None, 1e-7, p, p, big, None) == mxq.ERR_NULL
     assert L.newton_schulz(None, 0, 1, 8, 8, 1, co, 1e-7, p, p, big, None) == mxq.ERR_NULL
     assert L.newton_schulz(p, 0, 1, 8, 8, 1, co, 1e-7, p + 1, p, big, None) == mxq.ERR_ALIGN
-    assert L.newton_schulz(p, 0, 1, 8, 8, 1, co, 1e-7, p, p + 16, big, None) == mxq.ERR_ALIGN
-    assert L.newton_schulz(p, 0, 1, 8, 8, 1, co, 1e-7, p, p, 100, None) == mxq.ERR_WORKSPACE
+    assert L.newton_schulz(p, 0, 1, 200, 300, 1, co, 1e-7, p, p + 16, big, None) == mxq.ERR_ALIGN
+    assert L.newton_schulz(p, 0, 1, 200, 300, 1, co, 1e-7, p, p, 100, None) == mxq.ERR_WORKSPACE
     assert L.newton_schulz(p, 0, 0, 8, 8, 1, co, 1e-7, None, None, 0, None) == mxq.OK
     assert L.newton_schulz(None, 0, 3, 0, 8, 1, co, 1e-7, None, None, 0, None) == mxq.OK
     assert L.newton_schulz_workspace_bytes(0, 8, 8, 5) == 0
-    assert L.newton_schulz_workspace_bytes(2, 8, 8, 5) > 0
+    assert L.newton_schulz_workspace_bytes(2, 128, 2048, 5) == 0
+    assert L.newton_schulz_workspace_bytes(2, 129, 2048, 5) > 0
+    assert L.newton_schulz_workspace_bytes(2, 2049, 8, 5) > 0
 
 
 def test_refusals_of_the_binding_and_fake_shape():
@@ -120,7 +122,9 @@ def test_refusals_of_the_binding_and_fake_shape():
 
 # ------------------------------------------------------------ values
 SHAPES = [(1, 1, 1), (1, 1, 9), (2, 7, 1), (3, 16, 16), (2, 33, 65), (4, 96, 224), (2, 128, 128), (1, 129, 127),
-          (2, 256, 64), (3, 300, 260), (2, 257, 520), (1, 513, 511), (5, 64, 1000), (1, 1409, 577), (2, 768, 1280)]
+          (2, 256, 64), (3, 300, 260), (2, 257, 520), (1, 513, 511), (5, 64, 1000), (1, 1409, 577), (2, 768, 1280),
+          (2, 17, 255), (3, 100, 257), (1, 128, 513), (2, 900, 30), (2, 48, 1300), (1, 2048, 128), (2, 128, 2049),
+          (40, 65, 300)]
 
 
 @pytest.mark.gpu

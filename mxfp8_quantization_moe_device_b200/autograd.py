@@ -190,65 +190,23 @@ def fp8_grouped_mm(a, w, offs):
 
 # ---------------------------------------------------------------- around the grouped products
 
-class MoERoute(torch.autograd.Function):
-    """Router with balance loss: weights and loss are differentiable in the
-    logits; ids and counts are not."""
+# Their autograd nodes are C++ (csrc_torch/moe_autograd.cpp): a call is a few
+# launches of microseconds, and a Python node would cost more than they do.
 
-    @staticmethod
-    def forward(ctx, logits, top_k, valid, renormalize):
-        loss_grad = torch.empty(logits.shape[-1:], dtype=torch.float32, device=logits.device)
-        weights, ids, counts, loss = mxq.moe_route(logits, top_k, valid=valid, renormalize=renormalize,
-                                                   loss_grad=loss_grad)
-        ctx.set_materialize_grads(False)
-        ctx.mark_non_differentiable(ids, counts)
-        ctx.save_for_backward(logits, weights, ids, loss_grad, valid)
-        ctx.renormalize = renormalize
-        return weights, ids, counts, loss
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dweights, _ids, _counts, dloss):
-        if dweights is None and dloss is None:
-            return None, None, None, None
-        logits, weights, ids, loss_grad, valid = ctx.saved_tensors
-        if dweights is not None:
-            dweights = dweights.contiguous()
-        return mxq.moe_route_backward(logits, weights, ids, loss_grad, dweights, dloss, valid=valid,
-                                      renormalize=ctx.renormalize), None, None, None
+_ops = None
 
 
-class MoEDispatch(torch.autograd.Function):
-    """Token rows in the order by expert; the gradient of a token is the sum
-    of its rows' gradients."""
-
-    @staticmethod
-    def forward(ctx, x, pos, offs):
-        ctx.save_for_backward(pos)
-        return mxq.moe_dispatch(x, pos, offs)
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dxs):
-        (pos,) = ctx.saved_tensors
-        return mxq.moe_combine(dxs.contiguous(), pos), None, None
-
-
-class MoECombine(torch.autograd.Function):
-    """Weighted sum of every token's rows, differentiable in the rows and the
-    weights."""
-
-    @staticmethod
-    def forward(ctx, y, pos, weights, offs):
-        ctx.save_for_backward(y, pos, weights, offs)
-        return mxq.moe_combine(y, pos, weights)
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dout):
-        y, pos, weights, offs = ctx.saved_tensors
-        dy, dw = mxq.moe_combine_backward(dout.contiguous(), y, pos, weights, offs, need_y=ctx.needs_input_grad[0],
-                                          need_weights=ctx.needs_input_grad[2])
-        return dy, None, dw, None
+def _torch_ops():
+    global _ops
+    if _ops is None:
+        mxq.lib()
+        try:
+            from . import _torch_ops as ops
+        except ImportError as e:
+            raise RuntimeError("_torch_ops.so is not built; build it with "
+                               "`python -m mxfp8_quantization_moe_device_b200.build`") from e
+        _ops = ops
+    return _ops
 
 
 def moe_route(logits, top_k, *, valid=None, renormalize=False):
@@ -256,7 +214,7 @@ def moe_route(logits, top_k, *, valid=None, renormalize=False):
     () fp32) of router logits (T, E) bf16 or fp32; weights and loss are
     differentiable in the logits (the counts inside the loss are constants).
     See binding.moe_route."""
-    return MoERoute.apply(logits, top_k, valid, renormalize)
+    return _torch_ops().moe_route(logits, top_k, valid, renormalize)
 
 
 def moe_dispatch(x, ids, num_experts):
@@ -264,12 +222,11 @@ def moe_dispatch(x, ids, num_experts):
     (num_experts,)), ready for fp8_grouped_mm or mx_grouped_mm; M is T * top_k
     up to a multiple of 16 and the rows behind offs[-1] are zero. Entries with
     a negative id are dropped. Differentiable in x."""
-    pos, offs = mxq.moe_dispatch_plan(ids, num_experts)
-    return MoEDispatch.apply(x, pos, offs), pos, offs
+    return _torch_ops().moe_dispatch(x, ids, num_experts)
 
 
 def moe_combine(y, pos, weights, offs):
     """out (T, K): every token's rows y[pos[t]] weighted by weights (T, top_k)
     fp32 and summed; differentiable in y and weights. pos and offs as
     moe_dispatch returned them: together they name every row of y once."""
-    return MoECombine.apply(y, pos, weights, offs)
+    return _torch_ops().moe_combine(y, pos, weights, offs)

@@ -170,7 +170,8 @@ def test_workspace_sizes():
 def test_cpu_tensors_are_refused():
     x = torch.zeros(4, 8)
     ids = torch.zeros(4, 2, dtype=torch.int32)
-    for call in (lambda: mxq.moe_route(x, 2), lambda: mxq.moe_dispatch_plan(ids, 4),
+    for call in (lambda: autograd.moe_route(x, 2), lambda: autograd.moe_dispatch(x, ids, 4),
+                 lambda: autograd.moe_combine(x, ids, x, ids[0]), lambda: mxq.moe_route(x, 2), lambda: mxq.moe_dispatch_plan(ids, 4),
                  lambda: mxq.moe_dispatch(x, ids, ids[0]), lambda: mxq.moe_combine(x, ids),
                  lambda: mxq.moe_combine_backward(x, x, ids, None, ids[0])):
         with pytest.raises(TypeError):
@@ -500,6 +501,65 @@ def test_refusals_of_the_binding():
             call()
     with pytest.raises(mxq.MXQError):
         mxq.moe_route(x, 33)
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_refusals_of_the_differentiable_calls():
+    x = torch.randn(8, 64, device=DEV).bfloat16()
+    ids = torch.zeros(8, 2, dtype=torch.int32, device=DEV)
+    xs, pos, offs = autograd.moe_dispatch(x, ids, 4)
+    w = torch.ones(8, 2, device=DEV)
+    for call in (lambda: autograd.moe_route(x.half(), 2), lambda: autograd.moe_route(x.t(), 2),
+                 lambda: autograd.moe_route(x[:1].expand(8, 64), 2), lambda: autograd.moe_route(x, 2, valid=w[:, 0]),
+                 lambda: autograd.moe_dispatch(x, ids.long(), 4), lambda: autograd.moe_dispatch(x, ids[:7], 4),
+                 lambda: autograd.moe_dispatch(x.t(), ids, 4), lambda: autograd.moe_combine(xs, pos, w.double(), offs),
+                 lambda: autograd.moe_combine(xs, pos.long(), w, offs),
+                 lambda: autograd.moe_combine(xs, pos, w, offs.cpu())):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: autograd.moe_route(x, 0), lambda: autograd.moe_route(x, 65),
+                 lambda: autograd.moe_dispatch(x, ids, 0)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(mxq.MXQError) as e:
+        autograd.moe_route(x, 33)
+    assert e.value.code == mxq.ERR_UNSUPPORTED
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_gradients_through_odd_incoming_gradients():
+    """Expanded, strided and missing incoming gradients, a leaf that wants
+    none, and a second differentiation, which is refused."""
+    T, E, k, K = 30, 8, 2, 40
+    l = torch.randn(T, E, device=DEV, requires_grad=True)
+    x = torch.randn(T, K, device=DEV, requires_grad=True)
+    w, ids, counts, loss = autograd.moe_route(l, k)
+    assert not ids.requires_grad and not counts.requires_grad and w.requires_grad and loss.requires_grad
+    xs, pos, offs = autograd.moe_dispatch(x, ids, E)
+    y = autograd.moe_combine(xs, pos, w, offs)
+    gl, gx = torch.autograd.grad(y.sum() + 2 * loss, (l, x), retain_graph=True)  # a gradient of expanded ones
+    rl, rx = torch.autograd.grad((y, loss), (l, x), (torch.ones_like(y), torch.tensor(2.0, device=DEV)),
+                                 retain_graph=True)
+    assert torch.equal(gl, rl) and torch.equal(gx, rx)
+    g = torch.randn(K, T, device=DEV).t()
+    a = torch.autograd.grad(y, (l, x), g, retain_graph=True)
+    b = torch.autograd.grad(y, (l, x), g.contiguous(), retain_graph=True)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    assert torch.autograd.grad(y, (l,), g, retain_graph=True)[0].shape == l.shape
+    const = autograd.moe_combine(xs.detach(), pos, w.detach(), offs)
+    assert not const.requires_grad
+    only = autograd.moe_combine(xs.detach(), pos, w, offs)
+    torch.autograd.grad(only.sum(), (l,), retain_graph=True)
+    (first,) = torch.autograd.grad(y.sum(), (x,), create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiated again"):
+        first.sum().backward(retain_graph=True)
+    with pytest.raises(RuntimeError):  # the graph ends there, as with torch's once_differentiable
+        torch.autograd.grad(first.sum(), (x,))
+    (first,) = torch.autograd.grad(loss, (l,), create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiated again"):
+        first.square().sum().backward()
     assert mxq.device_status() == 0
 
 

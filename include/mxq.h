@@ -535,9 +535,11 @@ int moe_combine_backward(const void *grad_out, int64_t grad_row_stride, const vo
  * sums on X held in 22 bits; singular values should stay below 4 on the way
  * (they do for the usual coefficients) and coefficients within [-16, 16]. A
  * matrix of zeros gives zeros; a NaN or infinity makes its own matrix NaN and
- * no other. rows, cols <= 65536, batch <= 65535, steps <= 64. workspace:
- * newton_schulz_workspace_bytes() bytes (NULL when 0), 256-byte aligned, not
- * shared by calls that overlap on the GPU.
+ * no other. rows, cols <= 65536 and a matrix below 2^31 elements, batch <=
+ * 65535, steps <= 64. workspace:
+ * newton_schulz_workspace_bytes() bytes (NULL when 0; asked for with the
+ * device of the call current), 256-byte aligned, not shared by calls that
+ * overlap on the GPU.
  * ------------------------------------------------------------------------ */
 size_t newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, int32_t steps);
 int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols, int32_t steps,

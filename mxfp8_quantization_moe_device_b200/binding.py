@@ -786,7 +786,7 @@ def newton_schulz(g, *, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-
     dev = g.device
     E, N, K = g.shape if g.dim() == 3 else (1, *g.shape)
     out = _output(out, "out", torch.bfloat16, g.shape, dev)
-    ws = _workspace(lib().newton_schulz_workspace_bytes(E, N, K, steps), dev)
+    ws = _workspace(_sized("newton_schulz_workspace_bytes", dev, E, N, K, steps), dev)
     _call("newton_schulz", dev, _ptr(g), _DTYPES[g.dtype], E, N, K, steps, co, float(eps), _ptr(out), _ptr(ws),
           ws.numel() if ws is not None else 0)
     return out

@@ -109,6 +109,11 @@ template <int TN> MXQ_DEV void mma_pair_f16(uint32_t d_tmem, uint64_t adesc, uin
                  : "memory");
 }
 
+MXQ_DEV void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 MXQ_DEV uint32_t pack_half2(float lo, float hi)
 {
     uint32_t r;
@@ -380,6 +385,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     let_next_kernel_start();
     if (threadIdx.x == 0) {
+        prefetch_map(&tm_p);
+        prefetch_map(&tm_q);
+        if (MODE != LAST)
+            prefetch_map(&tm_o);
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&sm.full[s], 1);
             mbar_init(&sm.ready[s], 2);
@@ -534,23 +543,36 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int r = r0 + lane;
             const bool row_ok = r < q.m;
             const int cols = SYM ? q.m : q.n;
-            // this lane's column-wise position: element c of the row is at
-            // at + c * ldt in X^T, lo, A and B alike
-            const int64_t at = (int64_t)w.e * cols * q.ldt + r;
+            // this lane's column-wise position: element c of the row is `at` + c
+            // ldt elements into its matrix of X^T, lo, A and B alike (a matrix
+            // has less than 2^31 elements, so 32 bits hold its byte offsets)
+            const int64_t plane = (int64_t)w.e * cols * q.ldt;
+            const uint32_t at = (uint32_t)r, ldb = (uint32_t)q.ldt * 2u;
+            const bool rows_full = r0 + 32 <= q.m; // the same in every lane
             // what the chunk adds to the product: X (hi and lo), or A
             uint16_t old_h[CHUNK], old_l[MODE == POLY ? 1 : CHUNK];
+            const uint8_t *old_hi = reinterpret_cast<const uint8_t *>((MODE == POLY ? q.A : q.xt0) + plane);
+            uint8_t *old_lo = reinterpret_cast<uint8_t *>(q.lo + plane);
             auto load_old = [&](int c0) {
-                const int64_t o = at + (int64_t)c0 * q.ldt;
-                const uint16_t *ph = (MODE == POLY ? q.A : q.xt0) + o, *pl = q.lo + o;
+                uint32_t o = (uint32_t)c0 * ldb + at * 2u;
+                if (rows_full && c0 + CHUNK <= cols) {
 #pragma unroll
-                for (int k = 0; k < CHUNK; ++k, ph += q.ldt, pl += q.ldt) {
-                    const bool in = row_ok && c0 + k < cols;
-                    old_h[k] = in ? *ph : (uint16_t)0;
-                    if constexpr (MODE != POLY)
-                        old_l[k] = in ? *pl : (uint16_t)0;
+                    for (int k = 0; k < CHUNK; ++k, o += ldb) {
+                        old_h[k] = *reinterpret_cast<const uint16_t *>(old_hi + o);
+                        if constexpr (MODE != POLY)
+                            old_l[k] = *reinterpret_cast<const uint16_t *>(old_lo + o);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < CHUNK; ++k, o += ldb) {
+                        const bool in = row_ok && c0 + k < cols;
+                        old_h[k] = in ? *reinterpret_cast<const uint16_t *>(old_hi + o) : (uint16_t)0;
+                        if constexpr (MODE != POLY)
+                            old_l[k] = in ? *reinterpret_cast<const uint16_t *>(old_lo + o) : (uint16_t)0;
+                    }
                 }
             };
-            if constexpr (MODE == STEP || MODE == LAST)
+            if constexpr (MODE != GRAM)
                 load_old(w.j * TN + CHUNK * part); // in flight while the product finishes
             bool ok = mbar_wait(&sm.acc_full[acc], (uint32_t)(t / ACC) & 1u, wait_ns);
             ok = __all_sync(0xffffffffu, ok);
@@ -564,8 +586,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int c0 = w.j * TN + CHUNK * ch;
                 if (c0 >= cols)
                     break; // the same in every lane
-                if constexpr (MODE == POLY) // held only within the chunk: no registers for the next one's
-                    load_old(c0);
                 uint32_t d[CHUNK];
                 gm::tc_ld32(tmem + (uint32_t)(acc * TN + CHUNK * ch) + ((uint32_t)(32 * quad) << 16), d);
                 uint32_t h[CHUNK / 2], l[CHUNK / 2]; // pairs of the row, high and low words
@@ -596,23 +616,33 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 }
-                if constexpr (MODE == STEP || MODE == LAST) {
+                if constexpr (MODE != GRAM) {
                     if (ch + 2 < TN / CHUNK && c0 + 2 * CHUNK < cols)
                         load_old(c0 + 2 * CHUNK);
                 }
                 // down the columns
                 if (MODE != LAST || q.out_t) {
-                    const int64_t ld = MODE == LAST ? q.m : q.ldt;
-                    const int64_t o = (MODE == LAST ? (int64_t)w.e * cols * q.m + r : at) + c0 * ld;
-                    uint16_t *dst = (MODE == GRAM ? q.A : MODE == POLY ? q.B : MODE == STEP ? q.xt : q.out) + o;
-                    uint16_t *dst_l = q.lo + o;
+                    const uint32_t ld2 = MODE == LAST ? (uint32_t)q.m * 2u : ldb;
+                    uint32_t o = (uint32_t)c0 * ld2 + at * 2u;
+                    uint8_t *dst = MODE == LAST
+                                       ? reinterpret_cast<uint8_t *>(q.out + (int64_t)w.e * cols * q.m)
+                                       : reinterpret_cast<uint8_t *>((MODE == GRAM ? q.A : MODE == POLY ? q.B : q.xt) + plane);
+                    auto put = [&](int k) {
+                        *reinterpret_cast<uint16_t *>(dst + o) = (uint16_t)(k & 1 ? h[k >> 1] >> 16 : h[k >> 1]);
+                        if constexpr (MODE == STEP)
+                            *reinterpret_cast<uint16_t *>(old_lo + o) =
+                                (uint16_t)(k & 1 ? l[k >> 1] >> 16 : l[k >> 1]);
+                    };
+                    if (rows_full && c0 + CHUNK <= cols) {
 #pragma unroll
-                    for (int k = 0; k < CHUNK; ++k, dst += ld, dst_l += ld)
-                        if (row_ok && c0 + k < cols) {
-                            *dst = (uint16_t)(k & 1 ? h[k >> 1] >> 16 : h[k >> 1]);
-                            if constexpr (MODE == STEP)
-                                *dst_l = (uint16_t)(k & 1 ? l[k >> 1] >> 16 : l[k >> 1]);
-                        }
+                        for (int k = 0; k < CHUNK; ++k, o += ld2)
+                            put(k);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < CHUNK; ++k, o += ld2)
+                            if (row_ok && c0 + k < cols)
+                                put(k);
+                    }
                 }
                 // along the rows, through shared memory
                 const bool rows_too = MODE == LAST ? !q.out_t : !(SYM && w.j >= w.i * RATIO);
@@ -648,7 +678,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
         if (MODE != LAST && lane == 0)
-            bulk_wait<0>(); // the stores have left shared memory and are complete
+            bulk_wait_read<0>(); // the stores have left shared memory; the kernel's end completes them
     }
 
     __syncwarp(); // the cluster barrier below is warp-aligned

@@ -42,6 +42,9 @@ int ns_check(int64_t E, int64_t rows, int64_t cols, int32_t steps)
         return MXQ_ERR_SHAPE;
     if (E > 65535 || rows > 65536 || cols > 65536 || steps > 64)
         return MXQ_ERR_UNSUPPORTED;
+    // the kernels address a matrix with 32-bit byte offsets
+    if (std::max(rows, cols) * ((std::min(rows, cols) + 7) / 8 * 8) >= (int64_t(1) << 31))
+        return MXQ_ERR_UNSUPPORTED;
     return MXQ_OK;
 }
 
@@ -101,10 +104,18 @@ int ns_launch(const NsOperand &p, const NsOperand &q, const NsOperand &o, const 
                           stream, true, mp, mq, mo, a, (int)((p.inner + ns::BK - 1) / ns::BK), wait_ns());
 }
 
-// Tile width: a 256 x 128 tile takes 0.72 of a 256 x 256 tile's time (12.1 ms
-// against 8.4 for twice as many at (16, 2048, 7168)), so it is used where it
-// needs fewer than 1 / 0.72 as many rounds over the pairs: 269 us against 315
-// at (5, 1409, 577).
+// Tile width, by estimated time in units of one 64-column block of a 256 x 256
+// tile (about 0.4 us): a 256 x 128 tile's block takes about 0.8 of that (12.1
+// ms against 7.7 for all tiles of (16, 2048, 7168), twice as many); draining a
+// tile takes about 14 and 7, hidden under the next tile's blocks but for the
+// last round. The narrow tile wins where it spreads the work over more pairs or
+// where draining bounds: 243 us against 272 at (5, 1409, 577), 113 against 144
+// at (4, 256, 256); the wide one at 946 against 1112 at (8, 1024, 4096).
+int64_t ns_estimate(int64_t tiles, int64_t pairs, int64_t blocks100, int64_t drain100)
+{
+    return (tiles + pairs - 1) / pairs * std::max(blocks100, drain100) + drain100;
+}
+
 template <int MODE>
 int ns_product(const NsOperand &p, const NsOperand &q, const NsOperand &o, const ns::Args &a, cudaStream_t stream)
 {
@@ -112,10 +123,11 @@ int ns_product(const NsOperand &p, const NsOperand &q, const NsOperand &o, const
     int wide = 0, narrow = 0, rc;
     if ((rc = ns_pairs<MODE, 256>(&wide)) != MXQ_OK || (rc = ns_pairs<MODE, 128>(&narrow)) != MXQ_OK)
         return rc;
-    const int64_t rounds_w = (a.E * ns::sym_or_all_tiles<sym, 256>(a.m, a.n) + wide - 1) / wide;
-    const int64_t rounds_n = (a.E * ns::sym_or_all_tiles<sym, 128>(a.m, a.n) + narrow - 1) / narrow;
+    const int64_t blocks = (p.inner + ns::BK - 1) / ns::BK;
+    const int64_t t_wide = ns_estimate(a.E * ns::sym_or_all_tiles<sym, 256>(a.m, a.n), wide, 100 * blocks, 1400);
+    const int64_t t_narrow = ns_estimate(a.E * ns::sym_or_all_tiles<sym, 128>(a.m, a.n), narrow, 80 * blocks, 700);
     const int force = g_ns_tile.load();
-    if (force == 128 || (force == 0 && 18 * rounds_n < 25 * rounds_w))
+    if (force == 128 || (force == 0 && t_narrow < t_wide))
         return ns_launch<MODE, 128>(p, q, o, a, narrow, stream);
     return ns_launch<MODE, 256>(p, q, o, a, wide, stream);
 }
@@ -136,36 +148,88 @@ int ns_start(const T *g, int64_t E, int64_t rows, int64_t cols, const NsPlan &p,
                   reinterpret_cast<uint16_t *>(ws + p.xt[0]), reinterpret_cast<uint16_t *>(ws + p.lo), (int)p.ldt);
 }
 
-// one launch for all steps: the smaller side fits a tile, the larger a cluster
+// a launch of k_ns_small with `ctas` CTAs per matrix
+void ns_small_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int64_t E, int ctas, cudaStream_t stream)
+{
+    cfg->gridDim = dim3((unsigned)(E * ctas));
+    cfg->blockDim = dim3(ns::SM_THREADS);
+    cfg->dynamicSmemBytes = ns::small_smem_bytes(ctas > 1);
+    cfg->stream = stream;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = (unsigned)ctas;
+    attr->val.clusterDim.y = 1;
+    attr->val.clusterDim.z = 1;
+    cfg->attrs = attr;
+    cfg->numAttrs = 1;
+}
+
+template <typename T> int ns_small_attributes()
+{
+    static std::atomic<uint64_t> set[2];
+    int d = 0;
+    if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= 128)
+        return MXQ_ERR_CUDA;
+    if (set[d >> 6].load(std::memory_order_acquire) >> (d & 63) & 1)
+        return MXQ_OK;
+    if (cudaFuncSetAttribute(ns::k_ns_small<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)ns::small_smem_bytes(true)) != cudaSuccess ||
+        cudaFuncSetAttribute(ns::k_ns_small<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return MXQ_ERR_CUDA;
+    }
+    set[d >> 6].fetch_or(uint64_t(1) << (d & 63), std::memory_order_release);
+    return MXQ_OK;
+}
+
+// whether the current device runs clusters of SM_MAX_CTAS CTAs of k_ns_small
+bool ns_large_clusters()
+{
+    static std::atomic<int> known[128]; // 0 unknown, 1 no, 2 yes
+    int d = 0;
+    if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= 128) {
+        (void)cudaGetLastError();
+        return false;
+    }
+    int k = known[d].load(std::memory_order_relaxed);
+    if (k == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        int n = 0, m = 0;
+        ns_small_config(&cfg, attr, 1, ns::SM_MAX_CTAS, nullptr);
+        const bool yes = ns_small_attributes<uint16_t>() == MXQ_OK && ns_small_attributes<float>() == MXQ_OK &&
+                         cudaOccupancyMaxActiveClusters(&n, ns::k_ns_small<uint16_t>, &cfg) == cudaSuccess &&
+                         cudaOccupancyMaxActiveClusters(&m, ns::k_ns_small<float>, &cfg) == cudaSuccess && n > 0 &&
+                         m > 0;
+        (void)cudaGetLastError();
+        k = yes ? 2 : 1;
+        known[d].store(k, std::memory_order_relaxed);
+    }
+    return k == 2;
+}
+
+// One launch for all steps: the smaller side fits a tile, the larger one a
+// cluster, of eight CTAs (any device) or sixteen: 245 us by the general
+// kernels at (3, 90, 4000).
 bool ns_is_small(int64_t rows, int64_t cols)
 {
+    const int64_t ctas = (std::max(rows, cols) + ns::SM_SLAB - 1) / ns::SM_SLAB;
     return g_ns_tile.load() == 0 && std::min(rows, cols) <= ns::SM_M &&
-           std::max(rows, cols) <= ns::SM_SLAB * ns::SM_MAX_CTAS;
+           (ctas <= 8 || (ctas <= ns::SM_MAX_CTAS && ns_large_clusters()));
 }
 
 template <typename T>
 int ns_small(const T *g, int64_t E, int64_t rows, int64_t cols, int32_t steps, const float *coefficients, double eps,
              uint16_t *out, cudaStream_t stream)
 {
-    static std::atomic<uint64_t> set[2];
-    const int rc = allow_smem(ns::k_ns_small<T>, (int)ns::small_smem_bytes(true), set);
+    const int rc = ns_small_attributes<T>();
     if (rc != MXQ_OK)
         return rc;
     ns::Coefs co;
     std::memcpy(co.v, coefficients, sizeof(float) * 3 * (size_t)steps);
     const int ctas = (int)((std::max(rows, cols) + ns::SM_SLAB - 1) / ns::SM_SLAB);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(E * ctas));
-    cfg.blockDim = dim3(ns::SM_THREADS);
-    cfg.dynamicSmemBytes = ns::small_smem_bytes(ctas > 1);
-    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    ns_small_config(&cfg, attr, E, ctas, stream);
     if (cudaLaunchKernelEx(&cfg, ns::k_ns_small<T>, g, (int)rows, (int)cols, ctas, (int)(rows > cols), (int)steps, co,
                            eps, out, (int)(cols % 8 == 0 && aligned(out, 16)), wait_ns()) != cudaSuccess) {
         (void)cudaGetLastError();

@@ -5,7 +5,7 @@
 // X^T as fp16 in shared memory in the layout that tcgen05.mma reads, X itself
 // in fp32 in TMEM, as the accumulator of the step's last product: a X is
 // written there and B X added to it by the tensor core, so X is never rounded.
-// A matrix with more columns takes a cluster of up to eight CTAs: each
+// A matrix with more columns takes a cluster of up to sixteen CTAs: each
 // multiplies its slab with itself, the partial 128 x 128 products are summed
 // over distributed shared memory in rank order (every CTA sums some rows and
 // sends them to all), and the rest is local to the slab.
@@ -26,7 +26,7 @@ namespace ns {
 
 constexpr int SM_M = 128;              // rows of X, at most
 constexpr int SM_SLAB = 256;           // columns of X per CTA
-constexpr int SM_MAX_CTAS = 8;         // CTAs per matrix
+constexpr int SM_MAX_CTAS = 16;        // CTAs per matrix; more than 8 where the device has such clusters
 constexpr int SM_THREADS = 512;        // four warps per 32 rows, a quarter of the columns each
 constexpr int MAX_STEPS = 64;
 
@@ -315,15 +315,17 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                     continue;
                 const uint32_t at = (uint32_t)(row * 512 + ((ch ^ (row & 31)) << 4));
                 float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                float4 b[SM_MAX_CTAS]; // all loads in flight, then the sum in rank order
+                for (int p0 = 0; p0 < ctas; p0 += 8) { // eight loads in flight, then their sum in rank order
+                    float4 b[8];
 #pragma unroll
-                for (int p = 0; p < SM_MAX_CTAS; ++p)
-                    if (p < ctas)
-                        b[p] = ld_cluster_v4(g2::peer_addr(sm.part, (uint32_t)p) + at);
+                    for (int p = 0; p < 8; ++p)
+                        if (p0 + p < ctas)
+                            b[p] = ld_cluster_v4(g2::peer_addr(sm.part, (uint32_t)(p0 + p)) + at);
 #pragma unroll
-                for (int p = 0; p < SM_MAX_CTAS; ++p)
-                    if (p < ctas)
-                        a.x += b[p].x, a.y += b[p].y, a.z += b[p].z, a.w += b[p].w;
+                    for (int p = 0; p < 8; ++p)
+                        if (p0 + p < ctas)
+                            a.x += b[p].x, a.y += b[p].y, a.z += b[p].z, a.w += b[p].w;
+                }
                 constexpr float F = SA / (SX * SX);
                 const uint32_t h0 = pack_half2(a.x * F, a.y * F), h1 = pack_half2(a.z * F, a.w * F);
                 const uint32_t to = (uint32_t)((ch >> 4) * SM_M * 128) + swz(row, (ch & 15) * 8);

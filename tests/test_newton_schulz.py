@@ -108,7 +108,7 @@ def test_host_checks():
     assert L.newton_schulz_workspace_bytes(0, 8, 8, 5) == 0
     assert L.newton_schulz_workspace_bytes(2, 128, 2048, 5) == 0
     assert L.newton_schulz_workspace_bytes(2, 129, 2048, 5) > 0
-    assert L.newton_schulz_workspace_bytes(2, 2049, 8, 5) > 0
+    assert L.newton_schulz_workspace_bytes(2, 4097, 8, 5) > 0
 
 
 def test_refusals_of_the_binding_and_fake_shape():
@@ -124,7 +124,7 @@ def test_refusals_of_the_binding_and_fake_shape():
 SHAPES = [(1, 1, 1), (1, 1, 9), (2, 7, 1), (3, 16, 16), (2, 33, 65), (4, 96, 224), (2, 128, 128), (1, 129, 127),
           (2, 256, 64), (3, 300, 260), (2, 257, 520), (1, 513, 511), (5, 64, 1000), (1, 1409, 577), (2, 768, 1280),
           (2, 17, 255), (3, 100, 257), (1, 128, 513), (2, 900, 30), (2, 48, 1300), (1, 2048, 128), (2, 128, 2049),
-          (40, 65, 300)]
+          (40, 65, 300), (3, 90, 4000), (1, 4096, 128), (1, 20, 4097)]
 
 
 @pytest.mark.gpu

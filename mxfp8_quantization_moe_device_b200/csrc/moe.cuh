@@ -150,26 +150,67 @@ template <typename T, int EPL> struct Raw {
     }
 };
 
-// p of a token from its logits v and their largest m, both in the token's
-// lanes: v becomes p. A row of -inf alone has p = 0; a row with a NaN or +inf
-// has p = NaN (m - m is NaN there) and returns true. base: what was taken off
-// the logits. exp by ex2.approx of x log2(e): off by (2 + 1.2 |x|) ulp, that is
-// least where p is largest.
-template <int LPT, int EPL> MXQ_DEV bool softmax(float (&v)[EPL], float m, float &base, float &rz)
+// 2^x by ex2.approx (2 ulp)
+MXQ_DEV float exp2_fast(float x)
 {
-    base = m == -INFINITY ? 0.0f : m;
-    float z = 0.0f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        v[i] = __expf(v[i] - base);
-        z += v[i];
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float LOG2E = 1.4426950408889634f;
+
+// exp(v - m) as 2^(v log2(e) - c) with c = m log2(e): one instruction to the
+// exponent, and c's own rounding is a factor of all of a token's values, which
+// cancels. Where |m| is so large (2^20) that this factor is no small one, all
+// tokens of the warp take 2^((v - m) log2(e)).
+struct Shift {
+    float m, c;
+    bool far; // the same in every lane of the warp
+
+    MXQ_DEV explicit Shift(float largest)
+    {
+        m = largest == -INFINITY ? 0.0f : largest;
+        c = m * LOG2E;
+        far = __any_sync(0xffffffffu, fabsf(m) > 0x1p20f);
     }
-    z = group_sum<LPT>(z);
-    rz = z == 0.0f ? 0.0f : __fdiv_rn(1.0f, z);
+    MXQ_DEV float exp(float v) const { return exp2_fast(far ? (v - m) * LOG2E : fmaf(v, LOG2E, -c)); }
+};
+
+// a token's logits in its lanes become exp(v - m), rz the reciprocal of their
+// sum. A row of -inf alone gives zeros and rz 0; a row with a NaN or +inf gives
+// rz NaN (m - m is NaN there) and returns true.
+template <int LPT, int EPL> MXQ_DEV bool exponentials(float (&v)[EPL], const Shift &shift, float &rz)
+{
+    float z = 0.0f;
+    if (shift.far) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            v[i] = exp2_fast((v[i] - shift.m) * LOG2E);
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            v[i] = exp2_fast(fmaf(v[i], LOG2E, -shift.c));
+    }
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-        v[i] *= rz;
+        z += v[i];
+    z = group_sum<LPT>(z);
+    rz = z == 0.0f ? 0.0f : __fdiv_rn(1.0f, z);
     return !(z == z);
+}
+
+// selection keys of a pair of bf16 logits (x low, y high): the order of the
+// value above, the complement of the expert's index below. -0 becomes +0 by
+// adding zero; a negative value's bits are all turned over, a positive one's
+// sign is set.
+MXQ_DEV void pair_keys(uint32_t w, uint32_t code, uint32_t &x, uint32_t &y)
+{
+    uint32_t z;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(z) : "r"(w), "r"(0x3F803F80u), "r"(0u)); // w * 1 + 0
+    const uint32_t neg = ((z >> 15) & 0x00010001u) * 0xFFFFu;
+    const uint32_t k = z ^ (neg | 0x80008000u);
+    x = __byte_perm(k, code, 0x1054);     // key of the low half over code
+    y = __byte_perm(k, code - 1, 0x3254); // of the high half over the next index's
 }
 
 // Batcher's odd-even merge sort of N registers, descending: sort both halves,
@@ -200,8 +241,11 @@ template <int LO, int N, int S, typename K> MXQ_DEV void sort_descending(K (&c)[
     }
 }
 
-constexpr int ROUTE_THREADS = 256;
+constexpr int ROUTE_THREADS = 512;
 constexpr int ROUTE_WARPS = ROUTE_THREADS / 32;
+constexpr int ROUTE_BWD_THREADS = 256;
+constexpr int ROUTE_BWD_WARPS = ROUTE_BWD_THREADS / 32;
+constexpr int ROUTE_ROWS = 8;          // warps' sums of p side by side in shared memory
 
 // slots that a lane keeps: slot j of a token sits in its lane j % LPT
 template <int LPT, int EPL> constexpr int lane_slots() { return (LPT * EPL < MAX_K ? LPT * EPL : MAX_K) / LPT; }
@@ -240,11 +284,12 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
     using Key = std::conditional_t<sizeof(T) == 2, uint32_t, uint64_t>;
     constexpr int TPW = 32 / LPT, SLOTS = lane_slots<LPT, EPL>();
     constexpr uint32_t FIRST = 0x00800000u; // keys below belong to -inf
+    constexpr int STEP = LPT < 8 ? LPT : 8;  // rounds unrolled
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sub = lane / LPT, li = lane % LPT, e0 = li * EPL;
-    float *s_p = reinterpret_cast<float *>(smem);                      // (warps, E)
-    int *s_c = reinterpret_cast<int *>(s_p + (size_t)ROUTE_WARPS * E); // E
+    float *s_p = reinterpret_cast<float *>(smem);                     // (ROUTE_ROWS, E)
+    int *s_c = reinterpret_cast<int *>(s_p + (size_t)ROUTE_ROWS * E); // E
     __shared__ int s_n;
     let_next_kernel_start();
     for (int e = tid; e < E; e += ROUTE_THREADS)
@@ -260,21 +305,25 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
     int nvalid = 0;
     const int64_t step = (int64_t)gridDim.x * ROUTE_WARPS * TPW;
     int64_t t = ((int64_t)blockIdx.x * ROUTE_WARPS + warp) * TPW + sub; // this lane's token
+    const T *row = logits + t * ld;
+    float *w_out = weights + t * k + li;
+    int32_t *id_out = ids + t * k + li;
     Raw<T, EPL> next;
     bool next_live = false;
-    auto fetch = [&](int64_t at) {
+    auto fetch = [&](int64_t at, const T *p) {
         next.none();
         next_live = false;
         if (at < tokens) {
-            next.load(logits + at * ld, e0, E, vec);
+            next.load(p, e0, E, vec);
             next_live = !valid || valid[at] != 0;
         }
     };
-    fetch(t);
-    for (; t - sub < tokens; t += step) {
+    fetch(t, row);
+    for (; t - sub < tokens; t += step, w_out += step * k, id_out += step * k) {
         Raw<T, EPL> raw = next;
         const bool live = next_live;
-        fetch(t + step);
+        row += step * ld;
+        fetch(t + step, row);
         if (!live)
             raw.none();
         float v[EPL];
@@ -282,11 +331,10 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             v[i] = raw.get(i);
-            const uint32_t key = order_key(v[i] + 0.0f);
-            if constexpr (sizeof(T) == 2)
-                c[i] = (key & 0xFFFF0000u) | (0xFFFFu - (uint32_t)(e0 + i));
-            else
-                c[i] = ((uint64_t)key << 32) | (uint32_t)~(e0 + i);
+            if constexpr (sizeof(T) == 4)
+                c[i] = ((uint64_t)order_key(v[i] + 0.0f) << 32) | (uint32_t)~(e0 + i);
+            else if (i & 1)
+                pair_keys(raw.w[i >> 1], 0xFFFFu - (uint32_t)(e0 + i - 1), c[i - 1], c[i]);
         }
         sort_descending<0, EPL>(c);
         uint32_t top; // the token's largest key, without the index
@@ -296,11 +344,12 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
         } else {
             top = group_max<LPT>((uint32_t)(c[0] >> 32));
         }
-        float base, rz;
-        const bool bad = softmax<LPT, EPL>(v, key_value(top), base, rz);
+        const Shift shift(key_value(top));
+        float rz;
+        const bool bad = exponentials<LPT, EPL>(v, shift, rz);
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            acc[i] += v[i];
+            acc[i] = fmaf(v[i], rz, acc[i]);
         nvalid += live && li == 0;
 
         uint32_t best[SLOTS], who[SLOTS]; // this lane's slots: key and, for 32-bit logits, expert
@@ -309,33 +358,33 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
             best[s] = 0u;
             who[s] = 0u;
 #pragma unroll 1
-            for (int jj = 0; jj < LPT; ++jj) {
-                if (s * LPT + jj >= k)
-                    break;
-                bool pop;
-                if constexpr (sizeof(T) == 2) {
-                    const uint32_t g = group_max<LPT>(c[0]);
-                    best[s] = li == jj ? g : best[s];
-                    pop = c[0] == g;
-                } else {
-                    // the first lane with the largest key: its experts come first
-                    const uint32_t head = (uint32_t)(c[0] >> 32);
-                    const uint32_t g = group_max<LPT>(head);
-                    const uint32_t group = LPT == 32 ? 0xffffffffu : ((1u << (LPT & 31)) - 1u) << (lane & ~(LPT - 1));
-                    const uint32_t eq = __ballot_sync(0xffffffffu, head == g) & group;
-                    const int src = __ffs(eq) - 1; // a lane of this token holds its maximum
-                    const uint32_t e = __shfl_sync(0xffffffffu, ~(uint32_t)c[0], src);
-                    best[s] = li == jj ? g : best[s];
-                    who[s] = li == jj ? e : who[s];
-                    pop = lane == src;
-                }
-                if (pop) {
+            for (int j0 = 0; j0 < LPT && s * LPT + j0 < k; j0 += STEP)
 #pragma unroll
-                    for (int i = 0; i + 1 < EPL; ++i)
-                        c[i] = c[i + 1];
-                    c[EPL - 1] = 0;
+                for (int jj = j0; jj < j0 + STEP; ++jj) {
+                    if (s * LPT + jj >= k)
+                        break;
+                    bool pop;
+                    if constexpr (sizeof(T) == 2) {
+                        const uint32_t g = group_max<LPT>(c[0]);
+                        best[s] = li == jj ? g : best[s];
+                        pop = c[0] == g;
+                    } else {
+                        // the first lane with the largest key: its experts come first
+                        const uint32_t head = (uint32_t)(c[0] >> 32);
+                        const uint32_t g = group_max<LPT>(head);
+                        const uint32_t group = LPT == 32 ? 0xffffffffu : ((1u << (LPT & 31)) - 1u) << (lane & ~(LPT - 1));
+                        const uint32_t eq = __ballot_sync(0xffffffffu, head == g) & group;
+                        const int src = __ffs(eq) - 1; // a lane of this token holds its maximum
+                        const uint32_t e = __shfl_sync(0xffffffffu, ~(uint32_t)c[0], src);
+                        best[s] = li == jj ? g : best[s];
+                        who[s] = li == jj ? e : who[s];
+                        pop = lane == src;
+                    }
+#pragma unroll
+                    for (int i = 0; i + 1 < EPL; ++i) // by select: some lane always pops
+                        c[i] = pop ? c[i + 1] : c[i];
+                    c[EPL - 1] = pop ? 0 : c[EPL - 1];
                 }
-            }
         }
         float w[SLOTS], sum = 0.0f;
         int id[SLOTS];
@@ -345,7 +394,7 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
             const bool got = !bad && g >= FIRST;
             const uint32_t key = sizeof(T) == 4 ? g : (g & 0x80000000u ? g & 0xFFFF0000u : g | 0xFFFFu);
             id[s] = !got ? -1 : (sizeof(T) == 2 ? (int)(0xFFFFu - (g & 0xFFFFu)) : (int)who[s]);
-            w[s] = got ? __expf(key_value(key) - base) : 0.0f;
+            w[s] = got ? shift.exp(key_value(key)) : 0.0f;
             sum += w[s];
         }
         float scale = rz;
@@ -353,12 +402,13 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
             sum = group_sum<LPT>(sum);
             scale = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
         }
+        if (bad)
+            scale = NAN;
 #pragma unroll
         for (int s = 0; s < SLOTS; ++s) {
-            const int j = s * LPT + li;
-            if (j < k && t < tokens) {
-                ids[t * k + j] = id[s];
-                weights[t * k + j] = bad ? NAN : w[s] * scale;
+            if (s * LPT + li < k && t < tokens) {
+                id_out[s * LPT] = id[s];
+                w_out[s * LPT] = w[s] * scale;
                 if (id[s] >= 0)
                     atomicAdd(&s_c[id[s]], 1);
             }
@@ -370,9 +420,14 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
 #pragma unroll
         for (int o = LPT; o < 32; o <<= 1)
             acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-        if (sub == 0 && e0 + i < E)
+        if (warp < ROUTE_ROWS && sub == 0 && e0 + i < E)
             s_p[(size_t)warp * E + e0 + i] = acc[i];
     }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        if (warp >= ROUTE_ROWS && sub == 0 && e0 + i < E)
+            s_p[(size_t)(warp - ROUTE_ROWS) * E + e0 + i] += acc[i];
     for (int o = 16; o; o >>= 1)
         nvalid += __shfl_xor_sync(0xffffffffu, nvalid, o);
     if (lane == 0)
@@ -381,7 +436,7 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
     for (int e = tid; e < E; e += ROUTE_THREADS) {
         float p = 0.0f;
 #pragma unroll
-        for (int w = 0; w < ROUTE_WARPS; ++w)
+        for (int w = 0; w < ROUTE_ROWS; ++w)
             p += s_p[(size_t)w * E + e];
         s_p[e] = p; // row 0, which this thread alone reads from here on
         part.p[(size_t)blockIdx.x * E + e] = p;
@@ -494,7 +549,7 @@ __global__ void __launch_bounds__(1024)
 //   dl_e = p_e (b_e - sum p b) + { w_j g_j where e = id_j, - p_e G    plain
 //                                { w_j (g_j - G) where e = id_j       renormalized
 template <typename T, int LPT, int EPL>
-__global__ void __launch_bounds__(moe::ROUTE_THREADS)
+__global__ void __launch_bounds__(moe::ROUTE_BWD_THREADS)
     k_moe_route_bwd(const T *__restrict__ logits, int64_t tokens, int E, int64_t ld, const uint8_t *__restrict__ valid,
                     int k, int renorm, int vec, const float *__restrict__ weights, const int32_t *__restrict__ ids,
                     const float *__restrict__ loss_grad, const float *__restrict__ gw, const float *__restrict__ gl,
@@ -513,31 +568,33 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
         b[i] = gl && e0 + i < E ? g_loss * loss_grad[e0 + i] : 0.0f;
-    const int64_t step = (int64_t)gridDim.x * ROUTE_WARPS * TPW;
-    int64_t t = ((int64_t)blockIdx.x * ROUTE_WARPS + warp) * TPW + sub;
+    const int64_t step = (int64_t)gridDim.x * ROUTE_BWD_WARPS * TPW;
+    int64_t t = ((int64_t)blockIdx.x * ROUTE_BWD_WARPS + warp) * TPW + sub;
     Raw<T, EPL> next;
     bool next_live = false;
     int next_id[SLOTS];
     float next_w[SLOTS], next_g[SLOTS];
+    const T *row = logits + t * ld;
+    T *out_row = out + t * E + e0;
+    int64_t slot0 = t * k + li;
     auto fetch = [&](int64_t at) {
         next.none();
         next_live = false;
         const bool in = at < tokens;
         if (in) {
-            next.load(logits + at * ld, e0, E, vec);
+            next.load(row, e0, E, vec);
             next_live = !valid || valid[at] != 0;
         }
 #pragma unroll
         for (int s = 0; s < SLOTS; ++s) {
-            const int j = s * LPT + li;
-            const bool slot = in && gw && j < k;
-            next_id[s] = slot ? ids[at * k + j] : -1;
-            next_w[s] = slot ? weights[at * k + j] : 0.0f;
-            next_g[s] = slot ? gw[at * k + j] : 0.0f;
+            const bool slot = in && gw && s * LPT + li < k;
+            next_id[s] = slot ? ids[slot0 + s * LPT] : -1;
+            next_w[s] = slot ? weights[slot0 + s * LPT] : 0.0f;
+            next_g[s] = slot ? gw[slot0 + s * LPT] : 0.0f;
         }
     };
     fetch(t);
-    for (; t - sub < tokens; t += step) {
+    for (; t - sub < tokens; t += step, out_row += step * E) {
         Raw<T, EPL> raw = next;
         const bool live = next_live;
         int id[SLOTS];
@@ -549,6 +606,8 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
             g[s] = next_g[s];
             G = id[s] >= 0 ? fmaf(g[s], w[s], G) : G;
         }
+        row += step * ld;
+        slot0 += step * k;
         fetch(t + step);
         if (!live)
             raw.none();
@@ -564,8 +623,11 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
             m = fmaxf(m, v[i]); // a NaN shows in the sum of the exponentials
         }
         m = key_value(group_max<LPT>(order_key(m)));
-        float base, rz;
-        softmax<LPT, EPL>(v, m, base, rz);
+        float rz;
+        exponentials<LPT, EPL>(v, Shift(m), rz);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            v[i] *= rz;
         G = group_sum<LPT>(G);
         __syncwarp();
 #pragma unroll
@@ -592,22 +654,21 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
             for (int i = 0; i < EPL; ++i)
                 d[i] = 0.0f;
         if (t < tokens) {
-            T *row = out + t * E;
             if (vec && e0 + EPL <= E) {
 #pragma unroll
                 for (int i = 0; i < EPL; i += 16 / (int)sizeof(T)) {
                     if constexpr (sizeof(T) == 2)
-                        st_v4(row + e0 + i, pack_bf16(d[i], d[i + 1]), pack_bf16(d[i + 2], d[i + 3]),
+                        st_v4(out_row + i, pack_bf16(d[i], d[i + 1]), pack_bf16(d[i + 2], d[i + 3]),
                               pack_bf16(d[i + 4], d[i + 5]), pack_bf16(d[i + 6], d[i + 7]));
                     else
-                        st_v4(row + e0 + i, __float_as_uint(d[i]), __float_as_uint(d[i + 1]),
+                        st_v4(out_row + i, __float_as_uint(d[i]), __float_as_uint(d[i + 1]),
                               __float_as_uint(d[i + 2]), __float_as_uint(d[i + 3]));
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < EPL; ++i)
                     if (e0 + i < E)
-                        row[e0 + i] = Elem<T>::put(d[i]);
+                        out_row[i] = Elem<T>::put(d[i]);
             }
         }
         __syncwarp();

@@ -28,9 +28,9 @@ int64_t route_grid(int64_t T, int64_t E, int sms)
 {
     const int64_t per_cta = (int64_t)moe::ROUTE_WARPS * (32 / route_shape(E).lpt);
     const int64_t want = (T + per_cta - 1) / per_cta;
-    if (want <= 4)
+    if (want <= 2)
         return 1;
-    return std::min<int64_t>(want, (int64_t)sms * 4);
+    return std::min<int64_t>(want, (int64_t)sms * 2);
 }
 
 constexpr int64_t ROUTE_MAX_CTAS = 4096; // bound of the workspace, any device
@@ -77,7 +77,7 @@ int route_forward(const void *logits, int64_t tokens, int64_t E, int64_t ld, con
 {
     const RouteShape s = route_shape(E);
     // at most 36 KB (1024 experts), below what needs a function attribute
-    const size_t smem = (size_t)(moe::ROUTE_WARPS + 1) * E * 4;
+    const size_t smem = (size_t)(moe::ROUTE_ROWS + 1) * E * 4;
     const int vec = E % (16 / sizeof(T)) == 0 && rows_vec16(logits, ld, sizeof(T));
     const T *l = static_cast<const T *>(logits);
 #define MXQ_ROUTE_CASE(TT, LPT, EPL)                                                                                 \
@@ -97,13 +97,13 @@ int route_backward(const void *logits, int64_t tokens, int64_t E, int64_t ld, co
 {
     const RouteShape s = route_shape(E);
     const int vec = E % (16 / sizeof(T)) == 0 && rows_vec16(logits, ld, sizeof(T)) && aligned(out, 16);
-    const int64_t per_cta = (int64_t)moe::ROUTE_WARPS * (32 / s.lpt);
+    const int64_t per_cta = (int64_t)moe::ROUTE_BWD_WARPS * (32 / s.lpt);
     const int64_t grid = std::min<int64_t>((tokens + per_cta - 1) / per_cta, (int64_t)sms * 8);
-    const size_t smem = (size_t)moe::ROUTE_WARPS * 32 * s.epl * 4;
+    const size_t smem = (size_t)moe::ROUTE_BWD_WARPS * 32 * s.epl * 4;
     const T *l = static_cast<const T *>(logits);
 #define MXQ_ROUTE_CASE(TT, LPT, EPL)                                                                                 \
     if (s.lpt == LPT && s.epl == EPL)                                                                                \
-        return launch(k_moe_route_bwd<TT, LPT, EPL>, dim3((unsigned)grid), dim3(moe::ROUTE_THREADS), smem, stream,   \
+        return launch(k_moe_route_bwd<TT, LPT, EPL>, dim3((unsigned)grid), dim3(moe::ROUTE_BWD_THREADS), smem, stream,   \
                       false, l, tokens, (int)E, ld, valid, k, renorm, vec, weights, ids, loss_grad, gw, gl,          \
                       static_cast<TT *>(out));
     MXQ_ROUTE_VARIANTS(MXQ_ROUTE_CASE, T)

@@ -60,10 +60,26 @@ int ns_map(CUtensorMap *map, const void *p, int64_t inner, int64_t ld, int64_t r
                     store ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// the operands of one product: a matrix by rows, inner length and row length
+// one operand of the products, a matrix by rows with its inner length and row
+// length, and the maps of it that the call has made so far
 struct NsOperand {
     const void *p;
-    int64_t inner, ld, rows;
+    int64_t inner, ld, rows, E;
+    CUtensorMap maps[3];
+    bool made[3];
+
+    int map(int box_rows, const CUtensorMap **out)
+    {
+        const int i = box_rows == ns::HALF ? 0 : (box_rows == ns::CHUNK ? 1 : 2);
+        if (!made[i]) {
+            const int rc = ns_map(&maps[i], p, inner, ld, rows, E, box_rows);
+            if (rc != MXQ_OK)
+                return rc;
+            made[i] = true;
+        }
+        *out = &maps[i];
+        return MXQ_OK;
+    }
 };
 
 // co-resident CTA pairs on the current device; the four products differ in
@@ -89,19 +105,17 @@ template <int MODE, int TN> int ns_pairs(int *out)
 }
 
 template <int MODE, int TN>
-int ns_launch(const NsOperand &p, const NsOperand &q, const NsOperand &o, const ns::Args &a, int pairs,
-              cudaStream_t stream)
+int ns_launch(NsOperand &p, NsOperand &q, NsOperand &o, const ns::Args &a, int pairs, cudaStream_t stream)
 {
-    CUtensorMap mp, mq, mo;
+    const CUtensorMap *mp, *mq, *mo;
     int rc;
-    if ((rc = ns_map(&mp, p.p, p.inner, p.ld, p.rows, a.E, ns::HALF)) != MXQ_OK ||
-        (rc = ns_map(&mq, q.p, q.inner, q.ld, q.rows, a.E, TN / 2)) != MXQ_OK ||
-        (rc = ns_map(&mo, o.p, o.inner, o.ld, o.rows, a.E, ns::CHUNK)) != MXQ_OK)
+    if ((rc = p.map(ns::HALF, &mp)) != MXQ_OK || (rc = q.map(TN / 2, &mq)) != MXQ_OK ||
+        (rc = o.map(ns::CHUNK, &mo)) != MXQ_OK)
         return rc;
     constexpr bool sym = MODE == ns::GRAM || MODE == ns::POLY;
     const int64_t grid = std::min<int64_t>(a.E * ns::sym_or_all_tiles<sym, TN>(a.m, a.n), pairs);
     return launch_chained(ns::k_ns_gemm<MODE, TN>, dim3((unsigned)(2 * grid)), dim3(ns::THREADS), ns::smem_bytes<TN>(),
-                          stream, true, mp, mq, mo, a, (int)((p.inner + ns::BK - 1) / ns::BK), wait_ns());
+                          stream, true, *mp, *mq, *mo, a, (int)((p.inner + ns::BK - 1) / ns::BK), wait_ns());
 }
 
 // Tile width, by estimated time in units of one 64-column block of a 256 x 256
@@ -117,7 +131,7 @@ int64_t ns_estimate(int64_t tiles, int64_t pairs, int64_t blocks100, int64_t dra
 }
 
 template <int MODE>
-int ns_product(const NsOperand &p, const NsOperand &q, const NsOperand &o, const ns::Args &a, cudaStream_t stream)
+int ns_product(NsOperand &p, NsOperand &q, NsOperand &o, const ns::Args &a, cudaStream_t stream)
 {
     constexpr bool sym = MODE == ns::GRAM || MODE == ns::POLY;
     int wide = 0, narrow = 0, rc;
@@ -284,8 +298,9 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
     if (!aligned(workspace, 256))
         return MXQ_ERR_ALIGN;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const NsOperand x = {ws + p.xh, p.n, p.ldx, p.m}, A = {ws + p.A, p.m, p.ldt, p.m}, B = {ws + p.B, p.m, p.ldt, p.m};
-    const NsOperand xt[2] = {{ws + p.xt[0], p.m, p.ldt, p.n}, {ws + p.xt[1], p.m, p.ldt, p.n}};
+    NsOperand x = {ws + p.xh, p.n, p.ldx, p.m, batch, {}, {}}, A = {ws + p.A, p.m, p.ldt, p.m, batch, {}, {}};
+    NsOperand B = {ws + p.B, p.m, p.ldt, p.m, batch, {}, {}};
+    NsOperand xt[2] = {{ws + p.xt[0], p.m, p.ldt, p.n, batch, {}, {}}, {ws + p.xt[1], p.m, p.ldt, p.n, batch, {}, {}}};
     rc = dtype == MXQ_BF16 ? ns_start(static_cast<const uint16_t *>(g), batch, rows, cols, p, eps, ws, stream)
                            : ns_start(static_cast<const float *>(g), batch, rows, cols, p, eps, ws, stream);
     if (rc != MXQ_OK)

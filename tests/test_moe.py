@@ -287,6 +287,9 @@ def test_route_rows_that_choose_nothing(dtype):
     l[2, 2:] = -math.inf                   # fewer experts than slots
     l[3] = torch.finfo(dtype).max
     l[4, 1:] = torch.finfo(dtype).min
+    l[12] = l[12] * 0.1 + 3e6              # far from zero, near each other
+    l[13] = l[13] - 1e30
+    l[14, 3] = 2e38
     valid = torch.ones(T, dtype=torch.bool)
     valid[5:9] = False
     l[6] = math.nan                        # in a padded row: not looked at

@@ -586,8 +586,8 @@ int mxq_version(void);
  *                              kernel.
  *   MXQ_TESTING_NS_TILE        newton_schulz: 0 automatic (one launch for
  *                              small matrices, else the tile width with the
- *                              shorter estimated time), 128 or 256 columns
- *                              forced. */
+ *                              shortest estimated time), 64, 128 or 256
+ *                              columns forced. */
 #define MXQ_TESTING_WAIT_LIMIT_NS 1
 #define MXQ_TESTING_SKIP_ARRIVAL 2
 #define MXQ_TESTING_FORCE_PATH 3

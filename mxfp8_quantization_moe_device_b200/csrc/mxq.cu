@@ -30,7 +30,7 @@ std::atomic<int> g_drop_load{0};
 std::atomic<int> g_force_path{0};
 std::atomic<int> g_mx_bn{0}; // MX grouped GEMM tile width: 0 automatic, 128 forced
 std::atomic<int> g_blocked_words{0}; // blocked layouts: 1 forces the word-load kernels
-std::atomic<int> g_ns_tile{0};       // Newton-Schulz products: tile width, 0 automatic, 128 or 256 forced
+std::atomic<int> g_ns_tile{0};       // Newton-Schulz products: tile width, 0 automatic, 64, 128 or 256 forced
 std::atomic<int> g_gemm_one_sm{0};   // weight-gradient GEMM: 1 forces the one-SM kernel
 
 uint64_t wait_ns() { return (uint64_t)g_wait_ns.load(); }
@@ -1239,7 +1239,7 @@ int mxq_testing_set(int32_t what, int64_t value)
         g_gemm_one_sm.store((int)value);
         return MXQ_OK;
     case MXQ_TESTING_NS_TILE:
-        if (value != 0 && value != 128 && value != 256)
+        if (value != 0 && value != 64 && value != 128 && value != 256)
             return MXQ_ERR_UNSUPPORTED;
         g_ns_tile.store((int)value);
         return MXQ_OK;

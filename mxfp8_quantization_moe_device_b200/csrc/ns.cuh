@@ -64,7 +64,7 @@ constexpr float SA = 1024.0f;          // stored A, B = A, B 2^10
 constexpr float SLO = 2048.0f;         // stored lo = (X 2^8 - hi) 2^11
 
 template <int TN> struct __align__(1024) Smem {
-    static constexpr int STAGES = TN == 256 ? 6 : 8;
+    static constexpr int STAGES = TN == 256 ? 6 : (TN == 128 ? 8 : 9); // what 227 KB hold
     static constexpr int Q_BYTES = TN / 2 * 128; // column operand, one stage, one CTA
     uint8_t a[STAGES][OP_BYTES];
     uint8_t b[STAGES][Q_BYTES];

@@ -50,9 +50,12 @@ int ns_check(int64_t E, int64_t rows, int64_t cols, int32_t steps)
 
 // map of one fp16 matrix per plane: boxes of 64 elements x `box_rows` rows for
 // the operands (128-byte swizzle), of 32 x 32 for the epilogue's stores
+// (box_rows 0)
 int ns_map(CUtensorMap *map, const void *p, int64_t inner, int64_t ld, int64_t rows, int64_t E, int box_rows)
 {
-    const bool store = box_rows == ns::CHUNK;
+    const bool store = box_rows == 0;
+    if (store)
+        box_rows = ns::CHUNK;
     const uint64_t d[3] = {(uint64_t)inner, (uint64_t)rows, (uint64_t)E};
     const uint64_t s[2] = {(uint64_t)ld * 2, (uint64_t)ld * 2 * (uint64_t)rows};
     const uint32_t box[3] = {(uint32_t)(store ? ns::CHUNK : ns::BK), (uint32_t)box_rows, 1};
@@ -65,12 +68,12 @@ int ns_map(CUtensorMap *map, const void *p, int64_t inner, int64_t ld, int64_t r
 struct NsOperand {
     const void *p;
     int64_t inner, ld, rows, E;
-    CUtensorMap maps[3];
-    bool made[3];
+    CUtensorMap maps[4];
+    bool made[4];
 
     int map(int box_rows, const CUtensorMap **out)
     {
-        const int i = box_rows == ns::HALF ? 0 : (box_rows == ns::CHUNK ? 1 : 2);
+        const int i = box_rows == 0 ? 0 : (box_rows == 128 ? 1 : (box_rows == 64 ? 2 : 3));
         if (!made[i]) {
             const int rc = ns_map(&maps[i], p, inner, ld, rows, E, box_rows);
             if (rc != MXQ_OK)
@@ -110,7 +113,7 @@ int ns_launch(NsOperand &p, NsOperand &q, NsOperand &o, const ns::Args &a, int p
     const CUtensorMap *mp, *mq, *mo;
     int rc;
     if ((rc = p.map(ns::HALF, &mp)) != MXQ_OK || (rc = q.map(TN / 2, &mq)) != MXQ_OK ||
-        (rc = o.map(ns::CHUNK, &mo)) != MXQ_OK)
+        (rc = o.map(0, &mo)) != MXQ_OK)
         return rc;
     constexpr bool sym = MODE == ns::GRAM || MODE == ns::POLY;
     const int64_t grid = std::min<int64_t>(a.E * ns::sym_or_all_tiles<sym, TN>(a.m, a.n), pairs);
@@ -118,32 +121,43 @@ int ns_launch(NsOperand &p, NsOperand &q, NsOperand &o, const ns::Args &a, int p
                           stream, true, *mp, *mq, *mo, a, (int)((p.inner + ns::BK - 1) / ns::BK), wait_ns());
 }
 
-// Tile width, by estimated time in units of one 64-column block of a 256 x 256
-// tile (about 0.4 us): a 256 x 128 tile's block takes about 0.8 of that (12.1
-// ms against 7.7 for all tiles of (16, 2048, 7168), twice as many); draining a
-// tile takes about 14 and 7, hidden under the next tile's blocks but for the
-// last round. The narrow tile wins where it spreads the work over more pairs or
-// where draining bounds: 243 us against 272 at (5, 1409, 577), 113 against 144
-// at (4, 256, 256); the wide one at 946 against 1112 at (8, 1024, 4096).
-int64_t ns_estimate(int64_t tiles, int64_t pairs, int64_t blocks100, int64_t drain100)
+// Tile width, by estimated time in units of a hundredth of one 64-column block
+// of a 256 x 256 tile (about 4 ns): a block of a 256 x 128 tile takes 80 (12.1
+// ms against 7.7 for all tiles of (16, 2048, 7168), twice as many), of a 256 x
+// 64 tile about 70; draining a tile takes about 1400, 700 and 350, hidden under
+// the next tile's blocks but for the last round. The narrow tiles win where
+// they spread the work over more pairs or where draining bounds: 243 us against
+// 272 at (5, 1409, 577), 113 against 144 at (4, 256, 256); the wide one at 946
+// against 1112 at (8, 1024, 4096).
+template <int MODE, int TN>
+int ns_estimate(const ns::Args &a, int64_t blocks, int64_t block_cost, int64_t drain, int *pairs, int64_t *time)
 {
-    return (tiles + pairs - 1) / pairs * std::max(blocks100, drain100) + drain100;
+    const int rc = ns_pairs<MODE, TN>(pairs);
+    if (rc != MXQ_OK)
+        return rc;
+    const int64_t tiles = a.E * ns::sym_or_all_tiles<MODE == ns::GRAM || MODE == ns::POLY, TN>(a.m, a.n);
+    *time = (tiles + *pairs - 1) / *pairs * std::max(blocks * block_cost, drain) + drain;
+    const int force = g_ns_tile.load();
+    if (force)
+        *time = force == TN ? 0 : INT64_MAX;
+    return MXQ_OK;
 }
 
 template <int MODE>
 int ns_product(NsOperand &p, NsOperand &q, NsOperand &o, const ns::Args &a, cudaStream_t stream)
 {
-    constexpr bool sym = MODE == ns::GRAM || MODE == ns::POLY;
-    int wide = 0, narrow = 0, rc;
-    if ((rc = ns_pairs<MODE, 256>(&wide)) != MXQ_OK || (rc = ns_pairs<MODE, 128>(&narrow)) != MXQ_OK)
-        return rc;
     const int64_t blocks = (p.inner + ns::BK - 1) / ns::BK;
-    const int64_t t_wide = ns_estimate(a.E * ns::sym_or_all_tiles<sym, 256>(a.m, a.n), wide, 100 * blocks, 1400);
-    const int64_t t_narrow = ns_estimate(a.E * ns::sym_or_all_tiles<sym, 128>(a.m, a.n), narrow, 80 * blocks, 700);
-    const int force = g_ns_tile.load();
-    if (force == 128 || (force == 0 && t_narrow < t_wide))
-        return ns_launch<MODE, 128>(p, q, o, a, narrow, stream);
-    return ns_launch<MODE, 256>(p, q, o, a, wide, stream);
+    int pairs[3], rc;
+    int64_t t[3];
+    if ((rc = ns_estimate<MODE, 256>(a, blocks, 100, 1400, &pairs[0], &t[0])) != MXQ_OK ||
+        (rc = ns_estimate<MODE, 128>(a, blocks, 80, 700, &pairs[1], &t[1])) != MXQ_OK ||
+        (rc = ns_estimate<MODE, 64>(a, blocks, 70, 350, &pairs[2], &t[2])) != MXQ_OK)
+        return rc;
+    if (t[2] < t[1] && t[2] < t[0])
+        return ns_launch<MODE, 64>(p, q, o, a, pairs[2], stream);
+    if (t[1] < t[0])
+        return ns_launch<MODE, 128>(p, q, o, a, pairs[1], stream);
+    return ns_launch<MODE, 256>(p, q, o, a, pairs[0], stream);
 }
 
 template <typename T>

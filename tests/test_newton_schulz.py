@@ -133,7 +133,7 @@ SHAPES = [(1, 1, 1), (1, 1, 9), (2, 7, 1), (3, 16, 16), (2, 33, 65), (4, 96, 224
 def test_newton_schulz(E, N, K, dtype):
     g = matrices(E, N, K, dtype, E + N + K)
     check(mxq.newton_schulz(g), g, [COEF] * 5)
-    for tile in (128, 256):
+    for tile in (64, 128, 256):
         mxq.testing_set(mxq.TESTING_NS_TILE, tile)
         try:
             check(mxq.newton_schulz(g), g, [COEF] * 5)

@@ -26,12 +26,14 @@
 //
 // Epilogue. A lane holds one row of the accumulator, so what it writes along
 // the row lands in 32 different lines per store and what it writes down a
-// column is one line for the warp. Everything that the epilogue reads or
-// writes directly is therefore laid out by columns: X^T (hi) and lo, and A and
-// B through their symmetry; the row-major copies that the products read go
-// through shared memory and a TMA store.
-// (Row-wise 16-byte accesses kept the load/store unit busy for 16 K cycles a
-// tile against 8 K of MMAs: 1393 us for B X at (16, 2048, 7168).)
+// column is one line for the warp. What only the epilogue reads (X as hi and
+// lo, and A for the next product) is kept in chunks of 32 x 32 elements in the
+// order in which the warp holds them, 16 bytes per lane and access, padded to
+// whole chunks so that nothing is predicated; X^T and the mirrored halves of A
+// and B are written down the columns; the row-major copies that the products
+// read go through shared memory and a TMA store. Row-wise 16-byte accesses in
+// their place kept the load/store unit busy for 16 K cycles a tile against 8 K
+// of MMAs, 2-byte accesses down the columns for all of it cost 1.6 us a chunk.
 //
 // Kernel: the CTA-pair pipeline of gemm2.cuh (tcgen05.mma.cta_group::2, one
 // 256 x 256 tile per pair of SMs, six 32 KB stages of 64 fp16 columns, two
@@ -90,11 +92,11 @@ enum Mode { GRAM = 0, POLY = 1, STEP = 2, LAST = 3 };
 
 struct Args {
     int E, m, n;          // batch, X is (m, n)
-    int ldt;              // row length of X^T, its state, A and B (m up to 8)
+    int ldt;              // row length of X^T, A and B (m up to 8)
     float a, b, c;
-    uint16_t *lo;         // (E, n, ldt): low words of X, by columns
-    const uint16_t *xt0;  // (E, n, ldt): high words of X by columns (X^T), read
-    uint16_t *xt;         // the new ones, written by STEP
+    uint16_t *hi, *lo;    // X as the epilogue keeps it: chunks of (m, n)
+    uint16_t *a_own;      // A as the epilogue keeps it: chunks of (m, m)
+    uint16_t *xt;         // (E, n, ldt): X^T, written by STEP
     uint16_t *A, *B;      // (E, m, ldt)
     uint16_t *out;        // LAST: bf16, (E, m, n) or, transposed, (E, n, m)
     int out_t, out_vec;
@@ -109,6 +111,14 @@ template <int TN> MXQ_DEV void mma_pair_f16(uint32_t d_tmem, uint64_t adesc, uin
                  : "memory");
 }
 
+// chunks of 32 along `len`, and the first element of a chunk in the epilogue's
+// own arrays: piece g (8 columns) of lane l follows at g * 256 + l * 8
+__host__ __device__ constexpr int64_t chunks_of(int64_t len) { return (len + CHUNK - 1) / CHUNK; }
+MXQ_DEV int64_t chunk_at(int e, int m, int n, int r0, int c0)
+{
+    return (((int64_t)e * chunks_of(m) + r0 / CHUNK) * chunks_of(n) + c0 / CHUNK) * (CHUNK * CHUNK);
+}
+
 MXQ_DEV void prefetch_map(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -120,7 +130,7 @@ MXQ_DEV uint32_t pack_half2(float lo, float hi)
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-MXQ_DEV float half_value(uint16_t h) { return __half2float(__ushort_as_half(h)); }
+MXQ_DEV uint32_t word_of(const uint4 &v, int i) { return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w)); }
 MXQ_DEV float2 unpack_half2(uint32_t w) { return __half22float2(*reinterpret_cast<__half2 *>(&w)); }
 
 // A warp's 32 x 32 chunk of 16-bit values, one row per lane (two columns per
@@ -280,13 +290,13 @@ MXQ_DEV void scale_factors(double norm, float &f0, float &f1)
 }
 
 // X0 from G (rows, cols) in 64 x 64 tiles. X is G, or with `tall` G^T: the
-// tile as it is read goes to X (tall: to X^T and lo), its transpose to X^T and
-// lo (tall: to X). A thread moves pairs of neighbours.
+// tile as it is read goes to X (tall: to X^T), its transpose to X^T (tall: to X),
+// both halves to the epilogue's chunks. A thread moves pairs of neighbours.
 template <typename T>
 __global__ void __launch_bounds__(256)
     k_ns_init(const T *__restrict__ g, int rows, int cols, int pair, const double *__restrict__ part, int parts,
               double eps, int tall, uint16_t *__restrict__ xh, int ldx, uint16_t *__restrict__ xt,
-              uint16_t *__restrict__ xlo, int ldt)
+              int ldt, uint16_t *__restrict__ hi, uint16_t *__restrict__ lo)
 {
     __shared__ uint32_t tile[64][65];
     __shared__ float s_f[2];
@@ -330,7 +340,6 @@ __global__ void __launch_bounds__(256)
         if (R < rows && C < cols) { // rows of the targets are padded to pairs
             if (tall) {
                 *reinterpret_cast<uint32_t *>(xt + base_t + (int64_t)R * ldt + C) = h;
-                *reinterpret_cast<uint32_t *>(xlo + base_t + (int64_t)R * ldt + C) = l;
             } else {
                 *reinterpret_cast<uint32_t *>(xh + base_x + (int64_t)R * ldx + C) = h;
             }
@@ -347,8 +356,29 @@ __global__ void __launch_bounds__(256)
                 *reinterpret_cast<uint32_t *>(xh + base_x + (int64_t)C * ldx + R) = h;
             } else {
                 *reinterpret_cast<uint32_t *>(xt + base_t + (int64_t)C * ldt + R) = h;
-                *reinterpret_cast<uint32_t *>(xlo + base_t + (int64_t)C * ldt + R) = __byte_perm(w0, w1, 0x7632);
             }
+        }
+    }
+    // a warp per chunk and pair of pieces
+    const int m = tall ? cols : rows, n = tall ? rows : cols;
+    const int lane = threadIdx.x & 31, chunk = threadIdx.x >> 6, half = threadIdx.x >> 5 & 1;
+    const int y = CHUNK * (chunk >> 1), x = CHUNK * (chunk & 1); // in the tile, along X's rows and columns
+    const int xr = (tall ? c0 : r0) + y, xc = (tall ? r0 : c0) + x;
+    if (xr < m && xc < n) {
+        const int64_t at = chunk_at(e, m, n, xr, xc) + lane * 8;
+#pragma unroll
+        for (int g = 2 * half; g < 2 * half + 2; ++g) {
+            uint32_t w[8], a[4], b[4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i] = tall ? tile[x + 8 * g + i][y + lane] : tile[y + lane][x + 8 * g + i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x5410);
+                b[i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x7632);
+            }
+            st_v4(hi + at + g * 256, a[0], a[1], a[2], a[3]);
+            st_v4(lo + at + g * 256, b[0], b[1], b[2], b[3]);
         }
     }
 }
@@ -544,31 +574,22 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool row_ok = r < q.m;
             const int cols = SYM ? q.m : q.n;
             // this lane's column-wise position: element c of the row is `at` + c
-            // ldt elements into its matrix of X^T, lo, A and B alike (a matrix
+            // ldt elements into its matrix of X^T, A and B alike (a matrix
             // has less than 2^31 elements, so 32 bits hold its byte offsets)
             const int64_t plane = (int64_t)w.e * cols * q.ldt;
             const uint32_t at = (uint32_t)r, ldb = (uint32_t)q.ldt * 2u;
             const bool rows_full = r0 + 32 <= q.m; // the same in every lane
+            const bool rows_any = r0 < q.m;
             // what the chunk adds to the product: X (hi and lo), or A
-            uint16_t old_h[CHUNK], old_l[MODE == POLY ? 1 : CHUNK];
-            const uint8_t *old_hi = reinterpret_cast<const uint8_t *>((MODE == POLY ? q.A : q.xt0) + plane);
-            uint8_t *old_lo = reinterpret_cast<uint8_t *>(q.lo + plane);
+            uint4 old_h[4], old_l[MODE == POLY ? 1 : 4];
             auto load_old = [&](int c0) {
-                uint32_t o = (uint32_t)c0 * ldb + at * 2u;
-                if (rows_full && c0 + CHUNK <= cols) {
+                if (rows_any && c0 < cols) {
+                    const int64_t o = chunk_at(w.e, q.m, cols, r0, c0) + lane * 8;
 #pragma unroll
-                    for (int k = 0; k < CHUNK; ++k, o += ldb) {
-                        old_h[k] = *reinterpret_cast<const uint16_t *>(old_hi + o);
+                    for (int g = 0; g < 4; ++g) {
+                        old_h[g] = *reinterpret_cast<const uint4 *>((MODE == POLY ? q.a_own : q.hi) + o + g * 256);
                         if constexpr (MODE != POLY)
-                            old_l[k] = *reinterpret_cast<const uint16_t *>(old_lo + o);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < CHUNK; ++k, o += ldb) {
-                        const bool in = row_ok && c0 + k < cols;
-                        old_h[k] = in ? *reinterpret_cast<const uint16_t *>(old_hi + o) : (uint16_t)0;
-                        if constexpr (MODE != POLY)
-                            old_l[k] = in ? *reinterpret_cast<const uint16_t *>(old_lo + o) : (uint16_t)0;
+                            old_l[g] = *reinterpret_cast<const uint4 *>(q.lo + o + g * 256);
                     }
                 }
             };
@@ -597,13 +618,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                         v0 = d0 * (SA / (SX * SX));
                         v1 = d1 * (SA / (SX * SX));
                     } else {
-                        const float h0 = half_value(old_h[2 * k]), h1 = half_value(old_h[2 * k + 1]);
+                        const float2 oh = unpack_half2(word_of(old_h[k >> 2], k & 3));
                         if constexpr (MODE == POLY) {
-                            v0 = fmaf(q.c * (1.0f / SA), d0, q.b * h0);
-                            v1 = fmaf(q.c * (1.0f / SA), d1, q.b * h1);
+                            v0 = fmaf(q.c * (1.0f / SA), d0, q.b * oh.x);
+                            v1 = fmaf(q.c * (1.0f / SA), d1, q.b * oh.y);
                         } else {
-                            v0 = fmaf(q.a, fmaf(half_value(old_l[2 * k]), 1.0f / SLO, h0), d0 * (1.0f / SA));
-                            v1 = fmaf(q.a, fmaf(half_value(old_l[2 * k + 1]), 1.0f / SLO, h1), d1 * (1.0f / SA));
+                            const float2 ol = unpack_half2(word_of(old_l[k >> 2], k & 3));
+                            v0 = fmaf(q.a, fmaf(ol.x, 1.0f / SLO, oh.x), d0 * (1.0f / SA));
+                            v1 = fmaf(q.a, fmaf(ol.y, 1.0f / SLO, oh.y), d1 * (1.0f / SA));
                         }
                     }
                     if constexpr (MODE == LAST) {
@@ -620,6 +642,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (ch + 2 < TN / CHUNK && c0 + 2 * CHUNK < cols)
                         load_old(c0 + 2 * CHUNK);
                 }
+                // the epilogue's own copies
+                if constexpr (MODE == STEP || MODE == GRAM) {
+                    if (rows_any) {
+                        const int64_t o = chunk_at(w.e, q.m, cols, r0, c0) + lane * 8;
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            st_v4((MODE == GRAM ? q.a_own : q.hi) + o + g * 256, h[4 * g], h[4 * g + 1], h[4 * g + 2],
+                                  h[4 * g + 3]);
+                            if constexpr (MODE == STEP)
+                                st_v4(q.lo + o + g * 256, l[4 * g], l[4 * g + 1], l[4 * g + 2], l[4 * g + 3]);
+                        }
+                    }
+                }
                 // down the columns
                 if (MODE != LAST || q.out_t) {
                     const uint32_t ld2 = MODE == LAST ? (uint32_t)q.m * 2u : ldb;
@@ -629,9 +664,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                                        : reinterpret_cast<uint8_t *>((MODE == GRAM ? q.A : MODE == POLY ? q.B : q.xt) + plane);
                     auto put = [&](int k) {
                         *reinterpret_cast<uint16_t *>(dst + o) = (uint16_t)(k & 1 ? h[k >> 1] >> 16 : h[k >> 1]);
-                        if constexpr (MODE == STEP)
-                            *reinterpret_cast<uint16_t *>(old_lo + o) =
-                                (uint16_t)(k & 1 ? l[k >> 1] >> 16 : l[k >> 1]);
                     };
                     if (rows_full && c0 + CHUNK <= cols) {
 #pragma unroll

@@ -7,7 +7,7 @@ namespace {
 struct NsPlan {
     int64_t m, n, ldx, ldt;
     int tall, parts;
-    size_t xh, lo, xt[2], A, B, part, bytes;
+    size_t xh, hi, lo, xt[2], A, B, a_own, part, bytes;
 };
 
 NsPlan ns_plan(int64_t E, int64_t rows, int64_t cols, int32_t steps)
@@ -26,7 +26,9 @@ NsPlan ns_plan(int64_t E, int64_t rows, int64_t cols, int32_t steps)
         return at;
     };
     p.xh = take((size_t)E * p.m * p.ldx * 2);
-    p.lo = take((size_t)E * p.n * p.ldt * 2);
+    p.hi = take((size_t)E * ns::chunks_of(p.m) * ns::chunks_of(p.n) * ns::CHUNK_BYTES);
+    p.lo = take((size_t)E * ns::chunks_of(p.m) * ns::chunks_of(p.n) * ns::CHUNK_BYTES);
+    p.a_own = take((size_t)E * ns::chunks_of(p.m) * ns::chunks_of(p.m) * ns::CHUNK_BYTES);
     p.xt[0] = take((size_t)E * p.n * p.ldt * 2);
     p.xt[1] = steps > 1 ? take((size_t)E * p.n * p.ldt * 2) : p.xt[0];
     p.A = take((size_t)E * p.m * p.ldt * 2);
@@ -173,7 +175,8 @@ int ns_start(const T *g, int64_t E, int64_t rows, int64_t cols, const NsPlan &p,
                           dim3((unsigned)((cols + 63) / 64), (unsigned)((rows + 63) / 64), (unsigned)E), dim3(256), 0,
                           stream, false, g, (int)rows, (int)cols, (int)(aligned(g, 2 * sizeof(T)) && cols % 2 == 0),
                   (const double *)part, p.parts, eps, p.tall, reinterpret_cast<uint16_t *>(ws + p.xh), (int)p.ldx,
-                  reinterpret_cast<uint16_t *>(ws + p.xt[0]), reinterpret_cast<uint16_t *>(ws + p.lo), (int)p.ldt);
+                  reinterpret_cast<uint16_t *>(ws + p.xt[0]), (int)p.ldt, reinterpret_cast<uint16_t *>(ws + p.hi),
+                  reinterpret_cast<uint16_t *>(ws + p.lo));
 }
 
 // a launch of k_ns_small with `ctas` CTAs per matrix
@@ -324,7 +327,9 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
     a.m = (int)p.m;
     a.n = (int)p.n;
     a.ldt = (int)p.ldt;
+    a.hi = reinterpret_cast<uint16_t *>(ws + p.hi);
     a.lo = reinterpret_cast<uint16_t *>(ws + p.lo);
+    a.a_own = reinterpret_cast<uint16_t *>(ws + p.a_own);
     a.A = reinterpret_cast<uint16_t *>(ws + p.A);
     a.B = reinterpret_cast<uint16_t *>(ws + p.B);
     a.out = static_cast<uint16_t *>(out);
@@ -334,7 +339,6 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
         a.a = coefficients[3 * s];
         a.b = coefficients[3 * s + 1];
         a.c = coefficients[3 * s + 2];
-        a.xt0 = reinterpret_cast<const uint16_t *>(ws + p.xt[s & 1]);
         a.xt = reinterpret_cast<uint16_t *>(ws + p.xt[(s + 1) & 1]);
         if ((rc = ns_product<ns::GRAM>(x, x, A, a, stream)) != MXQ_OK ||
             (rc = ns_product<ns::POLY>(A, A, B, a, stream)) != MXQ_OK ||

@@ -38,8 +38,9 @@
 // Kernel: the CTA-pair pipeline of gemm2.cuh (tcgen05.mma.cta_group::2, one
 // 256 x 256 tile per pair of SMs, six 32 KB stages of 64 fp16 columns, two
 // accumulators in TMEM); warps 0-7 epilogue (a warp takes 32 lanes and half
-// of the columns), warp 8 TMA, warp 9 MMA and TMEM, warp 10 passes its CTA's
-// filled slots on to the leader. Edges are filled with zeros by TMA (every
+// of the columns), warp 8 TMA, warp 9 MMA and TMEM. Both CTAs' loads count on
+// the leader's barrier (TMA loads of cta_group::2), which its MMA thread waits
+// on. Edges are filled with zeros by TMA (every
 // matrix is its own plane of a rank-3 map) and cut off by the epilogue.
 #pragma once
 
@@ -55,7 +56,7 @@ constexpr int TILE = 2 * HALF;         // rows of a pair's tile; it has TN colum
 constexpr int BK = 64;                 // fp16 elements per 128-byte row
 constexpr int OP_BYTES = HALF * 128;   // row operand, one stage, one CTA
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = (EPI_WARPS + 3) * 32;
+constexpr int THREADS = (EPI_WARPS + 2) * 32;
 constexpr int ACC = 2;
 constexpr int CHUNK = 32;              // an epilogue step: 32 rows x 32 columns per warp
 constexpr int CHUNK_BYTES = CHUNK * CHUNK * 2;
@@ -71,8 +72,7 @@ template <int TN> struct __align__(1024) Smem {
     uint8_t a[STAGES][OP_BYTES];
     uint8_t b[STAGES][Q_BYTES];
     uint8_t stage[EPI_WARPS][2][CHUNK_BYTES]; // row-major chunks on their way out
-    uint64_t full[STAGES];
-    uint64_t ready[STAGES];
+    uint64_t full[STAGES];  // the leader's: both CTAs' loads
     uint64_t empty[STAGES];
     uint64_t acc_full[ACC];
     uint64_t acc_empty[ACC];
@@ -117,6 +117,16 @@ __host__ __device__ constexpr int64_t chunks_of(int64_t len) { return (len + CHU
 MXQ_DEV int64_t chunk_at(int e, int m, int n, int r0, int c0)
 {
     return (((int64_t)e * chunks_of(m) + r0 / CHUNK) * chunks_of(n) + c0 / CHUNK) * (CHUNK * CHUNK);
+}
+
+// TMA load into this CTA's shared memory that counts on a barrier of the
+// pair's leader (a shared::cluster address)
+MXQ_DEV void load_pair(void *dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+                 " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
 }
 
 MXQ_DEV void prefetch_map(const CUtensorMap *map)
@@ -421,7 +431,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             prefetch_map(&tm_o);
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.ready[s], 2);
             mbar_init(&sm.empty[s], 1);
         }
         for (int i = 0; i < ACC; ++i) {
@@ -475,6 +484,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == EPI_WARPS) {
         // ------------------------------------------------ TMA producer (both CTAs)
         if (lane == 0) {
+            const uint32_t leader_full0 = g2::peer_addr(&sm.full[0], 0);
             int seq = 0;
             for (int64_t it = pair; it < total && !gm::aborted(&sm.abort_flag); it += npairs) {
                 const Item w = item(it);
@@ -484,36 +494,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                         *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
                         break;
                     }
-                    mbar_arrive_expect_tx(&sm.full[s], OP_BYTES + Smem<TN>::Q_BYTES);
-                    tma_load_3d(sm.a[s], &tm_p, &sm.full[s], kb * BK, w.i * TILE + (int)rank * HALF, w.e);
-                    tma_load_3d(sm.b[s], &tm_q, &sm.full[s], kb * BK, w.j * TN + (int)rank * (TN / 2), w.e);
+                    if (leader)
+                        mbar_arrive_expect_tx(&sm.full[s], 2 * (OP_BYTES + Smem<TN>::Q_BYTES));
+                    const uint32_t bar = leader_full0 + (uint32_t)(s * sizeof(uint64_t));
+                    load_pair(sm.a[s], &tm_p, bar, kb * BK, w.i * TILE + (int)rank * HALF, w.e);
+                    load_pair(sm.b[s], &tm_q, bar, kb * BK, w.j * TN + (int)rank * (TN / 2), w.e);
                 }
             }
-            // drain: every issued fill has landed before the CTA leaves
-            for (int j = seq - STAGES; j < seq; ++j)
-                if (j >= 0)
-                    mbar_wait(&sm.full[j % STAGES], (uint32_t)(j / STAGES) & 1u, wait_ns);
-        }
-    } else if (warp == EPI_WARPS + 2) {
-        // ------------------------------------------------ hand-off of filled slots (both CTAs)
-        if (lane == 0) {
-            const uint32_t leader_ready0 = g2::peer_addr(&sm.ready[0], 0);
-            int s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int64_t it = pair; ok && it < total && !gm::aborted(&sm.abort_flag); it += npairs)
-                for (int kb = 0; kb < nkb; ++kb) {
-                    ok = mbar_wait(&sm.full[s], ph, wait_ns);
-                    if (!ok) {
-                        *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
-                        break;
-                    }
-                    g2::arrive_remote(leader_ready0 + (uint32_t)(s * sizeof(uint64_t)));
-                    if (++s == STAGES) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
-                }
+            // drain: every issued fill, of both CTAs, has landed before the
+            // leader goes to the closing barrier
+            if (leader)
+                for (int j = seq - STAGES; j < seq; ++j)
+                    if (j >= 0)
+                        mbar_wait(&sm.full[j % STAGES], (uint32_t)(j / STAGES) & 1u, wait_ns);
         }
     } else if (warp == EPI_WARPS + 1) {
         // ------------------------------------------------ leader: the pair's MMAs (one thread)
@@ -531,7 +524,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint32_t d = tmem + (uint32_t)(acc * TN);
                 // the next slot is waited on before this slot's last MMA, so
                 // that the wait overlaps MMAs already in the pipe
-                bool ok = mbar_wait(&sm.ready[s], ph, wait_ns);
+                bool ok = mbar_wait(&sm.full[s], ph, wait_ns);
                 for (int kb = 0; ok && kb < nkb; ++kb) {
                     gm::tc_fence_after();
                     const uint64_t ad = gm::smem_desc_k128(smem_u32(sm.a[s]));
@@ -542,7 +535,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int s_next = s + 1 == STAGES ? 0 : s + 1;
                     const uint32_t ph_next = s + 1 == STAGES ? ph ^ 1u : ph;
                     if (kb + 1 < nkb)
-                        ok = mbar_wait(&sm.ready[s_next], ph_next, wait_ns);
+                        ok = mbar_wait(&sm.full[s_next], ph_next, wait_ns);
                     mma_pair_f16<TN>(d, ad + 6, bd + 6, 1u);
                     g2::commit_pair(&sm.empty[s], 0x3);
                     issued = true;

@@ -9,15 +9,23 @@
 //
 // Numerics. The products run on the fp16 tensor cores with fp32 accumulators:
 // the values are bounded (singular values stay near one), so fp16's 11-bit
-// significand costs nothing in range and is eight times finer than bf16's.
-// X is held as a pair hi + lo of fp16 words (22 bits): the products read hi,
-// the term a X adds both. Without lo the rounding of X would be multiplied by
-// a = 3.4 in every later step wherever a singular value is small: on a matrix
-// whose singular values fall to 1e-4 the result was off by 0.9% of its norm,
-// with lo by 0.08%, half of what rounding the result to bf16 costs. A and B
-// are rounded once each to fp16. Scales are powers of two: X 2^8 (a random
-// 2048 x 7168 matrix starts with elements near 2^-12, fp16's normal range
-// ends at 2^-14), A and B 2^10, lo 2^11 on top of X's.
+// significand costs nothing in range and is eight times finer than bf16's. Two
+// things keep what fp16 rounds away below what rounding the result to bf16
+// costs (1.7e-3 of the norm; all errors below are without that):
+//   - X is held as hi + lo, two fp16 words (22 bits): the products read hi, the
+//     term a X adds both. With hi alone the rounding of X is multiplied by a =
+//     3.4 in every later step wherever a singular value is small: 9e-3 on a
+//     matrix whose singular values fall to 1e-4.
+//   - The diagonals of A and B stay in fp32. X comes near to orthogonal, so A
+//     is near to a multiple of the identity, and the diagonal is where most of
+//     its rounding error would be. With A = A' + diag(alpha), A' rounded once,
+//       B = B' + diag(beta),  beta = b alpha + c alpha^2 + c (A' A')_rr,
+//       B'_rs = c (A' A')_rs + (b + c (alpha_r + alpha_s)) A'_rs  off the diagonal
+//     and X <- (a + beta_r) X + B' X, row by row. On random 64 x 1000 matrices
+//     1.9e-3 falls to 2.5e-4, on 512 x 512 ones 1.5e-3 to 7e-4.
+// Scales are powers of two: X 2^8 (a random 2048 x 7168 matrix starts with
+// elements near 2^-12, fp16's normal range ends at 2^-14), A' and B' 2^10, lo
+// 2^11 on top of X's.
 //
 // Every product is D = P Q^T with both operands K-major: A = X X^T, A A = A
 // A^T (A is symmetric), B X = B (X^T)^T; the epilogue that writes X therefore
@@ -63,7 +71,7 @@ constexpr int CHUNK_BYTES = CHUNK * CHUNK * 2;
 constexpr int MAX_PARTS = 64;          // partial sums of squares per matrix
 
 constexpr float SX = 256.0f;           // stored X  = X 2^8
-constexpr float SA = 1024.0f;          // stored A, B = A, B 2^10
+constexpr float SA = 1024.0f;          // stored A', B' = A', B' 2^10
 constexpr float SLO = 2048.0f;         // stored lo = (X 2^8 - hi) 2^11
 
 template <int TN> struct __align__(1024) Smem {
@@ -95,7 +103,8 @@ struct Args {
     int ldt;              // row length of X^T, A and B (m up to 8)
     float a, b, c;
     uint16_t *hi, *lo;    // X as the epilogue keeps it: chunks of (m, n)
-    uint16_t *a_own;      // A as the epilogue keeps it: chunks of (m, m)
+    uint16_t *a_own;      // A' as the epilogue keeps it: chunks of (m, m)
+    float *alpha, *beta;  // (E, m): the diagonals of A and B
     uint16_t *xt;         // (E, n, ldt): X^T, written by STEP
     uint16_t *A, *B;      // (E, m, ldt)
     uint16_t *out;        // LAST: bf16, (E, m, n) or, transposed, (E, n, m)
@@ -575,7 +584,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool rows_any = r0 < q.m;
             // what the chunk adds to the product: X (hi and lo), or A
             uint4 old_h[4], old_l[MODE == POLY ? 1 : 4];
+            float alpha_c = 0.0f; // POLY: alpha of the chunk's column `lane`
             auto load_old = [&](int c0) {
+                if (MODE == POLY && c0 + lane < cols)
+                    alpha_c = q.alpha[(int64_t)w.e * q.m + c0 + lane];
                 if (rows_any && c0 < cols) {
                     const int64_t o = chunk_at(w.e, q.m, cols, r0, c0) + lane * 8;
 #pragma unroll
@@ -586,6 +598,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             };
+            const int64_t diag_at = (int64_t)w.e * q.m + r;
+            // this row's share of the diagonals: alpha_r, or a + beta_r
+            float own = 0.0f;
+            if (MODE != GRAM && row_ok)
+                own = MODE == POLY ? q.alpha[diag_at] : q.a + q.beta[diag_at];
             if constexpr (MODE != GRAM)
                 load_old(w.j * TN + CHUNK * part); // in flight while the product finishes
             bool ok = mbar_wait(&sm.acc_full[acc], (uint32_t)(t / ACC) & 1u, wait_ns);
@@ -603,6 +620,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint32_t d[CHUNK];
                 gm::tc_ld32(tmem + (uint32_t)(acc * TN + CHUNK * ch) + ((uint32_t)(32 * quad) << 16), d);
                 uint32_t h[CHUNK / 2], l[CHUNK / 2]; // pairs of the row, high and low words
+                // in the chunk on the diagonal, element `lane` of the row stays
+                // in fp32 and is zero in A' and B'
+                const int dk = SYM && c0 == r0 ? lane : -1;
+                float on_diag = 0.0f;
 #pragma unroll
                 for (int k = 0; k < CHUNK / 2; ++k) {
                     const float d0 = __uint_as_float(d[2 * k]), d1 = __uint_as_float(d[2 * k + 1]);
@@ -613,13 +634,20 @@ __global__ void __launch_bounds__(THREADS, 1)
                     } else {
                         const float2 oh = unpack_half2(word_of(old_h[k >> 2], k & 3));
                         if constexpr (MODE == POLY) {
-                            v0 = fmaf(q.c * (1.0f / SA), d0, q.b * oh.x);
-                            v1 = fmaf(q.c * (1.0f / SA), d1, q.b * oh.y);
+                            const float a0 = own + __shfl_sync(0xffffffffu, alpha_c, 2 * k);
+                            const float a1 = own + __shfl_sync(0xffffffffu, alpha_c, 2 * k + 1);
+                            v0 = fmaf(q.c * (1.0f / SA), d0, fmaf(q.c, a0, q.b) * oh.x);
+                            v1 = fmaf(q.c * (1.0f / SA), d1, fmaf(q.c, a1, q.b) * oh.y);
                         } else {
                             const float2 ol = unpack_half2(word_of(old_l[k >> 2], k & 3));
-                            v0 = fmaf(q.a, fmaf(ol.x, 1.0f / SLO, oh.x), d0 * (1.0f / SA));
-                            v1 = fmaf(q.a, fmaf(ol.y, 1.0f / SLO, oh.y), d1 * (1.0f / SA));
+                            v0 = fmaf(own, fmaf(ol.x, 1.0f / SLO, oh.x), d0 * (1.0f / SA));
+                            v1 = fmaf(own, fmaf(ol.y, 1.0f / SLO, oh.y), d1 * (1.0f / SA));
                         }
+                    }
+                    if constexpr (SYM) {
+                        on_diag = dk == 2 * k ? d0 : (dk == 2 * k + 1 ? d1 : on_diag);
+                        v0 = dk == 2 * k ? 0.0f : v0;
+                        v1 = dk == 2 * k + 1 ? 0.0f : v1;
                     }
                     if constexpr (MODE == LAST) {
                         h[k] = gm::pack_bf16x2(v0 * (1.0f / SX), v1 * (1.0f / SX));
@@ -630,6 +658,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                             l[k] = pack_half2((v0 - f.x) * SLO, (v1 - f.y) * SLO);
                         }
                     }
+                }
+                if (SYM && c0 == r0 && row_ok) { // the chunk on the diagonal
+                    if constexpr (MODE == GRAM)
+                        q.alpha[diag_at] = on_diag * (1.0f / (SX * SX));
+                    else
+                        q.beta[diag_at] = fmaf(fmaf(q.c, own, q.b), own, q.c * (on_diag * (1.0f / (SA * SA))));
                 }
                 if constexpr (MODE != GRAM) {
                     if (ch + 2 < TN / CHUNK && c0 + 2 * CHUNK < cols)

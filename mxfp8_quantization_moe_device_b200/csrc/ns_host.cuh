@@ -7,7 +7,7 @@ namespace {
 struct NsPlan {
     int64_t m, n, ldx, ldt;
     int tall, parts;
-    size_t xh, hi, lo, xt[2], A, B, a_own, part, bytes;
+    size_t xh, hi, lo, xt[2], A, B, a_own, alpha, beta, part, bytes;
 };
 
 NsPlan ns_plan(int64_t E, int64_t rows, int64_t cols, int32_t steps)
@@ -33,6 +33,8 @@ NsPlan ns_plan(int64_t E, int64_t rows, int64_t cols, int32_t steps)
     p.xt[1] = steps > 1 ? take((size_t)E * p.n * p.ldt * 2) : p.xt[0];
     p.A = take((size_t)E * p.m * p.ldt * 2);
     p.B = take((size_t)E * p.m * p.ldt * 2);
+    p.alpha = take((size_t)E * p.m * 4);
+    p.beta = take((size_t)E * p.m * 4);
     p.part = take((size_t)E * p.parts * 8);
     p.bytes = o;
     return p;
@@ -330,6 +332,8 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
     a.hi = reinterpret_cast<uint16_t *>(ws + p.hi);
     a.lo = reinterpret_cast<uint16_t *>(ws + p.lo);
     a.a_own = reinterpret_cast<uint16_t *>(ws + p.a_own);
+    a.alpha = reinterpret_cast<float *>(ws + p.alpha);
+    a.beta = reinterpret_cast<float *>(ws + p.beta);
     a.A = reinterpret_cast<uint16_t *>(ws + p.A);
     a.B = reinterpret_cast<uint16_t *>(ws + p.B);
     a.out = static_cast<uint16_t *>(out);

@@ -3,8 +3,9 @@
 //
 // A CTA holds a slab of up to 256 columns of X (m <= 128 rows): hi of X and of
 // X^T as fp16 in shared memory in the layout that tcgen05.mma reads, X itself
-// in fp32 in TMEM, as the accumulator of the step's last product: a X is
-// written there and B X added to it by the tensor core, so X is never rounded.
+// in fp32 in TMEM, as the accumulator of the step's last product: its rows are
+// multiplied by a + beta_r there and B' X added to them by the tensor core, so X
+// is never rounded.
 // A matrix with more columns takes a cluster of up to sixteen CTAs: each
 // multiplies its slab with itself, the partial 128 x 128 products are summed
 // over distributed shared memory in rank order (every CTA sums some rows and
@@ -38,6 +39,7 @@ struct __align__(1024) SmallSmem {
     uint8_t xh[SM_SLAB / 64][SM_M * 128];  // X: blocks of 64 columns, 128-byte rows
     uint8_t xt[SM_M / 64][SM_SLAB * 128];  // X^T: blocks of 64 rows of X
     uint8_t ab[SM_M / 64][SM_M * 128];     // A, then B
+    float alpha[SM_M], beta[SM_M];         // the diagonals of A and B
     double sums[SM_MAX_CTAS];              // every CTA's sum of squares
     double warp_sum[SM_THREADS / 32];
     uint64_t bar;
@@ -94,9 +96,26 @@ MXQ_DEV void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b)
 {
     asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
+MXQ_DEV void st_cluster_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 MXQ_DEV void st_cluster_f64(uint32_t addr, double v)
 {
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+
+// element `dk` (none if negative) of the row that a lane holds: returned, and
+// zero in v. By selects: a branch on the lane would put v into local memory.
+MXQ_DEV float take_diagonal(uint32_t (&v)[32], int dk)
+{
+    uint32_t x = 0u;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+        x = dk == k ? v[k] : x;
+        v[k] = dk == k ? 0u : v[k];
+    }
+    return __uint_as_float(x);
 }
 
 // byte of column byte `b` (of 128) of row `r` in a block of 128-byte rows with
@@ -233,7 +252,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                 (uint16_t)(k & 1 ? h[k >> 1] >> 16 : h[k >> 1]);
     };
     if (active) {
-        const float f0 = sm.factor[0], f1 = sm.factor[1], a0 = co.v[0] * SA;
+        const float f0 = sm.factor[0], f1 = sm.factor[1];
 #pragma unroll 1
         for (int ch = part; 32 * ch < n16; ch += 4) {
             uint32_t v[32];
@@ -242,7 +261,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
                 x[k] = (__uint_as_float(v[k]) * f0) * f1;
-                v[k] = __float_as_uint(a0 * x[k]);
+                v[k] = __float_as_uint(SA * x[k]);
             }
             put_x(32 * ch, x);
             tc_st32(lanes + d_x + 32 * ch, v);
@@ -284,6 +303,9 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                 uint32_t v[32];
                 gm::tc_ld32(lanes + d_a + 32 * ch, v);
                 if (ctas == 1) {
+                    const float on_diag = take_diagonal(v, ch == quad ? lane : -1); // to fp32, and out of A
+                    if (ch == quad)
+                        sm.alpha[r] = on_diag * (1.0f / (SX * SX));
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         if (32 * ch + 8 * q < m16) {
@@ -326,6 +348,14 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                         if (p0 + p < ctas)
                             a.x += b[p].x, a.y += b[p].y, a.z += b[p].z, a.w += b[p].w;
                 }
+                if (ch == row >> 2) { // the diagonal: to fp32 in every CTA, and out of A
+                    const int i = row & 3;
+                    const float x = i == 0 ? a.x : (i == 1 ? a.y : (i == 2 ? a.z : a.w));
+                    for (int p = 0; p < ctas; ++p)
+                        st_cluster_f32(g2::peer_addr(&sm.alpha[row], (uint32_t)p), x * (1.0f / (SX * SX)));
+                    a.x = i == 0 ? 0.0f : a.x, a.y = i == 1 ? 0.0f : a.y;
+                    a.z = i == 2 ? 0.0f : a.z, a.w = i == 3 ? 0.0f : a.w;
+                }
                 constexpr float F = SA / (SX * SX);
                 const uint32_t h0 = pack_half2(a.x * F, a.y * F), h1 = pack_half2(a.z * F, a.w * F);
                 const uint32_t to = (uint32_t)((ch >> 4) * SM_M * 128) + swz(row, (ch & 15) * 8);
@@ -336,13 +366,17 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             __syncwarp();
             g2::cluster_sync(); // A is whole in every CTA
         }
-        // ---- B = b A + c A A, in A's place
+        // ---- B' from A' and alpha, in A's place, and beta
         product(d_b, sm.ab[0], sm.ab[0], SM_M * 128, m16, m16, false);
         if (active) {
 #pragma unroll 1
             for (int ch = part; 32 * ch < m16; ch += 4) {
                 uint32_t v[32];
                 gm::tc_ld32(lanes + d_b + 32 * ch, v);
+                const float alpha_r = sm.alpha[r];
+                const float on_diag = take_diagonal(v, ch == quad ? lane : -1); // A' is zero there, so B' will be
+                if (ch == quad)
+                    sm.beta[r] = fmaf(fmaf(cc, alpha_r, cb), alpha_r, cc * (on_diag * (1.0f / (SA * SA))));
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     if (32 * ch + 8 * q < m16) {
@@ -353,17 +387,33 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float2 f = unpack_half2(w[k]);
-                            h[k] = pack_half2(fmaf(cc * (1.0f / SA), __uint_as_float(v[8 * q + 2 * k]), cb * f.x),
-                                              fmaf(cc * (1.0f / SA), __uint_as_float(v[8 * q + 2 * k + 1]), cb * f.y));
+                            const float2 ac = *reinterpret_cast<const float2 *>(&sm.alpha[32 * ch + 8 * q + 2 * k]);
+                            h[k] = pack_half2(fmaf(cc * (1.0f / SA), __uint_as_float(v[8 * q + 2 * k]),
+                                                   fmaf(cc, alpha_r + ac.x, cb) * f.x),
+                                              fmaf(cc * (1.0f / SA), __uint_as_float(v[8 * q + 2 * k + 1]),
+                                                   fmaf(cc, alpha_r + ac.y, cb) * f.y));
                         }
                         *reinterpret_cast<uint4 *>(p) = make_uint4(h[0], h[1], h[2], h[3]);
                     }
             }
         }
-        // ---- X = a X + B X, added in TMEM; its columns hold a X 2^18
+        // ---- X = (a + beta) X + B' X, added in TMEM; its columns hold X 2^18
+        __syncthreads(); // beta
+        if (active) {
+            const float scale = co.v[3 * s] + sm.beta[r];
+#pragma unroll 1
+            for (int ch = part; 32 * ch < n16; ch += 4) {
+                uint32_t v[32];
+                gm::tc_ld32(lanes + d_x + 32 * ch, v);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    v[k] = __float_as_uint(scale * __uint_as_float(v[k]));
+                tc_st32(lanes + d_x + 32 * ch, v);
+            }
+            tc_wait_st();
+        }
         product(d_x, sm.ab[0], sm.xt[0], SM_SLAB * 128, n16, m16, true);
         if (active) {
-            const float a_next = s + 1 < steps ? co.v[3 * (s + 1)] : 0.0f;
 #pragma unroll 1
             for (int ch = part; 32 * ch < n16; ch += 4) {
                 uint32_t v[32];
@@ -372,12 +422,9 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                 const int c0 = 32 * ch;
                 if (s + 1 < steps) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
+                    for (int k = 0; k < 32; ++k)
                         x[k] = __uint_as_float(v[k]) * (1.0f / SA);
-                        v[k] = __float_as_uint(a_next * __uint_as_float(v[k]));
-                    }
                     put_x(c0, x);
-                    tc_st32(lanes + d_x + c0, v);
                 } else {
                     uint32_t h[16];
 #pragma unroll
@@ -397,7 +444,6 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                     }
                 }
             }
-            tc_wait_st();
         }
     }
 

@@ -1,4 +1,5 @@
-"""Differentiable FP8 rowwise-scaled grouped matmul for MoE layers.
+"""Differentiable FP8 rowwise-scaled grouped matmul for MoE layers, and the
+router, dispatch and combine around it (moe_route, moe_dispatch, moe_combine).
 
 out[m] = a[m] . w[g]^T for the tokens m of expert g (groups given by device
 int32 ends `offs` along the token dimension), with every operand quantized

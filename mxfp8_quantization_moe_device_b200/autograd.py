@@ -191,31 +191,15 @@ def fp8_grouped_mm(a, w, offs):
 
 # ---------------------------------------------------------------- around the grouped products
 
-# Their autograd nodes are C++ (csrc_torch/moe_autograd.cpp): a call is a few
+# Their autograd nodes are C++ (csrc_torch/moe_ops.cpp): a call is a few
 # launches of microseconds, and a Python node would cost more than they do.
-
-_ops = None
-
-
-def _torch_ops():
-    global _ops
-    if _ops is None:
-        mxq.lib()
-        try:
-            from . import _torch_ops as ops
-        except ImportError as e:
-            raise RuntimeError("_torch_ops.so is not built; build it with "
-                               "`python -m mxfp8_quantization_moe_device_b200.build`") from e
-        _ops = ops
-    return _ops
-
 
 def moe_route(logits, top_k, *, valid=None, renormalize=False):
     """(weights (T, top_k) fp32, ids (T, top_k) int32, counts (E,) int32, loss
     () fp32) of router logits (T, E) bf16 or fp32; weights and loss are
     differentiable in the logits (the counts inside the loss are constants).
     See binding.moe_route."""
-    return _torch_ops().moe_route(logits, top_k, valid, renormalize)
+    return mxq.torch_ops().grad_route(logits, top_k, valid, renormalize)
 
 
 def moe_dispatch(x, ids, num_experts):
@@ -223,11 +207,11 @@ def moe_dispatch(x, ids, num_experts):
     (num_experts,)), ready for fp8_grouped_mm or mx_grouped_mm; M is T * top_k
     up to a multiple of 16 and the rows behind offs[-1] are zero. Entries with
     a negative id are dropped. Differentiable in x."""
-    return _torch_ops().moe_dispatch(x, ids, num_experts)
+    return mxq.torch_ops().grad_dispatch(x, ids, num_experts)
 
 
 def moe_combine(y, pos, weights, offs):
     """out (T, K): every token's rows y[pos[t]] weighted by weights (T, top_k)
     fp32 and summed; differentiable in y and weights. pos and offs as
     moe_dispatch returned them: together they name every row of y once."""
-    return _torch_ops().moe_combine(y, pos, weights, offs)
+    return mxq.torch_ops().grad_combine(y, pos, weights, offs)

@@ -5,6 +5,8 @@ library's CUDA kernels. PyTorch provides the device memory (outputs and the
 jagged workspace are allocated here with torch.empty) and the stream (the
 current torch stream of the input's device). There is no CPU fallback: when
 the library is missing, or a tensor is not on a CUDA device, the call raises.
+The operators around the experts' products take the same steps in C++
+(torch_ops).
 """
 import ctypes
 import os
@@ -568,60 +570,26 @@ def mx_grouped_gemm_wgrad(a, sfa, b, sfb, offs, tokens, *, out=None):
 
 # ---------------------------------------------------------------- experts: router, order, rows
 
-_DTYPES = {torch.bfloat16: BF16, torch.float32: FP32}
+# These go through _torch_ops.so (csrc_torch/moe_ops.cpp): checks, allocations
+# and the library's calls in C++, since the kernels of an ordinary call take
+# less time than the same steps here. A wrong tensor raises TypeError, a wrong
+# number ValueError, a status of the library MXQError, as elsewhere.
+
+_ops = None
 
 
-def _rows(t, name, dtype=None):
-    """A 2-D bf16 or fp32 CUDA tensor with contiguous rows that do not
-    overlap; returns (dtype code, rows, cols, row stride)."""
-    _cuda(t, name)
-    if t.dim() != 2 or t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{name} must be a 2-D {dtype or 'bfloat16 or float32'} tensor")
-    rows, cols = t.shape
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
-        raise TypeError(f"{name} must have contiguous rows that do not overlap")
-    return _DTYPES[t.dtype], rows, cols, (t.stride(0) if rows > 1 else cols)
-
-
-def _array(t, name, dtype, shape, dev):
-    """A contiguous input of this type and shape on `dev`."""
-    _cuda(t, name)
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
-        raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
-    return t
-
-
-def _output(t, name, dtype, shape, dev):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    return _out_buffer(t, name, shape, dtype.itemsize, dev, dtype)
-
-
-def _valid(valid, tokens, dev):
-    if valid is None:
-        return None
-    if isinstance(valid, torch.Tensor) and valid.dtype == torch.uint8:
-        return _array(valid, "valid", torch.uint8, (tokens,), dev)
-    return _array(valid, "valid", torch.bool, (tokens,), dev)
-
-
-def _positions(pos, tokens, dev):
-    _cuda(pos, "pos")
-    if pos.dim() != 2:
-        raise TypeError("pos must be a (tokens, top_k) int32 tensor")
-    return _array(pos, "pos", torch.int32, (pos.shape[0] if tokens is None else tokens, pos.shape[1]), dev)
-
-
-def _sized(name, dev, *args):
-    """A size that depends on the device, asked for with `dev` current."""
-    if dev.index == torch.cuda.current_device():
-        return getattr(lib(), name)(*args)
-    with torch.cuda.device(dev):
-        return getattr(lib(), name)(*args)
-
-
-def _workspace(nbytes, dev):
-    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+def torch_ops():
+    """Load _torch_ops.so once. Raises if it has not been built."""
+    global _ops
+    if _ops is None:
+        lib()
+        try:
+            from . import _torch_ops as ops
+        except ImportError as e:
+            raise RuntimeError("_torch_ops.so is not built; build it with "
+                               "`python -m mxfp8_quantization_moe_device_b200.build`") from e
+        _ops = ops
+    return _ops
 
 
 def moe_route(logits, top_k, *, valid=None, renormalize=False, weights=None, ids=None, counts=None, loss=None,
@@ -634,22 +602,7 @@ def moe_route(logits, top_k, *, valid=None, renormalize=False, weights=None, ids
     weight 0; a row with a NaN or +inf has ids -1 and NaN weights, and makes
     the loss NaN. loss_grad: optional (E,) fp32 buffer that receives d loss /
     d p[t][e], for moe_route_backward."""
-    code, T, E, ld = _rows(logits, "logits")
-    dev = logits.device
-    k = int(top_k)
-    if not 1 <= k <= E:
-        raise ValueError("top_k must lie in [1, experts]")
-    valid = _valid(valid, T, dev)
-    weights = _output(weights, "weights", torch.float32, (T, k), dev)
-    ids = _output(ids, "ids", torch.int32, (T, k), dev)
-    counts = _output(counts, "counts", torch.int32, (E,), dev)
-    loss = _output(loss, "loss", torch.float32, (), dev)
-    if loss_grad is not None:
-        _out_buffer(loss_grad, "loss_grad", (E,), 4, dev, torch.float32)
-    nbytes = _sized("moe_route_workspace_bytes", dev, T, E)
-    _call("moe_route", dev, _ptr(logits), code, T, E, ld, _ptr(valid), k, 1 if renormalize else 0, _ptr(weights),
-          _ptr(ids), _ptr(counts), _ptr(loss), _ptr(loss_grad), _ptr(_workspace(nbytes, dev)), nbytes)
-    return weights, ids, counts, loss
+    return torch_ops().moe_route(logits, top_k, valid, renormalize, weights, ids, counts, loss, loss_grad)
 
 
 def moe_route_backward(logits, weights, ids, loss_grad, grad_weights, grad_loss, *, valid=None, renormalize=False,
@@ -657,24 +610,8 @@ def moe_route_backward(logits, weights, ids, loss_grad, grad_weights, grad_loss,
     """Gradient of moe_route by the logits, (T, E) of their type, from what
     the forward returned and wrote (weights, ids, loss_grad) and the gradients
     of weights (T, top_k) fp32 and of loss () fp32; either may be None."""
-    code, T, E, ld = _rows(logits, "logits")
-    dev = logits.device
-    _cuda(ids, "ids")
-    if ids.dim() != 2 or not 1 <= ids.shape[1] <= E:
-        raise TypeError("ids must be a (tokens, top_k) int32 tensor")
-    k = ids.shape[1]
-    _array(ids, "ids", torch.int32, (T, k), dev)
-    _array(weights, "weights", torch.float32, (T, k), dev)
-    if grad_weights is not None:
-        _array(grad_weights, "grad_weights", torch.float32, (T, k), dev)
-    if grad_loss is not None:
-        _array(grad_loss, "grad_loss", torch.float32, (), dev)
-        _array(loss_grad, "loss_grad", torch.float32, (E,), dev)
-    out = _output(out, "out", logits.dtype, (T, E), dev)
-    _call("moe_route_backward", dev, _ptr(logits), code, T, E, ld, _ptr(_valid(valid, T, dev)), k,
-          1 if renormalize else 0, _ptr(weights), _ptr(ids), _ptr(loss_grad), _ptr(grad_weights), _ptr(grad_loss),
-          _ptr(out))
-    return out
+    return torch_ops().moe_route_backward(logits, weights, ids, loss_grad, grad_weights, grad_loss, valid,
+                                          renormalize, out)
 
 
 def moe_dispatch_plan(ids, num_experts, *, pos=None, offs=None):
@@ -683,20 +620,7 @@ def moe_dispatch_plan(ids, num_experts, *, pos=None, offs=None):
     id is negative; offs (num_experts,) int32, the group ends that the grouped
     GEMMs take). An id >= num_experts is dropped and reported by
     device_status."""
-    _cuda(ids, "ids")
-    if ids.dim() != 2:
-        raise TypeError("ids must be a (tokens, top_k) int32 tensor")
-    dev = ids.device
-    _array(ids, "ids", torch.int32, ids.shape, dev)
-    E = int(num_experts)
-    if E < 1:
-        raise ValueError("num_experts must be positive")
-    pos = _output(pos, "pos", torch.int32, ids.shape, dev)
-    offs = _output(offs, "offs", torch.int32, (E,), dev)
-    ws = _workspace(lib().moe_dispatch_plan_workspace_bytes(ids.numel(), E), dev)
-    _call("moe_dispatch_plan", dev, _ptr(ids), ids.numel(), E, _ptr(pos), _ptr(offs), _ptr(ws),
-          ws.numel() if ws is not None else 0)
-    return pos, offs
+    return torch_ops().moe_dispatch_plan(ids, num_experts, pos, offs)
 
 
 def moe_dispatch_rows(entries):
@@ -710,17 +634,7 @@ def moe_dispatch(x, pos, offs, *, out=None):
     offs[-1] on zero. x (T, K) bf16 or fp32 with contiguous rows, pos and offs
     from moe_dispatch_plan. Returns out (M, K) with M = moe_dispatch_rows(T *
     top_k), or fills the given out (any number of rows)."""
-    code, T, K, ld = _rows(x, "x")
-    dev = x.device
-    _positions(pos, T, dev)
-    _offsets(offs, dev)
-    M = moe_dispatch_rows(pos.numel()) if out is None else out.shape[0]
-    out = _output(out, "out", x.dtype, (M, K), dev)
-    if pos.shape[1] == 0:
-        raise ValueError("pos must have at least one slot per token")
-    _call("moe_dispatch", dev, _ptr(x), code, T, K, ld, _ptr(pos), pos.shape[1], _ptr(offs), offs.numel(), _ptr(out),
-          M)
-    return out
+    return torch_ops().moe_dispatch(x, pos, offs, out)
 
 
 def moe_combine(y, pos, weights=None, *, out=None):
@@ -728,17 +642,7 @@ def moe_combine(y, pos, weights=None, *, out=None):
     with pos >= 0, in fp32, rounded once. y (M, K) bf16 or fp32 with
     contiguous rows, weights (T, top_k) fp32 or None (ones). Returns out
     (T, K); rows of y that no slot names are not read."""
-    code, M, K, ld = _rows(y, "y")
-    dev = y.device
-    _positions(pos, None, dev)
-    T, k = pos.shape
-    if k == 0:
-        raise ValueError("pos must have at least one slot per token")
-    if weights is not None:
-        _array(weights, "weights", torch.float32, (T, k), dev)
-    out = _output(out, "out", y.dtype, (T, K), dev)
-    _call("moe_combine", dev, _ptr(y), code, M, K, ld, _ptr(pos), _ptr(weights), T, k, _ptr(out))
-    return out
+    return torch_ops().moe_combine(y, pos, weights, out)
 
 
 def moe_combine_backward(grad_out, y, pos, weights, offs, *, need_y=True, need_weights=True, grad_y=None,
@@ -747,24 +651,14 @@ def moe_combine_backward(grad_out, y, pos, weights, offs, *, need_y=True, need_w
     row pos[t][j], zero from offs[-1] on; grad_weights (T, top_k) fp32 =
     <grad_out[t], y[pos[t][j]]>, 0 for a dropped slot). What is not needed is
     returned as None."""
-    code, M, K, ld = _rows(y, "y")
-    dev = y.device
-    _, T, _, ldg = _rows(grad_out, "grad_out", y.dtype)
-    _positions(pos, T, dev)
-    k = pos.shape[1]
-    if grad_out.shape[1] != K or grad_out.device != dev or k == 0:
-        raise TypeError("shape mismatch between grad_out, y and pos")
-    _offsets(offs, dev)
-    if weights is not None:
-        _array(weights, "weights", torch.float32, (T, k), dev)
-    grad_y = _output(grad_y, "grad_y", y.dtype, (M, K), dev) if need_y else None
-    grad_weights = _output(grad_weights, "grad_weights", torch.float32, (T, k), dev) if need_weights else None
-    _call("moe_combine_backward", dev, _ptr(grad_out), ldg, _ptr(y), ld, code, M, K, _ptr(pos), _ptr(weights), T, k,
-          _ptr(offs), offs.numel(), _ptr(grad_y), _ptr(grad_weights))
-    return grad_y, grad_weights
+    return torch_ops().moe_combine_backward(grad_out, y, pos, weights, offs, need_y, need_weights, grad_y,
+                                            grad_weights)
 
 
 # ---------------------------------------------------------------- orthogonalisation
+
+_DTYPES = {torch.bfloat16: BF16, torch.float32: FP32}
+
 
 def newton_schulz(g, *, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, out=None):
     """Orthogonalise every matrix of g (E, N, K) (or one, (N, K)) bf16 or fp32
@@ -785,10 +679,13 @@ def newton_schulz(g, *, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-
     co = (ctypes.c_float * (3 * steps))(*(float(v) for r in rows for v in r))
     dev = g.device
     E, N, K = g.shape if g.dim() == 3 else (1, *g.shape)
-    out = _output(out, "out", torch.bfloat16, g.shape, dev)
-    ws = _workspace(_sized("newton_schulz_workspace_bytes", dev, E, N, K, steps), dev)
-    _call("newton_schulz", dev, _ptr(g), _DTYPES[g.dtype], E, N, K, steps, co, float(eps), _ptr(out), _ptr(ws),
-          ws.numel() if ws is not None else 0)
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=dev)
+    _out_buffer(out, "out", g.shape, 2, dev, torch.bfloat16)
+    with torch.cuda.device(dev):
+        nbytes = lib().newton_schulz_workspace_bytes(E, N, K, steps)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _call("newton_schulz", dev, _ptr(g), _DTYPES[g.dtype], E, N, K, steps, co, float(eps), _ptr(out), _ptr(ws), nbytes)
     return out
 
 

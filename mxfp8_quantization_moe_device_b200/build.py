@@ -1,5 +1,5 @@
 """Build libmxq.so (the sm_100a CUDA library) in-tree with nvcc, and
-_torch_ops.so, the C++ autograd nodes that call it, with g++.
+_torch_ops.so, the torch calls and autograd nodes in C++ that use it, with g++.
 
 The library is one translation unit (csrc/mxq.cu includes every kernel) so
 that the device status word is a single symbol without relocatable device
@@ -16,7 +16,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmxq.so")
-TORCH_SRC = os.path.join(HERE, "csrc_torch", "moe_autograd.cpp")
+TORCH_SRC = os.path.join(HERE, "csrc_torch", "moe_ops.cpp")
 TORCH_OPS = os.path.join(HERE, "_torch_ops.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -690,6 +690,9 @@ constexpr int PLAN_WARPS = PLAN_THREADS / 32;
 constexpr int PLAN_R = 4;                                // entries per thread and tile
 constexpr int PLAN_TILE = PLAN_THREADS * PLAN_R;         // 2048
 constexpr int PLAN_MAX_CHUNKS = 128;
+constexpr int PLAN_SELF_CHUNKS = 4;                      // up to here every CTA counts all entries itself:
+                                                         // 9.0 us at 8192 entries against 8 for two kernels,
+                                                         // and a launch less on the host; 14 at 16000
 
 // dynamic shared memory of the ranking kernel: first positions, sums over the
 // chunks, and the warps' counters
@@ -732,7 +735,9 @@ __global__ void __launch_bounds__(moe::PLAN_THREADS)
         hist[(size_t)blockIdx.x * E + e] = s_h[e];
 }
 
-// hist (C, E) of pass 1, or NULL when the grid is one CTA over one tile
+// hist (C, E) of pass 1, or NULL when the grid is one CTA over one tile, or
+// few enough that each counts the entries before and behind its own (a launch
+// less)
 __global__ void __launch_bounds__(moe::PLAN_THREADS)
     k_moe_plan_rank(const int32_t *__restrict__ ids, int64_t n, int E, int64_t chunk, const int *__restrict__ hist,
                     int C, int32_t *__restrict__ pos, int32_t *__restrict__ offs)
@@ -800,6 +805,34 @@ __global__ void __launch_bounds__(moe::PLAN_THREADS)
         __syncthreads();
         set_base();
     }
+    if (!hist && C > 1) {
+        auto count = [&](int64_t from, int64_t to, int *into) {
+            for (int64_t i0 = from; i0 < to; i0 += 8 * PLAN_THREADS) {
+                int e[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    e[u] = entry_expert(ids, i0 + u * PLAN_THREADS + tid, to, E);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    // a warp of one expert adds once; others' equals queue at the address
+                    const int first = __shfl_sync(0xffffffffu, e[u], 0);
+                    if (__all_sync(0xffffffffu, e[u] == first)) {
+                        if (lane == 0 && first >= 0)
+                            atomicAdd(&into[first], 32);
+                    } else if (e[u] >= 0) {
+                        atomicAdd(&into[e[u]], 1);
+                    }
+                }
+            }
+        };
+        count(0, lo, before);
+        count(lo, n, total);
+        __syncthreads();
+        for (int e = tid; e < E; e += PLAN_THREADS)
+            total[e] += before[e];
+        __syncthreads();
+        set_base();
+    }
     for (int64_t i0 = lo; i0 < hi || i0 == 0; i0 += PLAN_TILE) {
         for (int e = tid; e < PLAN_WARPS * E; e += PLAN_THREADS)
             cnt[e] = 0;
@@ -832,7 +865,7 @@ __global__ void __launch_bounds__(moe::PLAN_THREADS)
             total[x] = sum; // from here on the tile's counts
         }
         __syncthreads();
-        if (!hist)
+        if (C == 1)
             set_base(); // the only tile
 #pragma unroll
         for (int r = 0; r < PLAN_R; ++r) {

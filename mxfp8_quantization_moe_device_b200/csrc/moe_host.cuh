@@ -242,7 +242,7 @@ size_t moe_dispatch_plan_workspace_bytes(int64_t entries, int64_t experts)
         return 0;
     int64_t chunks, chunk;
     plan_chunks(entries, &chunks, &chunk);
-    return chunks == 1 && entries <= moe::PLAN_TILE ? 0 : (size_t)chunks * experts * 4;
+    return chunks <= moe::PLAN_SELF_CHUNKS ? 0 : (size_t)chunks * experts * 4;
 }
 
 int moe_dispatch_plan(const int32_t *ids, int64_t entries, int64_t experts, int32_t *pos, int32_t *offs,

@@ -3,9 +3,8 @@
 //
 // A CTA holds a slab of up to 256 columns of X (m <= 128 rows): hi of X and of
 // X^T as fp16 in shared memory in the layout that tcgen05.mma reads, X itself
-// in fp32 in TMEM, as the accumulator of the step's last product: its rows are
-// multiplied by a + beta_r there and B' X added to them by the tensor core, so X
-// is never rounded.
+// in fp32 in half of TMEM, so that it is never rounded; the other half takes
+// the products, A and A A and then, both read, B' X.
 // A matrix with more columns takes a cluster of up to sixteen CTAs: each
 // multiplies its slab with itself, the partial 128 x 128 products are summed
 // over distributed shared memory in rank order (every CTA sums some rows and
@@ -155,7 +154,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     __syncthreads();
     gm::tc_fence_after();
     const uint32_t lanes = sm.tmem_base + ((uint32_t)(32 * quad) << 16);
-    const uint32_t d_x = 0, d_a = SM_SLAB, d_b = SM_SLAB + SM_M; // TMEM columns of X, A, A A
+    const uint32_t d_x = 0, d_a = SM_SLAB, d_b = SM_SLAB + SM_M, d_y = SM_SLAB; // TMEM columns of X, A, A A, B' X
 
     // ---- G into TMEM, its sum of squares
     double sq = 0.0;
@@ -261,10 +260,10 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
                 x[k] = (__uint_as_float(v[k]) * f0) * f1;
-                v[k] = __float_as_uint(SA * x[k]);
+                v[k] = __float_as_uint(x[k]);
             }
             put_x(32 * ch, x);
-            tc_st32(lanes + d_x + 32 * ch, v);
+            tc_st32(lanes + d_x + 32 * ch, v); // X 2^8
         }
         tc_wait_st();
     }
@@ -272,7 +271,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     uint32_t phase = 0;
     // everything that the tensor core will read is written: then one thread
     // multiplies P (128 x 16 ks) by Q^T (N rows) into TMEM column d
-    auto product = [&](uint32_t d, const uint8_t *P, const uint8_t *Q, int q_block, int N, int K, bool add) {
+    auto product = [&](uint32_t d, const uint8_t *P, const uint8_t *Q, int q_block, int N, int K) {
         fence_proxy_async_all();
         gm::tc_fence_before();
         __syncthreads();
@@ -282,7 +281,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             for (int k = 0; k < K; k += 16) {
                 const uint64_t ad = gm::smem_desc_k128(smem_u32(P) + (k >> 6) * SM_M * 128) + 2 * ((k >> 4) & 3);
                 const uint64_t bd = gm::smem_desc_k128(smem_u32(Q) + (k >> 6) * q_block) + 2 * ((k >> 4) & 3);
-                mma_f16(sm.tmem_base + d, ad, bd, id, add || k > 0 ? 1u : 0u);
+                mma_f16(sm.tmem_base + d, ad, bd, id, k > 0 ? 1u : 0u);
             }
             gm::tc_commit(&sm.bar);
         }
@@ -296,7 +295,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     for (int s = 0; s < steps; ++s) {
         const float cb = co.v[3 * s + 1], cc = co.v[3 * s + 2];
         // ---- A = X X^T
-        product(d_a, sm.xh[0], sm.xh[0], SM_M * 128, m16, n16, false);
+        product(d_a, sm.xh[0], sm.xh[0], SM_M * 128, m16, n16);
         if (active) {
 #pragma unroll 1
             for (int ch = part; 32 * ch < m16; ch += 4) {
@@ -367,7 +366,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             g2::cluster_sync(); // A is whole in every CTA
         }
         // ---- B' from A' and alpha, in A's place, and beta
-        product(d_b, sm.ab[0], sm.ab[0], SM_M * 128, m16, m16, false);
+        product(d_b, sm.ab[0], sm.ab[0], SM_M * 128, m16, m16);
         if (active) {
 #pragma unroll 1
             for (int ch = part; 32 * ch < m16; ch += 4) {
@@ -397,40 +396,33 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                     }
             }
         }
-        // ---- X = (a + beta) X + B' X, added in TMEM; its columns hold X 2^18
-        __syncthreads(); // beta
+        // ---- X = (a + beta) X + B' X
+        product(d_y, sm.ab[0], sm.xt[0], SM_SLAB * 128, n16, m16);
         if (active) {
             const float scale = co.v[3 * s] + sm.beta[r];
 #pragma unroll 1
             for (int ch = part; 32 * ch < n16; ch += 4) {
-                uint32_t v[32];
-                gm::tc_ld32(lanes + d_x + 32 * ch, v);
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    v[k] = __float_as_uint(scale * __uint_as_float(v[k]));
-                tc_st32(lanes + d_x + 32 * ch, v);
-            }
-            tc_wait_st();
-        }
-        product(d_x, sm.ab[0], sm.xt[0], SM_SLAB * 128, n16, m16, true);
-        if (active) {
-#pragma unroll 1
-            for (int ch = part; 32 * ch < n16; ch += 4) {
-                uint32_t v[32];
+                uint32_t v[32], y[32];
                 float x[32];
-                gm::tc_ld32(lanes + d_x + 32 * ch, v);
+                gm::tc_ld32_nowait(lanes + d_x + 32 * ch, v);
+                gm::tc_ld32_nowait(lanes + d_y + 32 * ch, y);
+                gm::tc_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) // behind n16 no product was written, and X is zero
+                    x[k] = fmaf(scale, __uint_as_float(v[k]),
+                                32 * ch + (k & 16) < n16 ? __uint_as_float(y[k]) * (1.0f / SA) : 0.0f);
                 const int c0 = 32 * ch;
                 if (s + 1 < steps) {
+                    put_x(c0, x);
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        x[k] = __uint_as_float(v[k]) * (1.0f / SA);
-                    put_x(c0, x);
+                        v[k] = __float_as_uint(x[k]);
+                    tc_st32(lanes + d_x + c0, v);
                 } else {
                     uint32_t h[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
-                        h[k] = gm::pack_bf16x2(__uint_as_float(v[2 * k]) * (1.0f / (SA * SX)),
-                                               __uint_as_float(v[2 * k + 1]) * (1.0f / (SA * SX)));
+                        h[k] = gm::pack_bf16x2(x[2 * k] * (1.0f / SX), x[2 * k + 1] * (1.0f / SX));
                     uint16_t *dst = out + (int64_t)e * rows * cols;
                     if (tall) {
                         dst += (int64_t)(c_base + c0) * m + r;
@@ -444,6 +436,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                     }
                 }
             }
+            tc_wait_st();
         }
     }
 

@@ -162,7 +162,8 @@ def test_host_checks():
 def test_workspace_sizes():
     L = mxq.lib()
     assert L.moe_dispatch_plan_workspace_bytes(2048, 64) == 0
-    assert L.moe_dispatch_plan_workspace_bytes(2049, 64) == 2 * 64 * 4
+    assert L.moe_dispatch_plan_workspace_bytes(8192, 64) == 0
+    assert L.moe_dispatch_plan_workspace_bytes(8193, 64) == 5 * 64 * 4
     assert L.moe_dispatch_plan_workspace_bytes(128 * 2048 + 1, 64) == 65 * 64 * 4
     assert L.moe_route_workspace_bytes(-1, 64) == 0 and L.moe_route_workspace_bytes(16, 2000) == 0
 
@@ -348,7 +349,8 @@ def test_route_no_tokens_strides_and_many_tokens():
 # ------------------------------------------------------------ order by expert
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,E,k", [(0, 5, 2), (1, 1, 1), (5, 3, 2), (100, 16, 4), (1024, 60, 8), (1025, 64, 8),
-                                   (3000, 7, 6), (2000, 1024, 32), (300, 1000, 5)])
+                                   (3000, 7, 6), (2000, 1024, 32), (300, 1000, 5), (4096, 4, 4), (4000, 3, 2),
+                                   (8193, 33, 1), (8192, 1, 1)])
 @pytest.mark.parametrize("dropped", [0.0, 0.3])
 def test_plan(T, E, k, dropped):
     ids = ids_of(T, E, k, T + E + k, dropped)

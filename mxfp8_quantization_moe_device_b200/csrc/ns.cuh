@@ -68,7 +68,7 @@ constexpr int THREADS = (EPI_WARPS + 2) * 32;
 constexpr int ACC = 2;
 constexpr int CHUNK = 32;              // an epilogue step: 32 rows x 32 columns per warp
 constexpr int CHUNK_BYTES = CHUNK * CHUNK * 2;
-constexpr int MAX_PARTS = 64;          // partial sums of squares per matrix
+constexpr int MAX_PARTS = 256;         // partial sums of squares per matrix
 
 constexpr float SX = 256.0f;           // stored X  = X 2^8
 constexpr float SA = 1024.0f;          // stored A', B' = A', B' 2^10

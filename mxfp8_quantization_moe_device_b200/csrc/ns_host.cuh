@@ -18,7 +18,7 @@ NsPlan ns_plan(int64_t E, int64_t rows, int64_t cols, int32_t steps)
     p.n = std::max(rows, cols);
     p.ldx = (p.n + 7) / 8 * 8;
     p.ldt = (p.m + 7) / 8 * 8;
-    p.parts = (int)std::min<int64_t>(ns::MAX_PARTS, (rows * cols + 4095) / 4096);
+    p.parts = (int)std::min<int64_t>(ns::MAX_PARTS, (rows * cols + 8191) / 8192);
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;

@@ -77,9 +77,6 @@ template <typename T, int V> MXQ_DEV Vec<T, V> ld_now(const T *p)
     return x;
 }
 
-// the value, or zero whatever it is (a NaN times zero would stay)
-MXQ_DEV float keep_if(float v, uint32_t mask) { return __uint_as_float(__float_as_uint(v) & mask); }
-
 // unsigned key in the order of the float (-inf lowest; the caller has turned
 // -0 into +0 and has no NaN)
 MXQ_DEV uint32_t order_key(float f)
@@ -941,9 +938,9 @@ __global__ void __launch_bounds__(moe::ROW_THREADS)
 // warp takes one of `parts` runs of `run` vectors of a token's row and walks it
 // 32 * U vectors at a time (one run per row when there are tokens enough: the
 // slots are then looked up once a row). The loads of J slots are issued
-// together, without a branch or predicate between them: a dropped slot reads
-// the token's first row that is there and what it read is cleared, a lane
-// behind the run's end reads the run's last vector and stores nothing.
+// together: a branch that is the same for the whole warp leaves out a dropped
+// slot, a lane behind the run's end reads the run's last vector and stores
+// nothing.
 template <typename T, int V, int U, int J>
 __global__ void __launch_bounds__(moe::ROW_THREADS, 4)
     k_moe_combine(const T *__restrict__ y, int64_t M, int64_t K, int64_t ld, const int32_t *__restrict__ pos,
@@ -955,15 +952,16 @@ __global__ void __launch_bounds__(moe::ROW_THREADS, 4)
     const uint32_t nvec = (uint32_t)(K / V), all = tokens * parts, stride = gridDim.x * ROW_WARPS;
     for (uint32_t w = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5); w < all; w += stride) {
         const uint32_t t = w / parts, v_lo = (w - t * parts) * run, v_hi = min(v_lo + run, nvec);
-        int64_t row = -1; // lane j: slot j's row and weight
+        const T *row = nullptr; // lane j: slot j's row and weight
         float wl = 0.0f;
         if (lane < k) {
-            const int64_t i = (int64_t)t * k + lane;
-            row = slot_row(pos, i, M);
-            wl = row < 0 ? 0.0f : (weights ? weights[i] : 1.0f);
+            const int64_t i = (int64_t)t * k + lane, r = slot_row(pos, i, M);
+            if (r >= 0) {
+                row = y + r * ld;
+                wl = weights ? weights[i] : 1.0f;
+            }
         }
-        const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
-        const int64_t any = __shfl_sync(0xffffffffu, row, there ? __ffs(there) - 1 : 0);
+        const uint32_t there = __ballot_sync(0xffffffffu, row != nullptr);
         T *dst = out + (int64_t)t * K;
 #pragma unroll 1
         for (uint32_t v0 = v_lo + lane; v0 - lane < v_hi; v0 += 32 * U) {
@@ -978,26 +976,28 @@ __global__ void __launch_bounds__(moe::ROW_THREADS, 4)
             for (int u = 0; u < U; ++u)
                 at[u] = min(v0 + 32 * u, v_hi - 1) * V;
 #pragma unroll 1
-            for (int j0 = 0; j0 < k && there; j0 += J) {
+            for (int j0 = 0; j0 < k; j0 += J) {
+                const uint32_t on = there >> j0; // bit j: slot j0 + j has a row
                 Vec<T, V> r[J][U];
 #pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    const int64_t s = __shfl_sync(0xffffffffu, row, (j0 + j) & 31);
-                    const T *p = y + (s >= 0 ? s : any) * ld;
+                for (int j = 0; j < J; ++j)
+                    if (on >> j & 1u) {
+                        const T *p = reinterpret_cast<const T *>(
+                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), j0 + j));
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        r[j][u] = ld_now<T, V>(p + at[u]);
-                }
+                        for (int u = 0; u < U; ++u)
+                            r[j][u] = ld_now<T, V>(p + at[u]);
+                    }
 #pragma unroll
-                for (int j = 0; j < J; ++j) { // lanes from k on hold no slot
-                    const float wj = __shfl_sync(0xffffffffu, wl, (j0 + j) & 31);
-                    const uint32_t mask = (there >> ((j0 + j) & 31)) & 1u ? 0xffffffffu : 0u;
+                for (int j = 0; j < J; ++j)
+                    if (on >> j & 1u) {
+                        const float wj = __shfl_sync(0xffffffffu, wl, j0 + j);
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
+                        for (int u = 0; u < U; ++u)
 #pragma unroll
-                        for (int i = 0; i < V; ++i)
-                            acc[u][i] = fmaf(wj, keep_if(Elem<T>::get(r[j][u].v[i]), mask), acc[u][i]);
-                }
+                            for (int i = 0; i < V; ++i)
+                                acc[u][i] = fmaf(wj, Elem<T>::get(r[j][u].v[i]), acc[u][i]);
+                    }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -1045,19 +1045,27 @@ __global__ void __launch_bounds__(moe::ROW_THREADS)
         const float wt = weights ? weights[w] : 1.0f;
         float acc = 0.0f;
         const T *yr = y + s * ldy;
-#pragma unroll 1
-        for (uint32_t v0 = lane; v0 - lane < nvec; v0 += 32 * U) {
-            Vec<T, V> a[U], b[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) { // behind the end: the last vector, unused
-                const uint32_t at = min(v0 + 32 * u, nvec - 1) * V;
-                a[u] = ld_now<T, V>(g + at);
-                if (dw)
-                    b[u] = ld_now<T, V>(yr + at);
-            }
+        T *out = dy + s * K;
+        // 32 * U vectors from v0 on: with FULL all of them exist, and a lane's
+        // lie at fixed distances; else a lane behind the end reads the last one
+        auto block = [&](uint32_t v0, auto full) {
+            constexpr bool FULL = decltype(full)::value;
+            uint32_t at[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (v0 + 32 * u < nvec) {
+                at[u] = (FULL ? v0 + lane + 32 * u : min(v0 + lane + 32 * u, nvec - 1)) * V;
+            Vec<T, V> a[U], b[U];
+            const T *ga = g + at[0], *ya = yr + at[0];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                a[u] = ld_now<T, V>(FULL ? ga + 32 * u * V : ga + (at[u] - at[0]));
+                if (dw)
+                    b[u] = ld_now<T, V>(FULL ? ya + 32 * u * V : ya + (at[u] - at[0]));
+            }
+            T *d = out + at[0];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (FULL || v0 + lane + 32 * u < nvec) {
                     Vec<T, V> o;
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
@@ -1067,9 +1075,15 @@ __global__ void __launch_bounds__(moe::ROW_THREADS)
                         o.v[i] = Elem<T>::put(wt * f);
                     }
                     if (dy)
-                        st_vec<T, V>(dy + s * K + (int64_t)(v0 + 32 * u) * V, o);
+                        st_vec<T, V>(d + 32 * u * V, o);
                 }
-        }
+        };
+        uint32_t v0 = 0;
+#pragma unroll 1
+        for (; v0 + 32 * U <= nvec; v0 += 32 * U)
+            block(v0, std::true_type{});
+        if (v0 < nvec)
+            block(v0, std::false_type{});
         if (dw) {
 #pragma unroll
             for (int o = 16; o; o >>= 1)

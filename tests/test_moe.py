@@ -480,6 +480,39 @@ def test_rows_strides_offsets_and_poison(dtype):
 
 
 @pytest.mark.gpu
+def test_more_than_2_31_elements():
+    # dispatched rows and logits whose last elements lie behind 2^31
+    T, E, k, K = 66000, 12, 8, 4096
+    ids = torch.stack([torch.randperm(E, device=DEV)[:k] for _ in range(50)]).repeat(T // 50, 1).to(torch.int32)
+    ids[-7:, 3] = -1
+    x = torch.randn(T, K, device=DEV).bfloat16()
+    pos, offs = mxq.moe_dispatch_plan(ids, E)
+    xs = mxq.moe_dispatch(x, pos, offs)
+    assert xs.numel() > 2 ** 31 and int(offs[-1]) == T * k - 7
+    assert bool((xs[int(offs[-1]):] == 0).all())
+    top = torch.argsort(pos.reshape(-1))[-3000:]  # the entries of the last rows
+    assert torch.equal(xs[pos.reshape(-1)[top].long()], x[top // k])
+    w = torch.full((T, k), 0.25, device=DEV)
+    got = mxq.moe_combine(xs, pos, w)  # eight equal rows at a quarter: exact
+    assert torch.equal(got[:-7], (2 * x[:-7].float()).bfloat16())
+    dy, dw = mxq.moe_combine_backward(x, xs, pos, w, offs)
+    assert torch.equal(dy[pos.reshape(-1)[top].long()], (0.25 * x[top // k].float()).bfloat16())
+    sq = x.double().square().sum(1)
+    assert bool(((dw[:-7].double() - sq[:-7, None]).abs() <= K * 2.0 ** -24 * sq[:-7, None]).all())
+    del xs, dy
+    T, E = 2100000, 1024
+    l = torch.randn(T, E, device=DEV, dtype=torch.bfloat16)
+    w, ids, counts, loss = mxq.moe_route(l, 2)
+    assert l.numel() > 2 ** 31 and int(counts.sum()) == 2 * T
+    tail = l[-1000:]
+    ri = torch.sort(tail.float(), dim=1, descending=True, stable=True).indices[:, :2]
+    p = torch.softmax(tail.double(), 1).gather(1, ri)
+    assert torch.equal(ids[-1000:].long(), ri)
+    near(w[-1000:], p.cpu(), 2.0 ** -18 * p.cpu(), "weights")
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
 def test_refusals_of_the_binding():
     x = torch.randn(8, 64, device=DEV).bfloat16()
     ids = torch.zeros(8, 2, dtype=torch.int32, device=DEV)

@@ -147,6 +147,14 @@ def test_newton_schulz(E, N, K, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("E,N,K", [(2, 2500, 5001), (1, 9000, 3300), (300, 130, 140)])
+def test_larger(E, N, K):
+    g = matrices(E, N, K, torch.bfloat16, 6)
+    check(mxq.newton_schulz(g), g, [COEF] * 5)
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["noise", "decay"])
 @pytest.mark.parametrize("N,K", [(200, 500), (384, 256)])
 def test_spectra(kind, N, K):

@@ -450,7 +450,7 @@ size_t fp8_quant_jagged_colwise_noalloc_max_scratch_bytes(void);
  * Around the experts' grouped GEMMs: the router, the order of the tokens by
  * expert, and the rows' way into that order and back. Rows are bf16 or fp32
  * (mxq_dtype); sums are taken in fp32 or more, in a fixed order, and rounded
- * once.
+ * once. Outputs overlap neither inputs nor one another.
  * ------------------------------------------------------------------------ */
 typedef enum mxq_dtype {
     MXQ_BF16 = 0,
@@ -472,8 +472,8 @@ typedef enum mxq_dtype {
  * never chosen; where fewer than top_k experts are left the slots' ids are -1
  * and their weights 0. A row with a NaN or +inf chooses nothing, its weights
  * are NaN, and so is the loss. experts <= 1024, top_k <= 32. workspace:
- * moe_route_workspace_bytes() bytes, 256-byte aligned, not shared by calls
- * that overlap on the GPU. */
+ * moe_route_workspace_bytes() bytes (asked for with the device of the call
+ * current), 256-byte aligned, not shared by calls that overlap on the GPU. */
 size_t moe_route_workspace_bytes(int64_t tokens, int64_t experts);
 int moe_route(const void *logits, int32_t dtype, int64_t tokens, int64_t experts, int64_t row_stride,
               const uint8_t *valid, int32_t top_k, int32_t renormalize, float *weights, int32_t *ids,
@@ -531,7 +531,7 @@ int moe_combine_backward(const void *grad_out, int64_t grad_row_stride, const vo
  *   X = G / (|G|_F + eps), transposed when rows > cols; then `steps` times,
  *   with (a, b, c) = coefficients[3 s], [3 s + 1], [3 s + 2] (host memory):
  *   A = X X^T;  X = a X + (b A + c A A) X
- * out (batch, rows, cols) bf16, row-major. The products run in fp16 with fp32
+ * out (batch, rows, cols) bf16, row-major, not overlapping g. The products run in fp16 with fp32
  * sums on X held in 22 bits; singular values should stay below 4 on the way
  * (they do for the usual coefficients) and coefficients within [-16, 16]. A
  * matrix of zeros gives zeros; a NaN or infinity makes its own matrix NaN and

@@ -665,8 +665,8 @@ def newton_schulz(g, *, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-
     by Newton-Schulz products: X = G / (|G|_F + eps), then steps times A = X
     X^T, X = a X + (b A + c A A) X (on the transpose when N > K).
     coefficients: one (a, b, c) for all steps or one per step. Returns bf16 of
-    g's shape. Takes the expert weight gradients (or their momentum) that the
-    weight-gradient GEMMs return."""
+    g's shape; out, where given, must not overlap g. Takes the expert weight
+    gradients (or their momentum) that the weight-gradient GEMMs return."""
     _cuda(g, "g")
     if g.dim() not in (2, 3) or g.dtype not in _DTYPES or not g.is_contiguous():
         raise TypeError("g must be a contiguous (E, N, K) or (N, K) bfloat16 or float32 tensor")
@@ -682,6 +682,9 @@ def newton_schulz(g, *, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-
     if out is None:
         out = torch.empty(g.shape, dtype=torch.bfloat16, device=dev)
     _out_buffer(out, "out", g.shape, 2, dev, torch.bfloat16)
+    lo, g_lo = out.data_ptr(), g.data_ptr()
+    if lo < g_lo + g.numel() * g.element_size() and g_lo < lo + 2 * g.numel():
+        raise ValueError("out must not overlap g")
     with torch.cuda.device(dev):
         nbytes = lib().newton_schulz_workspace_bytes(E, N, K, steps)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None

@@ -59,7 +59,7 @@ int route_check(const void *logits, int32_t dtype, int64_t T, int64_t E, int64_t
 {
     if (T < 0 || E < 1 || k < 1 || k > E || (T > 0 && ld < E))
         return MXQ_ERR_SHAPE;
-    if (!dtype_ok(dtype) || E > moe::MAX_E || k > moe::MAX_K || T * k >= (int64_t(1) << 31))
+    if (!dtype_ok(dtype) || E > moe::MAX_E || k > moe::MAX_K || T >= (int64_t(1) << 31) / k)
         return MXQ_ERR_UNSUPPORTED;
     if (T > 0 && !logits)
         return MXQ_ERR_NULL;

@@ -9,7 +9,9 @@
 // again in the engine's thread); here 13, 14 and about 60. Nothing is computed
 // here: checks, torch allocations on the current stream, the library's calls,
 // and what the backward keeps.
+#include <ATen/MemoryOverlap.h>
 #include <ATen/cuda/CUDAContext.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/extension.h>
@@ -69,11 +71,17 @@ Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Device &dev)
     return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
 }
 using Given = std::optional<Tensor>; // an output that the caller may have
-Tensor output(const Given &t, const char *name, at::ScalarType type, at::IntArrayRef shape, const at::Device &dev)
+Tensor output(const Given &t, const char *name, at::ScalarType type, at::IntArrayRef shape, const at::Device &dev,
+              at::TensorList inputs = {})
 {
     if (!t || !t->defined())
         return empty(shape, type, dev);
     array(*t, name, type, shape, dev);
+    for (const Tensor &i : inputs) { // rows are read while others are written
+        const auto overlap = at::get_overlap_status(*t, i);
+        TORCH_CHECK_VALUE(overlap != at::MemOverlapStatus::Full && overlap != at::MemOverlapStatus::Partial, name,
+                          " must not overlap an input");
+    }
     return *t;
 }
 Tensor given(const Given &t) { return t.value_or(Tensor()); }
@@ -102,6 +110,24 @@ variable_list once(variable_list grads)
         if (g.defined())
             g = marked[i++];
     return grads;
+}
+
+// A backward pass runs every node on the stream of its forward. During a
+// stream capture, a leaf or node whose own stream is the default one (a graph
+// that was built before the capture and still lives) would have the captured
+// pass wait on that stream, which breaks the capture and can end the process.
+void check_capture(const Tensor &t, const char *name)
+{
+    if (!at::GradMode::is_enabled() || !t.requires_grad() || !t.is_cuda())
+        return;
+    const c10::cuda::CUDAGuard guard(t.device());
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None)
+        return;
+    const auto node = t.grad_fn() ? t.grad_fn() : torch::autograd::impl::try_get_grad_accumulator(t);
+    const auto at = node ? node->stream() : std::nullopt;
+    TORCH_CHECK(!at || *at != c10::cuda::getDefaultCUDAStream(t.device().index()).unwrap(), name,
+                " belongs to an autograd graph built on the default stream before this capture; free that graph first"
+                " (and warm up on a side stream), or capture without gradients");
 }
 
 // ------------------------------------------------------------------ calls
@@ -157,7 +183,7 @@ Tensor route_backward(const Tensor &logits, const Tensor &weights, const Tensor 
         array(loss_grad, "loss_grad", at::kFloat, {l.cols}, dev);
     }
     const c10::cuda::CUDAGuard guard(dev);
-    const Tensor out = output(out_, "out", logits.scalar_type(), {l.rows, l.cols}, dev);
+    const Tensor out = output(out_, "out", logits.scalar_type(), {l.rows, l.cols}, dev, {logits});
     check("moe_route_backward",
           moe_route_backward(ptr(logits), l.dtype, l.rows, l.cols, l.stride, ptr_as<uint8_t>(valid), (int)k,
                              renormalize, ptr_as<float>(weights), ptr_as<int32_t>(ids), ptr_as<float>(loss_grad),
@@ -205,7 +231,7 @@ Tensor dispatch(const Tensor &x, const Tensor &pos, const Tensor &offs, const Gi
     TORCH_CHECK_TYPE(mine || out_->dim() == 2, "out must be a (rows, cols) tensor");
     const int64_t rows = mine ? (pos.numel() + 15) / 16 * 16 : out_->size(0);
     const c10::cuda::CUDAGuard guard(dev);
-    const Tensor out = output(out_, "out", x.scalar_type(), {rows, r.cols}, dev);
+    const Tensor out = output(out_, "out", x.scalar_type(), {rows, r.cols}, dev, {x});
     check("moe_dispatch", moe_dispatch(ptr(x), r.dtype, r.rows, r.cols, r.stride, ptr_as<int32_t>(pos),
                                        (int)std::min<int64_t>(pos.size(1), INT32_MAX), ptr_as<int32_t>(offs),
                                        (int)offs.numel(), out_ptr(out), rows, stream(dev)));
@@ -221,7 +247,7 @@ Tensor combine(const Tensor &y, const Tensor &pos, const Given &weights_, const 
     if (weights.defined())
         array(weights, "weights", at::kFloat, pos.sizes(), dev);
     const c10::cuda::CUDAGuard guard(dev);
-    const Tensor out = output(out_, "out", y.scalar_type(), {pos.size(0), r.cols}, dev);
+    const Tensor out = output(out_, "out", y.scalar_type(), {pos.size(0), r.cols}, dev, {y});
     check("moe_combine", moe_combine(ptr(y), r.dtype, r.rows, r.cols, r.stride, ptr_as<int32_t>(pos),
                                      ptr_as<float>(weights), pos.size(0),
                                      (int)std::min<int64_t>(pos.size(1), INT32_MAX), out_ptr(out), stream(dev)));
@@ -244,7 +270,7 @@ std::tuple<Given, Given> combine_backward(const Tensor &grad_out, const Tensor &
     const c10::cuda::CUDAGuard guard(dev);
     Tensor dy, dw;
     if (need_y)
-        dy = output(grad_y_, "grad_y", y.scalar_type(), {r.rows, r.cols}, dev);
+        dy = output(grad_y_, "grad_y", y.scalar_type(), {r.rows, r.cols}, dev, {y, grad_out});
     if (need_weights)
         dw = output(grad_weights_, "grad_weights", at::kFloat, pos.sizes(), dev);
     check("moe_combine_backward",
@@ -330,16 +356,20 @@ struct MoECombine : torch::autograd::Function<MoECombine> {
 std::tuple<Tensor, Tensor, Tensor, Tensor> grad_route(const Tensor &logits, int64_t top_k, const Given &valid,
                                                       bool renormalize)
 {
+    check_capture(logits, "logits");
     const variable_list o = MoERoute::apply(logits, top_k, valid, renormalize);
     return {o[0], o[1], o[2], o[3]};
 }
 std::tuple<Tensor, Tensor, Tensor> grad_dispatch(const Tensor &x, const Tensor &ids, int64_t num_experts)
 {
+    check_capture(x, "x");
     const variable_list o = MoEDispatch::apply(x, ids, num_experts);
     return {o[0], o[1], o[2]};
 }
 Tensor grad_combine(const Tensor &y, const Tensor &pos, const Tensor &weights, const Tensor &offs)
 {
+    check_capture(y, "y");
+    check_capture(weights, "weights");
     return MoECombine::apply(y, pos, weights, offs)[0];
 }
 

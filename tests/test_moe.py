@@ -686,3 +686,78 @@ def test_streams_graphs_and_calls_at_once():
     for _, out in graphs:
         assert all(torch.equal(a, b) for a, b in zip(out, want))
     assert mxq.device_status() == 0
+
+
+def _train(l, x, k):
+    """a step of router, dispatch and combine through the differentiable calls"""
+    w, ids, counts, loss = autograd.moe_route(l, k, renormalize=True)
+    xs, pos, offs = autograd.moe_dispatch(x, ids, l.shape[1])
+    out = autograd.moe_combine(xs, pos, w, offs)
+    return torch.autograd.grad((out, loss), (l, x), (x.detach(), torch.ones_like(loss)))
+
+
+@pytest.mark.gpu
+def test_captured_training_step():
+    T, E, k, K = 777, 24, 3, 200
+    l = torch.randn(T, E, device=DEV).bfloat16().requires_grad_(True)
+    x = torch.randn(T, K, device=DEV).bfloat16().requires_grad_(True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _train(l, x, k)
+    torch.cuda.current_stream().wait_stream(side)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        got = _train(l, x, k)
+    with torch.no_grad():
+        l.copy_(torch.randn(T, E, device=DEV))
+        x.copy_(torch.randn(T, K, device=DEV))
+    gr.replay()
+    gr.replay()
+    torch.cuda.synchronize()
+    want = _train(l, x, k)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_capture_beside_a_living_graph_is_refused():
+    T, E, k, K = 64, 8, 2, 64
+    l = torch.randn(T, E, device=DEV).requires_grad_(True)
+    x = torch.randn(T, K, device=DEV).requires_grad_(True)
+    w, ids, _, _ = autograd.moe_route(l, k)  # graphs on the default stream that live on
+    xs, pos, offs = autograd.moe_dispatch(x, ids, E)
+    xd, wd, ld = x.detach(), w.detach(), l.detach()
+    calls = (lambda: autograd.moe_route(l, k), lambda: autograd.moe_dispatch(x, ids, E),
+             lambda: autograd.moe_combine(xs, pos, wd, offs), lambda: autograd.moe_combine(xs.detach(), pos, w, offs))
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        for call in calls:
+            with pytest.raises(RuntimeError, match="default stream before this capture"):
+                call()
+        with torch.no_grad():
+            a = autograd.moe_route(l, k)[0]
+        b = autograd.moe_route(ld.requires_grad_(True), k)[0].detach()  # a leaf of its own
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a, w) and torch.equal(b, w) and torch.equal(mxq.moe_dispatch(xd, pos, offs), xs)
+
+
+@pytest.mark.gpu
+def test_outputs_over_inputs_are_refused():
+    T, E, k, K = 16, 4, 1, 64
+    x = torch.randn(T, K, device=DEV)
+    l = torch.randn(T, E, device=DEV)
+    g = torch.zeros(E, device=DEV)
+    w, ids, _, _ = mxq.moe_route(l, k, loss_grad=g)
+    pos, offs = mxq.moe_dispatch_plan(ids, E)
+    y, big = mxq.moe_dispatch(x, pos, offs), torch.randn(2 * T, K, device=DEV)
+    for call in (lambda: mxq.moe_dispatch(x, pos, offs, out=x), lambda: mxq.moe_combine(y, pos, w, out=y),
+                 lambda: mxq.moe_combine(big[:T], pos, w, out=big[1:T + 1]),
+                 lambda: mxq.moe_combine_backward(x, y, pos, w, offs, grad_y=y),
+                 lambda: mxq.moe_combine_backward(x, y, pos, w, offs, grad_y=x),
+                 lambda: mxq.moe_route_backward(l, w, ids, g, w, None, out=l)):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    assert torch.equal(mxq.moe_combine(big[:T], pos, w, out=big[T:]), mxq.moe_combine(big[:T].clone(), pos, w))

@@ -155,6 +155,17 @@ def test_larger(E, N, K):
 
 
 @pytest.mark.gpu
+def test_more_than_2_31_elements():
+    E, N, K = 260, 2050, 4100
+    g = torch.randn(E, N, K, device=DEV, dtype=torch.bfloat16)
+    assert g.numel() > 2 ** 31
+    out = mxq.newton_schulz(g, steps=3)
+    for i in (0, E // 2, E - 1):  # a matrix alone goes through the same products in other tiles
+        check(out[i:i + 1], g[i:i + 1], [COEF] * 3)
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["noise", "decay"])
 @pytest.mark.parametrize("N,K", [(200, 500), (384, 256)])
 def test_spectra(kind, N, K):
@@ -215,6 +226,17 @@ def test_gpu_refusals():
     torch.library.opcheck(torch.ops.mxq.newton_schulz, (g, 5, list(COEF), 1e-7),
                           test_utils=("test_schema", "test_faketensor"))
     assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_out_over_its_input_is_refused():
+    b = torch.randn(4, 64, 96, device=DEV).bfloat16()
+    f = torch.randn(2, 64, 96, device=DEV)
+    for call in (lambda: mxq.newton_schulz(b, out=b), lambda: mxq.newton_schulz(b[:2], out=b[1:3]),
+                 lambda: mxq.newton_schulz(f, out=f.view(torch.bfloat16).reshape(4, 64, 96)[2:])):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    assert torch.equal(mxq.newton_schulz(b[:2], out=b[2:]), mxq.newton_schulz(b[:2]))
 
 
 @pytest.mark.gpu

@@ -942,7 +942,7 @@ __global__ void __launch_bounds__(moe::ROW_THREADS)
 // slot, a lane behind the run's end reads the run's last vector and stores
 // nothing.
 template <typename T, int V, int U, int J>
-__global__ void __launch_bounds__(moe::ROW_THREADS, 4)
+__global__ void __launch_bounds__(moe::ROW_THREADS, V * sizeof(T) == 16 ? 4 : 5)
     k_moe_combine(const T *__restrict__ y, int64_t M, int64_t K, int64_t ld, const int32_t *__restrict__ pos,
                   const float *__restrict__ weights, uint32_t tokens, uint32_t parts, uint32_t run, int k,
                   T *__restrict__ out)

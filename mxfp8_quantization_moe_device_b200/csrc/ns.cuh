@@ -312,7 +312,7 @@ MXQ_DEV void scale_factors(double norm, float &f0, float &f1)
 // tile as it is read goes to X (tall: to X^T), its transpose to X^T (tall: to X),
 // both halves to the epilogue's chunks. A thread moves pairs of neighbours.
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 8)
     k_ns_init(const T *__restrict__ g, int rows, int cols, int pair, const double *__restrict__ part, int parts,
               double eps, int tall, uint16_t *__restrict__ xh, int ldx, uint16_t *__restrict__ xt,
               int ldt, uint16_t *__restrict__ hi, uint16_t *__restrict__ lo)
@@ -322,7 +322,18 @@ __global__ void __launch_bounds__(256)
     const int e = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
     let_next_kernel_start();
     wait_for_previous_kernel();
-    if (threadIdx.x < 32) {
+    const T *p = g + (int64_t)e * rows * cols;
+    const int64_t base_x = (int64_t)e * (tall ? cols : rows) * ldx;
+    const int64_t base_t = (int64_t)e * (tall ? rows : cols) * ldt;
+    const int tx = 2 * (threadIdx.x & 31), ty = threadIdx.x >> 5;
+    float2 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int R = r0 + ty + 8 * i, C = c0 + tx;
+        v[i] = R < rows && C < cols ? in_pair(p + (int64_t)R * cols + C, pair != 0, C + 1 < cols)
+                                    : make_float2(0.0f, 0.0f);
+    }
+    if (threadIdx.x < 32) { // the norm, while the tile is on its way
         double s = 0.0;
         for (int i = threadIdx.x; i < parts; i += 32)
             s += part[(size_t)e * parts + i];
@@ -335,17 +346,6 @@ __global__ void __launch_bounds__(256)
     }
     __syncthreads();
     const float f0 = s_f[0], f1 = s_f[1];
-    const T *p = g + (int64_t)e * rows * cols;
-    const int64_t base_x = (int64_t)e * (tall ? cols : rows) * ldx;
-    const int64_t base_t = (int64_t)e * (tall ? rows : cols) * ldt;
-    const int tx = 2 * (threadIdx.x & 31), ty = threadIdx.x >> 5;
-    float2 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int R = r0 + ty + 8 * i, C = c0 + tx;
-        v[i] = R < rows && C < cols ? in_pair(p + (int64_t)R * cols + C, pair != 0, C + 1 < cols)
-                                    : make_float2(0.0f, 0.0f);
-    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = ty + 8 * i, R = r0 + r, C = c0 + tx;

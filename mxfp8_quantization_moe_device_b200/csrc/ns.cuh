@@ -96,6 +96,16 @@ template <int TN> constexpr uint32_t idesc()
     return (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
 }
 
+// An operand read by columns (MN-major): K runs down its rows, which lie W = 64
+// or 128 bytes apart with the W-byte swizzle, eight rows a group; blocks of
+// W / 2 columns follow at `block` bytes. The instruction is told by a bit.
+template <int W> MXQ_DEV uint64_t smem_desc_columns(uint32_t addr, uint32_t block)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(block >> 4) << 16 | (uint64_t(8 * W) >> 4) << 32 |
+           (uint64_t(1) << 46) | (uint64_t(W == 128 ? 2 : 4) << 61);
+}
+constexpr uint32_t IDESC_B_COLUMNS = 1u << 16;
+
 enum Mode { GRAM = 0, POLY = 1, STEP = 2, LAST = 3 };
 
 struct Args {

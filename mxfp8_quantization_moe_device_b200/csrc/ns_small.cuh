@@ -1,10 +1,11 @@
 // ns_small.cuh - newton_schulz (see ns.cuh) for matrices whose smaller side is
 // at most 128: all steps of a matrix in one launch, on chip.
 //
-// A CTA holds a slab of up to 256 columns of X (m <= 128 rows): hi of X and of
-// X^T as fp16 in shared memory in the layout that tcgen05.mma reads, X itself
-// in fp32 in half of TMEM, so that it is never rounded; the other half takes
-// the products, A and A A and then, both read, B' X.
+// A CTA holds a slab of up to 256 columns of X (m <= 128 rows): hi of X as fp16
+// in shared memory in the layout that tcgen05.mma reads, by rows for X X^T and
+// by columns for B' X, X itself in fp32 in half of TMEM, so that it is never
+// rounded; the other half takes the products, A and A A and then, both read,
+// B' X.
 // A matrix with more columns takes a cluster of up to sixteen CTAs: each
 // multiplies its slab with itself, the partial 128 x 128 products are summed
 // over distributed shared memory in rank order (every CTA sums some rows and
@@ -36,10 +37,8 @@ struct Coefs {
 
 struct __align__(1024) SmallSmem {
     uint8_t xh[SM_SLAB / 64][SM_M * 128];  // X: blocks of 64 columns, 128-byte rows
-    uint8_t xt[SM_M / 64][SM_SLAB * 128];  // X^T: blocks of 64 rows of X
     uint8_t ab[SM_M / 64][SM_M * 128];     // A, then B
     float alpha[SM_M], beta[SM_M];         // the diagonals of A and B
-    double sums[SM_MAX_CTAS];              // every CTA's sum of squares
     double warp_sum[SM_THREADS / 32];
     uint64_t bar;
     uint32_t tmem_base;
@@ -99,9 +98,11 @@ MXQ_DEV void st_cluster_f32(uint32_t addr, float v)
 {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-MXQ_DEV void st_cluster_f64(uint32_t addr, double v)
+MXQ_DEV double ld_cluster_f64(uint32_t addr)
 {
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+    double v;
+    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // element `dk` (none if negative) of the row that a lane holds: returned, and
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
                     f[k] = r < m && 32 * ch + k < ncol ? in_pair(q + (int64_t)k * cols, false, false).x : 0.0f;
-            } else { // a row at a time, turned over where X and X^T will be
+            } else { // a row at a time, turned over where X and A will be
                 const T *q = p + (int64_t)(32 * quad) * cols + c0 + lane;
                 const bool in = 32 * ch + lane < ncol;
 #pragma unroll
@@ -214,26 +215,26 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
         sm.warp_sum[warp] = sq;
     __syncwarp();
     g2::cluster_sync(); // every CTA of the cluster runs and has its sums
-    // rows and columns that are never written stay zero
-    for (int i = tid; i < (int)(sizeof(sm.xh) + sizeof(sm.xt) + sizeof(sm.ab)) / 16; i += SM_THREADS)
-        reinterpret_cast<uint4 *>(sm.xh)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (tid < ctas) {
+    if (warp == 0) { // a lane per CTA, then the lanes, in the same order everywhere
         double s = 0.0;
-        for (int w = 0; w < SM_THREADS / 32; ++w)
-            s += sm.warp_sum[w];
-        st_cluster_f64(g2::peer_addr(&sm.sums[rank], (uint32_t)tid), s);
-    }
-    __syncwarp(); // the cluster barrier is warp-aligned
-    g2::cluster_sync();
-    if (tid == 0) {
-        double s = 0.0;
-        for (int p = 0; p < ctas; ++p)
-            s += sm.sums[p];
-        scale_factors(sqrt(s) + eps, sm.factor[0], sm.factor[1]);
+        if (lane < ctas) {
+            double w[SM_THREADS / 32];
+#pragma unroll
+            for (int i = 0; i < SM_THREADS / 32; ++i)
+                w[i] = ld_cluster_f64(g2::peer_addr(&sm.warp_sum[i], (uint32_t)lane));
+#pragma unroll
+            for (int i = 0; i < SM_THREADS / 32; ++i)
+                s += w[i];
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0)
+            scale_factors(sqrt(s) + eps, sm.factor[0], sm.factor[1]);
     }
     __syncthreads();
 
-    // X of a chunk, times 2^8, to its places: hi to xh and xt
+    // hi of a chunk of X, times 2^8, to its place
     auto put_x = [&](int c0, const float (&x)[32]) {
         uint32_t h[16];
 #pragma unroll
@@ -244,11 +245,6 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
         for (int q = 0; q < 4; ++q)
             sts_v4(smem_u32(row) + swz(r, (c0 & 32) * 2 + 16 * q),
                    make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]));
-        uint8_t *colp = sm.xt[r >> 6];
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-            *reinterpret_cast<uint16_t *>(colp + swz(c0 + k, (r & 63) * 2)) =
-                (uint16_t)(k & 1 ? h[k >> 1] >> 16 : h[k >> 1]);
     };
     if (active) {
         const float f0 = sm.factor[0], f1 = sm.factor[1];
@@ -270,17 +266,21 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
 
     uint32_t phase = 0;
     // everything that the tensor core will read is written: then one thread
-    // multiplies P (128 x 16 ks) by Q^T (N rows) into TMEM column d
-    auto product = [&](uint32_t d, const uint8_t *P, const uint8_t *Q, int q_block, int N, int K) {
+    // multiplies P (128 x K) by Q^T (Q has N rows) or, by_columns, by Q (N
+    // columns) into TMEM column d. Rows and columns of shared memory that were
+    // never written reach only rows of the product that nothing reads.
+    auto product = [&](uint32_t d, const uint8_t *P, const uint8_t *Q, bool by_columns, int N, int K) {
         fence_proxy_async_all();
         gm::tc_fence_before();
         __syncthreads();
         if (tid == 0) {
             gm::tc_fence_after();
-            const uint32_t id = small_idesc(N);
+            const uint32_t id = small_idesc(N) | (by_columns ? IDESC_B_COLUMNS : 0u);
             for (int k = 0; k < K; k += 16) {
                 const uint64_t ad = gm::smem_desc_k128(smem_u32(P) + (k >> 6) * SM_M * 128) + 2 * ((k >> 4) & 3);
-                const uint64_t bd = gm::smem_desc_k128(smem_u32(Q) + (k >> 6) * q_block) + 2 * ((k >> 4) & 3);
+                const uint64_t bd = by_columns
+                                        ? smem_desc_columns<128>(smem_u32(Q) + k * 128, SM_M * 128)
+                                        : gm::smem_desc_k128(smem_u32(Q) + (k >> 6) * SM_M * 128) + 2 * ((k >> 4) & 3);
                 mma_f16(sm.tmem_base + d, ad, bd, id, k > 0 ? 1u : 0u);
             }
             gm::tc_commit(&sm.bar);
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
     for (int s = 0; s < steps; ++s) {
         const float cb = co.v[3 * s + 1], cc = co.v[3 * s + 2];
         // ---- A = X X^T
-        product(d_a, sm.xh[0], sm.xh[0], SM_M * 128, m16, n16);
+        product(d_a, sm.xh[0], sm.xh[0], false, m16, n16);
         if (active) {
 #pragma unroll 1
             for (int ch = part; 32 * ch < m16; ch += 4) {
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             g2::cluster_sync(); // A is whole in every CTA
         }
         // ---- B' from A' and alpha, in A's place, and beta
-        product(d_b, sm.ab[0], sm.ab[0], SM_M * 128, m16, m16);
+        product(d_b, sm.ab[0], sm.ab[0], false, m16, m16);
         if (active) {
 #pragma unroll 1
             for (int ch = part; 32 * ch < m16; ch += 4) {
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
             }
         }
         // ---- X = (a + beta) X + B' X
-        product(d_y, sm.ab[0], sm.xt[0], SM_SLAB * 128, n16, m16);
+        product(d_y, sm.ab[0], sm.xh[0], true, n16, m16);
         if (active) {
             const float scale = co.v[3 * s] + sm.beta[r];
 #pragma unroll 1
@@ -430,8 +430,8 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                         for (int k = 0; k < 32; ++k)
                             if (r < m && c0 + k < ncol)
                                 dst[(int64_t)k * m] = (uint16_t)(k & 1 ? h[k >> 1] >> 16 : h[k >> 1]);
-                    } else { // turned over where X^T was: its last product is done
-                        rows_out(sm.xt[0] + warp * CHUNK_BYTES, h, dst + (int64_t)(32 * quad) * n + c_base + c0, n,
+                    } else { // turned over where hi was: its last product is done
+                        rows_out(sm.xh[0] + warp * CHUNK_BYTES, h, dst + (int64_t)(32 * quad) * n + c_base + c0, n,
                                  m - 32 * quad, ncol - c0, out_vec);
                     }
                 }

@@ -27,19 +27,20 @@
 // elements near 2^-12, fp16's normal range ends at 2^-14), A' and B' 2^10, lo
 // 2^11 on top of X's.
 //
-// Every product is D = P Q^T with both operands K-major: A = X X^T, A A = A
-// A^T (A is symmetric), B X = B (X^T)^T; the epilogue that writes X therefore
-// writes X^T too. A and A A are computed on and below the diagonal of tiles
-// and mirrored by the epilogue.
+// The first operand of every product is read by rows. So is the second of A =
+// X X^T and of A A = A A^T (A is symmetric); that of B X is X itself, read by
+// columns (MN-major), so that X^T is never written. X is held twice, since the
+// tiles of B X read what others replace. A and A A are computed on and below
+// the diagonal of tiles and mirrored by the epilogue.
 //
 // Epilogue. A lane holds one row of the accumulator, so what it writes along
 // the row lands in 32 different lines per store and what it writes down a
 // column is one line for the warp. What only the epilogue reads (X as hi and
 // lo, and A for the next product) is kept in chunks of 32 x 32 elements in the
 // order in which the warp holds them, 16 bytes per lane and access, padded to
-// whole chunks so that nothing is predicated; X^T and the mirrored halves of A
-// and B are written down the columns; the row-major copies that the products
-// read go through shared memory and a TMA store. Row-wise 16-byte accesses in
+// whole chunks so that nothing is predicated; the mirrored halves of A and B
+// are written down the columns; the row-major copies that the products read go
+// through shared memory and a TMA store. Row-wise 16-byte accesses in
 // their place kept the load/store unit busy for 16 K cycles a tile against 8 K
 // of MMAs, 2-byte accesses down the columns for all of it cost 1.6 us a chunk.
 //
@@ -90,11 +91,25 @@ template <int TN> struct __align__(1024) Smem {
 };
 template <int TN> constexpr size_t smem_bytes() { return sizeof(Smem<TN>) + 1024; }
 
-// fp32 accumulator, f16 x f16, both K-major, N = TN, M 256 (the pair)
+// fp32 accumulator, f16 x f16, N = TN, M 256 (the pair)
 template <int TN> constexpr uint32_t idesc()
 {
     return (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
 }
+
+enum Mode { GRAM = 0, POLY = 1, STEP = 2, LAST = 3 };
+
+struct Args {
+    int E, m, n;          // batch, X is (m, n)
+    int ldt;              // row length of A and B (m up to 8)
+    float a, b, c;
+    uint16_t *hi, *lo;    // X as the epilogue keeps it: chunks of (m, n)
+    uint16_t *a_own;      // A' as the epilogue keeps it: chunks of (m, m)
+    float *alpha, *beta;  // (E, m): the diagonals of A and B
+    uint16_t *A, *B;      // (E, m, ldt)
+    uint16_t *out;        // LAST: bf16, (E, m, n) or, transposed, (E, n, m)
+    int out_t, out_vec;
+};
 
 // An operand read by columns (MN-major): K runs down its rows, which lie W = 64
 // or 128 bytes apart with the W-byte swizzle, eight rows a group; blocks of
@@ -106,27 +121,14 @@ template <int W> MXQ_DEV uint64_t smem_desc_columns(uint32_t addr, uint32_t bloc
 }
 constexpr uint32_t IDESC_B_COLUMNS = 1u << 16;
 
-enum Mode { GRAM = 0, POLY = 1, STEP = 2, LAST = 3 };
-
-struct Args {
-    int E, m, n;          // batch, X is (m, n)
-    int ldt;              // row length of X^T, A and B (m up to 8)
-    float a, b, c;
-    uint16_t *hi, *lo;    // X as the epilogue keeps it: chunks of (m, n)
-    uint16_t *a_own;      // A' as the epilogue keeps it: chunks of (m, m)
-    float *alpha, *beta;  // (E, m): the diagonals of A and B
-    uint16_t *xt;         // (E, n, ldt): X^T, written by STEP
-    uint16_t *A, *B;      // (E, m, ldt)
-    uint16_t *out;        // LAST: bf16, (E, m, n) or, transposed, (E, n, m)
-    int out_t, out_vec;
-};
-
-template <int TN> MXQ_DEV void mma_pair_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate)
+// COLUMNS: the second operand is read by columns
+template <int TN, bool COLUMNS>
+MXQ_DEV void mma_pair_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate)
 {
     asm volatile("{\n\t.reg .pred p;\n\t"
                  "setp.ne.b32 p, %3, 0;\n\t"
                  "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %4, p;\n\t}" ::"r"(d_tmem),
-                 "l"(adesc), "l"(bdesc), "r"(accumulate), "r"(idesc<TN>())
+                 "l"(adesc), "l"(bdesc), "r"(accumulate), "r"(idesc<TN>() | (COLUMNS ? IDESC_B_COLUMNS : 0u))
                  : "memory");
 }
 
@@ -319,13 +321,13 @@ MXQ_DEV void scale_factors(double norm, float &f0, float &f1)
 }
 
 // X0 from G (rows, cols) in 64 x 64 tiles. X is G, or with `tall` G^T: the
-// tile as it is read goes to X (tall: to X^T), its transpose to X^T (tall: to X),
-// both halves to the epilogue's chunks. A thread moves pairs of neighbours.
+// tile as it is read, or its transpose, goes to X, and both halves to the
+// epilogue's chunks. A thread moves pairs of neighbours.
 template <typename T>
 __global__ void __launch_bounds__(256, 8)
     k_ns_init(const T *__restrict__ g, int rows, int cols, int pair, const double *__restrict__ part, int parts,
-              double eps, int tall, uint16_t *__restrict__ xh, int ldx, uint16_t *__restrict__ xt,
-              int ldt, uint16_t *__restrict__ hi, uint16_t *__restrict__ lo)
+              double eps, int tall, uint16_t *__restrict__ xh, int ldx, uint16_t *__restrict__ hi,
+              uint16_t *__restrict__ lo)
 {
     __shared__ uint32_t tile[64][65];
     __shared__ float s_f[2];
@@ -334,7 +336,6 @@ __global__ void __launch_bounds__(256, 8)
     wait_for_previous_kernel();
     const T *p = g + (int64_t)e * rows * cols;
     const int64_t base_x = (int64_t)e * (tall ? cols : rows) * ldx;
-    const int64_t base_t = (int64_t)e * (tall ? rows : cols) * ldt;
     const int tx = 2 * (threadIdx.x & 31), ty = threadIdx.x >> 5;
     float2 v[8];
 #pragma unroll
@@ -366,26 +367,17 @@ __global__ void __launch_bounds__(256, 8)
         const uint32_t w0 = __byte_perm(h, l, 0x5410), w1 = __byte_perm(h, l, 0x7632);
         tile[r][tx] = w0;
         tile[r][tx + 1] = w1;
-        if (R < rows && C < cols) { // rows of the targets are padded to pairs
-            if (tall) {
-                *reinterpret_cast<uint32_t *>(xt + base_t + (int64_t)R * ldt + C) = h;
-            } else {
-                *reinterpret_cast<uint32_t *>(xh + base_x + (int64_t)R * ldx + C) = h;
-            }
-        }
+        if (!tall && R < rows && C < cols) // X's rows are padded to pairs
+            *reinterpret_cast<uint32_t *>(xh + base_x + (int64_t)R * ldx + C) = h;
     }
     __syncthreads();
+    if (tall) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = ty + 8 * i, C = c0 + c, R = r0 + tx;
-        if (R < rows && C < cols) {
-            const uint32_t w0 = tile[tx][c], w1 = tile[tx + 1][c];
-            const uint32_t h = __byte_perm(w0, w1, 0x5410);
-            if (tall) {
-                *reinterpret_cast<uint32_t *>(xh + base_x + (int64_t)C * ldx + R) = h;
-            } else {
-                *reinterpret_cast<uint32_t *>(xt + base_t + (int64_t)C * ldt + R) = h;
-            }
+        for (int i = 0; i < 8; ++i) {
+            const int c = ty + 8 * i, C = c0 + c, R = r0 + tx;
+            if (R < rows && C < cols)
+                *reinterpret_cast<uint32_t *>(xh + base_x + (int64_t)C * ldx + R) =
+                    __byte_perm(tile[tx][c], tile[tx + 1][c], 0x5410);
         }
     }
     // a warp per chunk and pair of pieces
@@ -423,16 +415,19 @@ template <bool SYM, int TN> __host__ __device__ inline int64_t sym_or_all_tiles(
     return (TILE / TN) * (tm * (tm - 1) / 2) + tn;
 }
 
-// D = P Q^T over K = 64 nkb columns for every matrix, with the epilogue of
-// MODE. tm_o: the row-major copy of the result (X, A or B) in boxes of 32 x 32
-// with the 64-byte swizzle, unused by LAST. Grid: an even number of CTAs in
-// clusters of two.
+// D = P Q^T (GRAM, POLY) or P Q (STEP, LAST) over K = 64 nkb for every matrix,
+// with the epilogue of MODE. tm_q by columns: boxes of 64 rows and 64 columns
+// (TN 64: 32 columns, with the 64-byte swizzle). tm_o: the row-major copy of the
+// result (X, A or B) in boxes of 32 x 32 with the 64-byte swizzle, unused by
+// LAST. Grid: an even number of CTAs in clusters of two.
 template <int MODE, int TN>
 __global__ void __launch_bounds__(THREADS, 1)
     k_ns_gemm(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
               const __grid_constant__ CUtensorMap tm_o, const Args q, int nkb, uint64_t wait_ns)
 {
     constexpr bool SYM = MODE == GRAM || MODE == POLY;
+    constexpr bool COLUMNS = !SYM;             // Q is read by columns
+    constexpr int QW = TN == 64 ? 64 : 128;    // bytes of its rows in shared memory
     constexpr int STAGES = Smem<TN>::STAGES;
     constexpr int TMEM_COLS = ACC * TN;
     constexpr int RATIO = TILE / TN; // column tiles per row tile
@@ -478,7 +473,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int64_t total = per * q.E;
     // tile t of a matrix: row tile i, column tile j; symmetric products take
     // the column tiles up to the diagonal's, the others run down the row tiles
-    // first, so that the pairs at work share a column tile of X^T and all of B
+    // first, so that the pairs at work share a column tile of X and all of B
     struct Item {
         int e, i, j;
     };
@@ -517,7 +512,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                         mbar_arrive_expect_tx(&sm.full[s], 2 * (OP_BYTES + Smem<TN>::Q_BYTES));
                     const uint32_t bar = leader_full0 + (uint32_t)(s * sizeof(uint64_t));
                     load_pair(sm.a[s], &tm_p, bar, kb * BK, w.i * TILE + (int)rank * HALF, w.e);
-                    load_pair(sm.b[s], &tm_q, bar, kb * BK, w.j * TN + (int)rank * (TN / 2), w.e);
+                    const int q0 = w.j * TN + (int)rank * (TN / 2);
+                    if constexpr (COLUMNS) {
+#pragma unroll
+                        for (int c = 0; c < TN / 2; c += QW / 2)
+                            load_pair(sm.b[s] + c * 2 * BK, &tm_q, bar, q0 + c, kb * BK, w.e);
+                    } else {
+                        load_pair(sm.b[s], &tm_q, bar, kb * BK, q0, w.e);
+                    }
                 }
             }
             // drain: every issued fill, of both CTAs, has landed before the
@@ -547,15 +549,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int kb = 0; ok && kb < nkb; ++kb) {
                     gm::tc_fence_after();
                     const uint64_t ad = gm::smem_desc_k128(smem_u32(sm.a[s]));
-                    const uint64_t bd = gm::smem_desc_k128(smem_u32(sm.b[s]));
+                    const uint64_t bd = COLUMNS ? smem_desc_columns<QW>(smem_u32(sm.b[s]), QW * BK)
+                                                : gm::smem_desc_k128(smem_u32(sm.b[s]));
+                    // 16 of K per MMA: 32 bytes of a row, or 16 rows
+                    constexpr int Q_STEP = COLUMNS ? QW : 2;
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) // 16 columns per MMA: 32 bytes
-                        mma_pair_f16<TN>(d, ad + 2 * k, bd + 2 * k, (kb > 0 || k > 0) ? 1u : 0u);
+                    for (int k = 0; k < 3; ++k)
+                        mma_pair_f16<TN, COLUMNS>(d, ad + 2 * k, bd + Q_STEP * k, (kb > 0 || k > 0) ? 1u : 0u);
                     const int s_next = s + 1 == STAGES ? 0 : s + 1;
                     const uint32_t ph_next = s + 1 == STAGES ? ph ^ 1u : ph;
                     if (kb + 1 < nkb)
                         ok = mbar_wait(&sm.full[s_next], ph_next, wait_ns);
-                    mma_pair_f16<TN>(d, ad + 6, bd + 6, 1u);
+                    mma_pair_f16<TN, COLUMNS>(d, ad + 6, bd + 3 * Q_STEP, 1u);
                     g2::commit_pair(&sm.empty[s], 0x3);
                     issued = true;
                     s = s_next;
@@ -586,8 +591,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool row_ok = r < q.m;
             const int cols = SYM ? q.m : q.n;
             // this lane's column-wise position: element c of the row is `at` + c
-            // ldt elements into its matrix of X^T, A and B alike (a matrix
-            // has less than 2^31 elements, so 32 bits hold its byte offsets)
+            // ldt elements into its matrix of A and B (a matrix has less than
+            // 2^31 elements, so 32 bits hold its byte offsets)
             const int64_t plane = (int64_t)w.e * cols * q.ldt;
             const uint32_t at = (uint32_t)r, ldb = (uint32_t)q.ldt * 2u;
             const bool rows_full = r0 + 32 <= q.m; // the same in every lane
@@ -693,12 +698,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
                 // down the columns
-                if (MODE != LAST || q.out_t) {
+                if (SYM || (MODE == LAST && q.out_t)) {
                     const uint32_t ld2 = MODE == LAST ? (uint32_t)q.m * 2u : ldb;
                     uint32_t o = (uint32_t)c0 * ld2 + at * 2u;
                     uint8_t *dst = MODE == LAST
                                        ? reinterpret_cast<uint8_t *>(q.out + (int64_t)w.e * cols * q.m)
-                                       : reinterpret_cast<uint8_t *>((MODE == GRAM ? q.A : MODE == POLY ? q.B : q.xt) + plane);
+                                       : reinterpret_cast<uint8_t *>((MODE == GRAM ? q.A : q.B) + plane);
                     auto put = [&](int k) {
                         *reinterpret_cast<uint16_t *>(dst + o) = (uint16_t)(k & 1 ? h[k >> 1] >> 16 : h[k >> 1]);
                     };

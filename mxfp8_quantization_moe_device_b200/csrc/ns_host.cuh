@@ -7,7 +7,7 @@ namespace {
 struct NsPlan {
     int64_t m, n, ldx, ldt;
     int tall, parts;
-    size_t xh, hi, lo, xt[2], A, B, a_own, alpha, beta, part, bytes;
+    size_t xh[2], hi, lo, A, B, a_own, alpha, beta, part, bytes;
 };
 
 NsPlan ns_plan(int64_t E, int64_t rows, int64_t cols, int32_t steps)
@@ -25,12 +25,11 @@ NsPlan ns_plan(int64_t E, int64_t rows, int64_t cols, int32_t steps)
         o = round_up(o + bytes, 256);
         return at;
     };
-    p.xh = take((size_t)E * p.m * p.ldx * 2);
+    p.xh[0] = take((size_t)E * p.m * p.ldx * 2);
+    p.xh[1] = steps > 1 ? take((size_t)E * p.m * p.ldx * 2) : p.xh[0];
     p.hi = take((size_t)E * ns::chunks_of(p.m) * ns::chunks_of(p.n) * ns::CHUNK_BYTES);
     p.lo = take((size_t)E * ns::chunks_of(p.m) * ns::chunks_of(p.n) * ns::CHUNK_BYTES);
     p.a_own = take((size_t)E * ns::chunks_of(p.m) * ns::chunks_of(p.m) * ns::CHUNK_BYTES);
-    p.xt[0] = take((size_t)E * p.n * p.ldt * 2);
-    p.xt[1] = steps > 1 ? take((size_t)E * p.n * p.ldt * 2) : p.xt[0];
     p.A = take((size_t)E * p.m * p.ldt * 2);
     p.B = take((size_t)E * p.m * p.ldt * 2);
     p.alpha = take((size_t)E * p.m * 4);
@@ -52,34 +51,34 @@ int ns_check(int64_t E, int64_t rows, int64_t cols, int32_t steps)
     return MXQ_OK;
 }
 
-// map of one fp16 matrix per plane: boxes of 64 elements x `box_rows` rows for
-// the operands (128-byte swizzle), of 32 x 32 for the epilogue's stores
-// (box_rows 0)
-int ns_map(CUtensorMap *map, const void *p, int64_t inner, int64_t ld, int64_t rows, int64_t E, int box_rows)
-{
-    const bool store = box_rows == 0;
-    if (store)
-        box_rows = ns::CHUNK;
-    const uint64_t d[3] = {(uint64_t)inner, (uint64_t)rows, (uint64_t)E};
-    const uint64_t s[2] = {(uint64_t)ld * 2, (uint64_t)ld * 2 * (uint64_t)rows};
-    const uint32_t box[3] = {(uint32_t)(store ? ns::CHUNK : ns::BK), (uint32_t)box_rows, 1};
-    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, d, s, box,
-                    store ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
-}
+// how a product reads or writes a matrix: boxes of 64 elements x rows for the
+// operands (128-byte swizzle; by columns 64 rows, for the narrowest tiles of 32
+// elements with the 64-byte swizzle), of 32 x 32 for the epilogue's stores
+enum NsBox { NS_STORE, NS_ROWS_128, NS_ROWS_64, NS_ROWS_32, NS_COLUMNS_32, NS_NUM_BOXES };
+constexpr struct {
+    int width, rows;
+    CUtensorMapSwizzle swizzle;
+} NS_BOXES[NS_NUM_BOXES] = {{ns::CHUNK, ns::CHUNK, CU_TENSOR_MAP_SWIZZLE_64B},
+                            {ns::BK, 128, CU_TENSOR_MAP_SWIZZLE_128B},
+                            {ns::BK, 64, CU_TENSOR_MAP_SWIZZLE_128B},
+                            {ns::BK, 32, CU_TENSOR_MAP_SWIZZLE_128B},
+                            {32, ns::BK, CU_TENSOR_MAP_SWIZZLE_64B}};
 
-// one operand of the products, a matrix by rows with its inner length and row
-// length, and the maps of it that the call has made so far
+// one operand of the products: fp16 matrices by rows, a plane each, with their
+// inner length and row length, and the maps that the call has made so far
 struct NsOperand {
     const void *p;
     int64_t inner, ld, rows, E;
-    CUtensorMap maps[4];
-    bool made[4];
+    CUtensorMap maps[NS_NUM_BOXES];
+    bool made[NS_NUM_BOXES];
 
-    int map(int box_rows, const CUtensorMap **out)
+    int map(NsBox i, const CUtensorMap **out)
     {
-        const int i = box_rows == 0 ? 0 : (box_rows == 128 ? 1 : (box_rows == 64 ? 2 : 3));
         if (!made[i]) {
-            const int rc = ns_map(&maps[i], p, inner, ld, rows, E, box_rows);
+            const uint64_t d[3] = {(uint64_t)inner, (uint64_t)rows, (uint64_t)E};
+            const uint64_t s[2] = {(uint64_t)ld * 2, (uint64_t)ld * 2 * (uint64_t)rows};
+            const uint32_t box[3] = {(uint32_t)NS_BOXES[i].width, (uint32_t)NS_BOXES[i].rows, 1};
+            const int rc = make_map(&maps[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, d, s, box, NS_BOXES[i].swizzle);
             if (rc != MXQ_OK)
                 return rc;
             made[i] = true;
@@ -116,10 +115,12 @@ int ns_launch(NsOperand &p, NsOperand &q, NsOperand &o, const ns::Args &a, int p
 {
     const CUtensorMap *mp, *mq, *mo;
     int rc;
-    if ((rc = p.map(ns::HALF, &mp)) != MXQ_OK || (rc = q.map(TN / 2, &mq)) != MXQ_OK ||
-        (rc = o.map(0, &mo)) != MXQ_OK)
-        return rc;
     constexpr bool sym = MODE == ns::GRAM || MODE == ns::POLY;
+    constexpr NsBox rows = TN == 256 ? NS_ROWS_128 : (TN == 128 ? NS_ROWS_64 : NS_ROWS_32);
+    constexpr NsBox columns = TN == 64 ? NS_COLUMNS_32 : NS_ROWS_64;
+    if ((rc = p.map(NS_ROWS_128, &mp)) != MXQ_OK || (rc = q.map(sym ? rows : columns, &mq)) != MXQ_OK ||
+        (rc = o.map(NS_STORE, &mo)) != MXQ_OK)
+        return rc;
     const int64_t grid = std::min<int64_t>(a.E * ns::sym_or_all_tiles<sym, TN>(a.m, a.n), pairs);
     return launch_chained(ns::k_ns_gemm<MODE, TN>, dim3((unsigned)(2 * grid)), dim3(ns::THREADS), ns::smem_bytes<TN>(),
                           stream, true, *mp, *mq, *mo, a, (int)((p.inner + ns::BK - 1) / ns::BK), wait_ns());
@@ -176,9 +177,8 @@ int ns_start(const T *g, int64_t E, int64_t rows, int64_t cols, const NsPlan &p,
     return launch_chained(ns::k_ns_init<T>,
                           dim3((unsigned)((cols + 63) / 64), (unsigned)((rows + 63) / 64), (unsigned)E), dim3(256), 0,
                           stream, false, g, (int)rows, (int)cols, (int)(aligned(g, 2 * sizeof(T)) && cols % 2 == 0),
-                  (const double *)part, p.parts, eps, p.tall, reinterpret_cast<uint16_t *>(ws + p.xh), (int)p.ldx,
-                  reinterpret_cast<uint16_t *>(ws + p.xt[0]), (int)p.ldt, reinterpret_cast<uint16_t *>(ws + p.hi),
-                  reinterpret_cast<uint16_t *>(ws + p.lo));
+                  (const double *)part, p.parts, eps, p.tall, reinterpret_cast<uint16_t *>(ws + p.xh[0]),
+                  (int)p.ldx, reinterpret_cast<uint16_t *>(ws + p.hi), reinterpret_cast<uint16_t *>(ws + p.lo));
 }
 
 // a launch of k_ns_small with `ctas` CTAs per matrix
@@ -317,9 +317,8 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
     if (!aligned(workspace, 256))
         return MXQ_ERR_ALIGN;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    NsOperand x = {ws + p.xh, p.n, p.ldx, p.m, batch, {}, {}}, A = {ws + p.A, p.m, p.ldt, p.m, batch, {}, {}};
-    NsOperand B = {ws + p.B, p.m, p.ldt, p.m, batch, {}, {}};
-    NsOperand xt[2] = {{ws + p.xt[0], p.m, p.ldt, p.n, batch, {}, {}}, {ws + p.xt[1], p.m, p.ldt, p.n, batch, {}, {}}};
+    NsOperand A = {ws + p.A, p.m, p.ldt, p.m, batch, {}, {}}, B = {ws + p.B, p.m, p.ldt, p.m, batch, {}, {}};
+    NsOperand xs[2] = {{ws + p.xh[0], p.n, p.ldx, p.m, batch, {}, {}}, {ws + p.xh[1], p.n, p.ldx, p.m, batch, {}, {}}};
     rc = dtype == MXQ_BF16 ? ns_start(static_cast<const uint16_t *>(g), batch, rows, cols, p, eps, ws, stream)
                            : ns_start(static_cast<const float *>(g), batch, rows, cols, p, eps, ws, stream);
     if (rc != MXQ_OK)
@@ -343,11 +342,11 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
         a.a = coefficients[3 * s];
         a.b = coefficients[3 * s + 1];
         a.c = coefficients[3 * s + 2];
-        a.xt = reinterpret_cast<uint16_t *>(ws + p.xt[(s + 1) & 1]);
+        NsOperand &x = xs[s & 1], &next = xs[(s + 1) & 1];
         if ((rc = ns_product<ns::GRAM>(x, x, A, a, stream)) != MXQ_OK ||
             (rc = ns_product<ns::POLY>(A, A, B, a, stream)) != MXQ_OK ||
-            (rc = s + 1 < steps ? ns_product<ns::STEP>(B, xt[s & 1], x, a, stream)
-                                : ns_product<ns::LAST>(B, xt[s & 1], x, a, stream)) != MXQ_OK)
+            (rc = s + 1 < steps ? ns_product<ns::STEP>(B, x, next, a, stream)
+                                : ns_product<ns::LAST>(B, x, next, a, stream)) != MXQ_OK)
             return rc;
     }
     return MXQ_OK;

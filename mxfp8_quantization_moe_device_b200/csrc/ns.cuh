@@ -27,31 +27,34 @@
 // elements near 2^-12, fp16's normal range ends at 2^-14), A' and B' 2^10, lo
 // 2^11 on top of X's.
 //
-// The first operand of every product is read by rows. So is the second of A =
-// X X^T and of A A = A A^T (A is symmetric); that of B X is X itself, read by
-// columns (MN-major), so that X^T is never written. X is held twice, since the
-// tiles of B X read what others replace. A and A A are computed on and below
-// the diagonal of tiles and mirrored by the epilogue.
+// Every matrix is written once, by rows, and read by rows or by columns
+// (K-major or MN-major) as a product needs it. A = X X^T takes X by rows twice,
+// B X takes X by columns: X^T is never written. X is held twice, since the
+// tiles of B X read what others replace. A and A A are symmetric: computed on
+// and below the diagonal of 256 x 256 blocks, and a block of K above the
+// diagonal is read by columns from below. Writing X^T as well took 253 us in
+// place of 240 at (5, 1409, 577), 453 of 415 at (16, 512, 2048); writing both
+// halves of A and B 199 in place of 189 at (2, 1024, 1024).
 //
 // Epilogue. A lane holds one row of the accumulator, so what it writes along
-// the row lands in 32 different lines per store and what it writes down a
-// column is one line for the warp. What only the epilogue reads (X as hi and
-// lo, and A for the next product) is kept in chunks of 32 x 32 elements in the
-// order in which the warp holds them, 16 bytes per lane and access, padded to
-// whole chunks so that nothing is predicated; the mirrored halves of A and B
-// are written down the columns; the row-major copies that the products read go
-// through shared memory and a TMA store. Row-wise 16-byte accesses in
-// their place kept the load/store unit busy for 16 K cycles a tile against 8 K
-// of MMAs, 2-byte accesses down the columns for all of it cost 1.6 us a chunk.
+// the row lands in 32 different lines per store. What only the epilogue reads
+// (X as hi and lo, and A for the next product) is kept in chunks of 32 x 32
+// elements in the order in which the warp holds them, 16 bytes per lane and
+// access, padded to whole chunks so that nothing is predicated; what the
+// products read goes through shared memory and a TMA store. Row-wise 16-byte
+// accesses in their place kept the load/store unit busy for 16 K cycles a tile
+// against 8 K of MMAs, 2-byte accesses down the columns cost 1.6 us a chunk.
 //
 // Kernel: the CTA-pair pipeline of gemm2.cuh (tcgen05.mma.cta_group::2, one
 // 256 x 256 tile per pair of SMs, six 32 KB stages of 64 fp16 columns, two
 // accumulators in TMEM); warps 0-7 epilogue (a warp takes 32 lanes and half
 // of the columns), warp 8 TMA, warp 9 MMA and TMEM. Both CTAs' loads count on
 // the leader's barrier (TMA loads of cta_group::2), which its MMA thread waits
-// on. Edges are filled with zeros by TMA (every
-// matrix is its own plane of a rank-3 map) and cut off by the epilogue.
+// on. Edges are filled with zeros by TMA (every matrix is its own plane of a
+// rank-3 map) and cut off by the epilogue.
 #pragma once
+
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -101,12 +104,10 @@ enum Mode { GRAM = 0, POLY = 1, STEP = 2, LAST = 3 };
 
 struct Args {
     int E, m, n;          // batch, X is (m, n)
-    int ldt;              // row length of A and B (m up to 8)
     float a, b, c;
     uint16_t *hi, *lo;    // X as the epilogue keeps it: chunks of (m, n)
     uint16_t *a_own;      // A' as the epilogue keeps it: chunks of (m, m)
     float *alpha, *beta;  // (E, m): the diagonals of A and B
-    uint16_t *A, *B;      // (E, m, ldt)
     uint16_t *out;        // LAST: bf16, (E, m, n) or, transposed, (E, n, m)
     int out_t, out_vec;
 };
@@ -119,16 +120,15 @@ template <int W> MXQ_DEV uint64_t smem_desc_columns(uint32_t addr, uint32_t bloc
     return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(block >> 4) << 16 | (uint64_t(8 * W) >> 4) << 32 |
            (uint64_t(1) << 46) | (uint64_t(W == 128 ? 2 : 4) << 61);
 }
-constexpr uint32_t IDESC_B_COLUMNS = 1u << 16;
+constexpr uint32_t IDESC_A_COLUMNS = 1u << 15, IDESC_B_COLUMNS = 1u << 16;
 
-// COLUMNS: the second operand is read by columns
-template <int TN, bool COLUMNS>
+template <uint32_t IDESC>
 MXQ_DEV void mma_pair_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate)
 {
     asm volatile("{\n\t.reg .pred p;\n\t"
                  "setp.ne.b32 p, %3, 0;\n\t"
                  "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %4, p;\n\t}" ::"r"(d_tmem),
-                 "l"(adesc), "l"(bdesc), "r"(accumulate), "r"(idesc<TN>() | (COLUMNS ? IDESC_B_COLUMNS : 0u))
+                 "l"(adesc), "l"(bdesc), "r"(accumulate), "r"(IDESC)
                  : "memory");
 }
 
@@ -148,6 +148,21 @@ MXQ_DEV void load_pair(void *dst, const CUtensorMap *map, uint32_t bar, int x, i
                  " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
                  "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
                  : "memory");
+}
+
+// a stage's operand of N rows or columns and 64 of K, by rows or by columns (in
+// blocks of W bytes)
+template <int N, int W>
+MXQ_DEV void load_operand(uint8_t *dst, const CUtensorMap *rows, const CUtensorMap *columns, bool by_columns,
+                          uint32_t bar, int first, int k, int e)
+{
+    if (by_columns) {
+#pragma unroll
+        for (int c = 0; c < N; c += W / 2)
+            load_pair(dst + c * 2 * BK, columns, bar, first + c, k, e);
+    } else {
+        load_pair(dst, rows, bar, k, first, e);
+    }
 }
 
 MXQ_DEV void prefetch_map(const CUtensorMap *map)
@@ -404,8 +419,8 @@ __global__ void __launch_bounds__(256, 8)
     }
 }
 
-// tiles of one matrix: row tile i of a symmetric product needs the columns up
-// to its last row, of the others all
+// tiles of one matrix: row tile i of a symmetric product has the columns up to
+// its diagonal block's end, of the others all
 template <bool SYM, int TN> __host__ __device__ inline int64_t sym_or_all_tiles(int m, int n)
 {
     const int64_t tm = (m + TILE - 1) / TILE, tn = ((SYM ? m : n) + TN - 1) / TN;
@@ -416,18 +431,19 @@ template <bool SYM, int TN> __host__ __device__ inline int64_t sym_or_all_tiles(
 }
 
 // D = P Q^T (GRAM, POLY) or P Q (STEP, LAST) over K = 64 nkb for every matrix,
-// with the epilogue of MODE. tm_q by columns: boxes of 64 rows and 64 columns
-// (TN 64: 32 columns, with the 64-byte swizzle). tm_o: the row-major copy of the
-// result (X, A or B) in boxes of 32 x 32 with the 64-byte swizzle, unused by
-// LAST. Grid: an even number of CTAs in clusters of two.
+// with the epilogue of MODE. Maps of P and Q by rows (boxes of 128 and TN / 2
+// rows) and by columns (64 rows and 64 columns, for Q and TN 64 32 columns with
+// the 64-byte swizzle), of the result's row-major copy (X, A or B) in boxes of
+// 32 x 32 with the 64-byte swizzle, unused by LAST. Grid: an even number of
+// CTAs in clusters of two.
 template <int MODE, int TN>
 __global__ void __launch_bounds__(THREADS, 1)
-    k_ns_gemm(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
+    k_ns_gemm(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_pc,
+              const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qc,
               const __grid_constant__ CUtensorMap tm_o, const Args q, int nkb, uint64_t wait_ns)
 {
     constexpr bool SYM = MODE == GRAM || MODE == POLY;
-    constexpr bool COLUMNS = !SYM;             // Q is read by columns
-    constexpr int QW = TN == 64 ? 64 : 128;    // bytes of its rows in shared memory
+    constexpr int QW = TN == 64 ? 64 : 128; // bytes of a row of Q read by columns, in shared memory
     constexpr int STAGES = Smem<TN>::STAGES;
     constexpr int TMEM_COLS = ACC * TN;
     constexpr int RATIO = TILE / TN; // column tiles per row tile
@@ -440,7 +456,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     let_next_kernel_start();
     if (threadIdx.x == 0) {
         prefetch_map(&tm_p);
-        prefetch_map(&tm_q);
+        if (MODE != GRAM)
+            prefetch_map(&tm_pc);
+        if (SYM)
+            prefetch_map(&tm_q);
+        if (MODE != GRAM)
+            prefetch_map(&tm_qc);
         if (MODE != LAST)
             prefetch_map(&tm_o);
         for (int s = 0; s < STAGES; ++s) {
@@ -495,6 +516,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         return w;
     };
 
+    // the first of K's blocks for which P and Q are read by columns: a
+    // symmetric operand behind the diagonal block of the tile's rows (P) or
+    // columns (Q), X in B X always
+    auto p_turn = [&](const Item &w) { return MODE == GRAM ? nkb : (w.i + 1) * (TILE / BK); };
+    auto q_turn = [&](const Item &w) {
+        return MODE == GRAM ? nkb : (MODE == POLY ? (w.j / RATIO + 1) * (TILE / BK) : 0);
+    };
+
     if (warp == EPI_WARPS) {
         // ------------------------------------------------ TMA producer (both CTAs)
         if (lane == 0) {
@@ -511,15 +540,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (leader)
                         mbar_arrive_expect_tx(&sm.full[s], 2 * (OP_BYTES + Smem<TN>::Q_BYTES));
                     const uint32_t bar = leader_full0 + (uint32_t)(s * sizeof(uint64_t));
-                    load_pair(sm.a[s], &tm_p, bar, kb * BK, w.i * TILE + (int)rank * HALF, w.e);
-                    const int q0 = w.j * TN + (int)rank * (TN / 2);
-                    if constexpr (COLUMNS) {
-#pragma unroll
-                        for (int c = 0; c < TN / 2; c += QW / 2)
-                            load_pair(sm.b[s] + c * 2 * BK, &tm_q, bar, q0 + c, kb * BK, w.e);
-                    } else {
-                        load_pair(sm.b[s], &tm_q, bar, kb * BK, q0, w.e);
-                    }
+                    load_operand<HALF, 128>(sm.a[s], &tm_p, &tm_pc, kb >= p_turn(w), bar,
+                                            w.i * TILE + (int)rank * HALF, kb * BK, w.e);
+                    load_operand<TN / 2, QW>(sm.b[s], &tm_q, &tm_qc, kb >= q_turn(w), bar,
+                                             w.j * TN + (int)rank * (TN / 2), kb * BK, w.e);
                 }
             }
             // drain: every issued fill, of both CTAs, has landed before the
@@ -543,29 +567,39 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 gm::tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * TN);
-                // the next slot is waited on before this slot's last MMA, so
-                // that the wait overlaps MMAs already in the pipe
+                const Item w = item(it);
+                const int turn_p = p_turn(w), turn_q = q_turn(w);
                 bool ok = mbar_wait(&sm.full[s], ph, wait_ns);
-                for (int kb = 0; ok && kb < nkb; ++kb) {
+                // one block of K; the next slot is waited on before this slot's
+                // last MMA, so that the wait overlaps MMAs already in the pipe
+                auto block = [&](int kb, auto p_columns, auto q_columns) {
+                    constexpr bool PC = decltype(p_columns)::value, QC = decltype(q_columns)::value;
+                    constexpr uint32_t ID = idesc<TN>() | (PC ? IDESC_A_COLUMNS : 0u) | (QC ? IDESC_B_COLUMNS : 0u);
+                    constexpr int P_STEP = PC ? 128 : 2, Q_STEP = QC ? QW : 2; // 16 of K: 16 rows, or 32 bytes of a row
                     gm::tc_fence_after();
-                    const uint64_t ad = gm::smem_desc_k128(smem_u32(sm.a[s]));
-                    const uint64_t bd = COLUMNS ? smem_desc_columns<QW>(smem_u32(sm.b[s]), QW * BK)
-                                                : gm::smem_desc_k128(smem_u32(sm.b[s]));
-                    // 16 of K per MMA: 32 bytes of a row, or 16 rows
-                    constexpr int Q_STEP = COLUMNS ? QW : 2;
+                    const uint32_t pa = smem_u32(sm.a[s]), qa = smem_u32(sm.b[s]);
+                    const uint64_t ad = PC ? smem_desc_columns<128>(pa, 128 * BK) : gm::smem_desc_k128(pa);
+                    const uint64_t bd = QC ? smem_desc_columns<QW>(qa, QW * BK) : gm::smem_desc_k128(qa);
 #pragma unroll
                     for (int k = 0; k < 3; ++k)
-                        mma_pair_f16<TN, COLUMNS>(d, ad + 2 * k, bd + Q_STEP * k, (kb > 0 || k > 0) ? 1u : 0u);
+                        mma_pair_f16<ID>(d, ad + P_STEP * k, bd + Q_STEP * k, (kb > 0 || k > 0) ? 1u : 0u);
                     const int s_next = s + 1 == STAGES ? 0 : s + 1;
                     const uint32_t ph_next = s + 1 == STAGES ? ph ^ 1u : ph;
                     if (kb + 1 < nkb)
                         ok = mbar_wait(&sm.full[s_next], ph_next, wait_ns);
-                    mma_pair_f16<TN, COLUMNS>(d, ad + 6, bd + 3 * Q_STEP, 1u);
+                    mma_pair_f16<ID>(d, ad + P_STEP * 3, bd + Q_STEP * 3, 1u);
                     g2::commit_pair(&sm.empty[s], 0x3);
                     issued = true;
                     s = s_next;
                     ph = ph_next;
-                }
+                };
+                int kb = 0;
+                for (; ok && kb < min(turn_q, nkb); ++kb)
+                    block(kb, std::false_type{}, std::false_type{});
+                for (; MODE != GRAM && ok && kb < min(turn_p, nkb); ++kb) // turn_q <= turn_p
+                    block(kb, std::false_type{}, std::true_type{});
+                for (; MODE != GRAM && ok && kb < nkb; ++kb)
+                    block(kb, std::true_type{}, std::true_type{});
                 if (!ok) {
                     *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
                     break;
@@ -590,11 +624,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int r = r0 + lane;
             const bool row_ok = r < q.m;
             const int cols = SYM ? q.m : q.n;
-            // this lane's column-wise position: element c of the row is `at` + c
-            // ldt elements into its matrix of A and B (a matrix has less than
-            // 2^31 elements, so 32 bits hold its byte offsets)
-            const int64_t plane = (int64_t)w.e * cols * q.ldt;
-            const uint32_t at = (uint32_t)r, ldb = (uint32_t)q.ldt * 2u;
             const bool rows_full = r0 + 32 <= q.m; // the same in every lane
             const bool rows_any = r0 < q.m;
             // what the chunk adds to the product: X (hi and lo), or A
@@ -697,13 +726,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 }
-                // down the columns
-                if (SYM || (MODE == LAST && q.out_t)) {
-                    const uint32_t ld2 = MODE == LAST ? (uint32_t)q.m * 2u : ldb;
-                    uint32_t o = (uint32_t)c0 * ld2 + at * 2u;
-                    uint8_t *dst = MODE == LAST
-                                       ? reinterpret_cast<uint8_t *>(q.out + (int64_t)w.e * cols * q.m)
-                                       : reinterpret_cast<uint8_t *>((MODE == GRAM ? q.A : q.B) + plane);
+                // G^T's update: down the columns (a matrix has less than 2^31
+                // elements, so 32 bits hold its byte offsets)
+                if (MODE == LAST && q.out_t) {
+                    const uint32_t ld2 = (uint32_t)q.m * 2u;
+                    uint32_t o = (uint32_t)c0 * ld2 + (uint32_t)r * 2u;
+                    uint8_t *dst = reinterpret_cast<uint8_t *>(q.out + (int64_t)w.e * cols * q.m);
                     auto put = [&](int k) {
                         *reinterpret_cast<uint16_t *>(dst + o) = (uint16_t)(k & 1 ? h[k >> 1] >> 16 : h[k >> 1]);
                     };
@@ -719,8 +747,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
                 // along the rows, through shared memory
-                const bool rows_too = MODE == LAST ? !q.out_t : !(SYM && w.j >= w.i * RATIO);
-                if (rows_too) {
+                if (MODE != LAST || !q.out_t) {
                     uint8_t *st = sm.stage[warp][buf];
                     if constexpr (MODE != LAST) {
                         if (lane == 0)

@@ -51,18 +51,18 @@ int ns_check(int64_t E, int64_t rows, int64_t cols, int32_t steps)
     return MXQ_OK;
 }
 
-// how a product reads or writes a matrix: boxes of 64 elements x rows for the
-// operands (128-byte swizzle; by columns 64 rows, for the narrowest tiles of 32
-// elements with the 64-byte swizzle), of 32 x 32 for the epilogue's stores
-enum NsBox { NS_STORE, NS_ROWS_128, NS_ROWS_64, NS_ROWS_32, NS_COLUMNS_32, NS_NUM_BOXES };
+// how a product reads or writes a matrix: boxes of width x rows elements, the
+// operands' with 128-byte rows and swizzle, but for narrow column tiles' 32 x 64,
+// which has the 64-byte one as the epilogue's stores
+enum NsBox { NS_STORE, NS_64x128, NS_64x64, NS_64x32, NS_32x64, NS_NUM_BOXES };
 constexpr struct {
     int width, rows;
     CUtensorMapSwizzle swizzle;
 } NS_BOXES[NS_NUM_BOXES] = {{ns::CHUNK, ns::CHUNK, CU_TENSOR_MAP_SWIZZLE_64B},
-                            {ns::BK, 128, CU_TENSOR_MAP_SWIZZLE_128B},
-                            {ns::BK, 64, CU_TENSOR_MAP_SWIZZLE_128B},
-                            {ns::BK, 32, CU_TENSOR_MAP_SWIZZLE_128B},
-                            {32, ns::BK, CU_TENSOR_MAP_SWIZZLE_64B}};
+                            {64, 128, CU_TENSOR_MAP_SWIZZLE_128B},
+                            {64, 64, CU_TENSOR_MAP_SWIZZLE_128B},
+                            {64, 32, CU_TENSOR_MAP_SWIZZLE_128B},
+                            {32, 64, CU_TENSOR_MAP_SWIZZLE_64B}};
 
 // one operand of the products: fp16 matrices by rows, a plane each, with their
 // inner length and row length, and the maps that the call has made so far
@@ -113,27 +113,28 @@ template <int MODE, int TN> int ns_pairs(int *out)
 template <int MODE, int TN>
 int ns_launch(NsOperand &p, NsOperand &q, NsOperand &o, const ns::Args &a, int pairs, cudaStream_t stream)
 {
-    const CUtensorMap *mp, *mq, *mo;
-    int rc;
     constexpr bool sym = MODE == ns::GRAM || MODE == ns::POLY;
-    constexpr NsBox rows = TN == 256 ? NS_ROWS_128 : (TN == 128 ? NS_ROWS_64 : NS_ROWS_32);
-    constexpr NsBox columns = TN == 64 ? NS_COLUMNS_32 : NS_ROWS_64;
-    if ((rc = p.map(NS_ROWS_128, &mp)) != MXQ_OK || (rc = q.map(sym ? rows : columns, &mq)) != MXQ_OK ||
+    constexpr NsBox rows = TN == 256 ? NS_64x128 : (TN == 128 ? NS_64x64 : NS_64x32);
+    constexpr NsBox columns = TN == 64 ? NS_32x64 : NS_64x64;
+    const CUtensorMap *mp, *mpc, *mq, *mqc, *mo;
+    int rc;
+    if ((rc = p.map(NS_64x128, &mp)) != MXQ_OK || (rc = p.map(NS_64x64, &mpc)) != MXQ_OK ||
+        (rc = q.map(rows, &mq)) != MXQ_OK || (rc = q.map(columns, &mqc)) != MXQ_OK ||
         (rc = o.map(NS_STORE, &mo)) != MXQ_OK)
         return rc;
     const int64_t grid = std::min<int64_t>(a.E * ns::sym_or_all_tiles<sym, TN>(a.m, a.n), pairs);
     return launch_chained(ns::k_ns_gemm<MODE, TN>, dim3((unsigned)(2 * grid)), dim3(ns::THREADS), ns::smem_bytes<TN>(),
-                          stream, true, *mp, *mq, *mo, a, (int)((p.inner + ns::BK - 1) / ns::BK), wait_ns());
+                          stream, true, *mp, *mpc, *mq, *mqc, *mo, a, (int)((p.inner + ns::BK - 1) / ns::BK), wait_ns());
 }
 
 // Tile width, by estimated time in units of a hundredth of one 64-column block
-// of a 256 x 256 tile (about 4 ns): a block of a 256 x 128 tile takes 80 (12.1
-// ms against 7.7 for all tiles of (16, 2048, 7168), twice as many), of a 256 x
-// 64 tile about 70; draining a tile takes about 1400, 700 and 350, hidden under
-// the next tile's blocks but for the last round. The narrow tiles win where
-// they spread the work over more pairs or where draining bounds: 243 us against
-// 272 at (5, 1409, 577), 113 against 144 at (4, 256, 256); the wide one at 946
-// against 1112 at (8, 1024, 4096).
+// of a 256 x 256 tile (about 4 ns): a block of a 256 x 128 tile takes about 88
+// (half the products, three quarters of the loads), of a 256 x 64 tile 75;
+// draining a tile takes about 1100, 550 and 275, hidden under the next tile's
+// blocks but for the last round. The narrow tiles win where they spread the
+// work over more pairs or where draining bounds: 238 us against 257 at (5, 1409,
+// 577), 101 against 143 at (4, 256, 256); the wide one at 361 against 425 at (8,
+// 1024, 1024), 400 against 442 at (16, 512, 2048).
 template <int MODE, int TN>
 int ns_estimate(const ns::Args &a, int64_t blocks, int64_t block_cost, int64_t drain, int *pairs, int64_t *time)
 {
@@ -154,9 +155,9 @@ int ns_product(NsOperand &p, NsOperand &q, NsOperand &o, const ns::Args &a, cuda
     const int64_t blocks = (p.inner + ns::BK - 1) / ns::BK;
     int pairs[3], rc;
     int64_t t[3];
-    if ((rc = ns_estimate<MODE, 256>(a, blocks, 100, 1400, &pairs[0], &t[0])) != MXQ_OK ||
-        (rc = ns_estimate<MODE, 128>(a, blocks, 80, 700, &pairs[1], &t[1])) != MXQ_OK ||
-        (rc = ns_estimate<MODE, 64>(a, blocks, 70, 350, &pairs[2], &t[2])) != MXQ_OK)
+    if ((rc = ns_estimate<MODE, 256>(a, blocks, 100, 1100, &pairs[0], &t[0])) != MXQ_OK ||
+        (rc = ns_estimate<MODE, 128>(a, blocks, 88, 550, &pairs[1], &t[1])) != MXQ_OK ||
+        (rc = ns_estimate<MODE, 64>(a, blocks, 75, 275, &pairs[2], &t[2])) != MXQ_OK)
         return rc;
     if (t[2] < t[1] && t[2] < t[0])
         return ns_launch<MODE, 64>(p, q, o, a, pairs[2], stream);
@@ -327,14 +328,11 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
     a.E = (int)batch;
     a.m = (int)p.m;
     a.n = (int)p.n;
-    a.ldt = (int)p.ldt;
     a.hi = reinterpret_cast<uint16_t *>(ws + p.hi);
     a.lo = reinterpret_cast<uint16_t *>(ws + p.lo);
     a.a_own = reinterpret_cast<uint16_t *>(ws + p.a_own);
     a.alpha = reinterpret_cast<float *>(ws + p.alpha);
     a.beta = reinterpret_cast<float *>(ws + p.beta);
-    a.A = reinterpret_cast<uint16_t *>(ws + p.A);
-    a.B = reinterpret_cast<uint16_t *>(ws + p.B);
     a.out = static_cast<uint16_t *>(out);
     a.out_t = p.tall;
     a.out_vec = cols % 8 == 0 && aligned(out, 16);

@@ -229,6 +229,29 @@ def test_gpu_refusals():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("tile", [0, 64, 128, 256])
+@pytest.mark.parametrize("E,N,K", [(2, 130, 135), (1, 700, 300), (1, 513, 1030)])
+def test_a_workspace_of_nans(E, N, K, tile):
+    # what a call did not write itself it does not read: half of A and B, edges
+    g = matrices(E, N, K, torch.bfloat16, 9)
+    mxq.testing_set(mxq.TESTING_NS_TILE, tile)
+    try:
+        want = mxq.newton_schulz(g)
+        L = mxq.lib()
+        nbytes = L.newton_schulz_workspace_bytes(E, N, K, 5)
+        assert nbytes > 0
+        ws = torch.full((nbytes,), 255, dtype=torch.uint8, device=DEV)
+        out = torch.empty_like(g)
+        co = (ctypes.c_float * 15)(*(COEF * 5))
+        torch.cuda.synchronize()
+        assert L.newton_schulz(g.data_ptr(), 0, E, N, K, 5, co, 1e-7, out.data_ptr(), ws.data_ptr(), nbytes, None) == 0
+        torch.cuda.synchronize()
+    finally:
+        mxq.testing_set(mxq.TESTING_NS_TILE, 0)
+    assert torch.equal(out, want)
+
+
+@pytest.mark.gpu
 def test_out_over_its_input_is_refused():
     b = torch.randn(4, 64, 96, device=DEV).bfloat16()
     f = torch.randn(2, 64, 96, device=DEV)

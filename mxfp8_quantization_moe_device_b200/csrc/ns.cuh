@@ -152,11 +152,11 @@ MXQ_DEV void load_pair(void *dst, const CUtensorMap *map, uint32_t bar, int x, i
 
 // a stage's operand of N rows or columns and 64 of K, by rows or by columns (in
 // blocks of W bytes)
-template <int N, int W>
-MXQ_DEV void load_operand(uint8_t *dst, const CUtensorMap *rows, const CUtensorMap *columns, bool by_columns,
-                          uint32_t bar, int first, int k, int e)
+template <int N, int W, bool COLUMNS>
+MXQ_DEV void load_operand(uint8_t *dst, const CUtensorMap *rows, const CUtensorMap *columns, uint32_t bar, int first,
+                          int k, int e)
 {
-    if (by_columns) {
+    if constexpr (COLUMNS) {
 #pragma unroll
         for (int c = 0; c < N; c += W / 2)
             load_pair(dst + c * 2 * BK, columns, bar, first + c, k, e);
@@ -531,20 +531,33 @@ __global__ void __launch_bounds__(THREADS, 1)
             int seq = 0;
             for (int64_t it = pair; it < total && !gm::aborted(&sm.abort_flag); it += npairs) {
                 const Item w = item(it);
-                for (int kb = 0; kb < nkb; ++kb, ++seq) {
+                const int turn_p = p_turn(w), turn_q = q_turn(w);
+                int kb = 0;
+                bool ok = true;
+                auto fill = [&](auto p_columns, auto q_columns) {
                     const int s = seq % STAGES;
                     if (seq >= STAGES && !mbar_wait(&sm.empty[s], ((uint32_t)(seq / STAGES) & 1u) ^ 1u, wait_ns)) {
                         *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
-                        break;
+                        ok = false;
+                        return;
                     }
                     if (leader)
                         mbar_arrive_expect_tx(&sm.full[s], 2 * (OP_BYTES + Smem<TN>::Q_BYTES));
                     const uint32_t bar = leader_full0 + (uint32_t)(s * sizeof(uint64_t));
-                    load_operand<HALF, 128>(sm.a[s], &tm_p, &tm_pc, kb >= p_turn(w), bar,
-                                            w.i * TILE + (int)rank * HALF, kb * BK, w.e);
-                    load_operand<TN / 2, QW>(sm.b[s], &tm_q, &tm_qc, kb >= q_turn(w), bar,
-                                             w.j * TN + (int)rank * (TN / 2), kb * BK, w.e);
-                }
+                    load_operand<HALF, 128, decltype(p_columns)::value>(sm.a[s], &tm_p, &tm_pc, bar,
+                                                                        w.i * TILE + (int)rank * HALF, kb * BK, w.e);
+                    load_operand<TN / 2, QW, decltype(q_columns)::value>(
+                        sm.b[s], &tm_q, &tm_qc, bar, w.j * TN + (int)rank * (TN / 2), kb * BK, w.e);
+                    ++kb;
+                    ++seq;
+                };
+                // a branch per block in place of these loops cost B X 10 %
+                while (ok && kb < min(turn_q, nkb))
+                    fill(std::false_type{}, std::false_type{});
+                while (MODE != GRAM && ok && kb < min(turn_p, nkb)) // turn_q <= turn_p
+                    fill(std::false_type{}, std::true_type{});
+                while (MODE != GRAM && ok && kb < nkb)
+                    fill(std::true_type{}, std::true_type{});
             }
             // drain: every issued fill, of both CTAs, has landed before the
             // leader goes to the closing barrier

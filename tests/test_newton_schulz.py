@@ -230,7 +230,7 @@ def test_gpu_refusals():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("tile", [0, 64, 128, 256])
-@pytest.mark.parametrize("E,N,K", [(2, 130, 135), (1, 700, 300), (1, 513, 1030)])
+@pytest.mark.parametrize("E,N,K", [(2, 130, 135), (1, 700, 300), (1, 513, 1030), (2, 1100, 1030)])
 def test_a_workspace_of_nans(E, N, K, tile):
     # what a call did not write itself it does not read: half of A and B, edges
     g = matrices(E, N, K, torch.bfloat16, 9)

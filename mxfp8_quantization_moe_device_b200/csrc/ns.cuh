@@ -528,15 +528,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ------------------------------------------------ TMA producer (both CTAs)
         if (lane == 0) {
             const uint32_t leader_full0 = g2::peer_addr(&sm.full[0], 0);
-            int seq = 0;
+            int s = 0, filled = 0; // the next stage, stages filled so far (up to STAGES)
+            uint32_t ph = 1;       // of the wait for it: passes at once in the first round
             for (int64_t it = pair; it < total && !gm::aborted(&sm.abort_flag); it += npairs) {
                 const Item w = item(it);
                 const int turn_p = p_turn(w), turn_q = q_turn(w);
+                const int p0 = w.i * TILE + (int)rank * HALF, q0 = w.j * TN + (int)rank * (TN / 2);
                 int kb = 0;
                 bool ok = true;
                 auto fill = [&](auto p_columns, auto q_columns) {
-                    const int s = seq % STAGES;
-                    if (seq >= STAGES && !mbar_wait(&sm.empty[s], ((uint32_t)(seq / STAGES) & 1u) ^ 1u, wait_ns)) {
+                    if (!mbar_wait(&sm.empty[s], ph, wait_ns)) {
                         *reinterpret_cast<volatile int *>(&sm.abort_flag) = 1;
                         ok = false;
                         return;
@@ -544,12 +545,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (leader)
                         mbar_arrive_expect_tx(&sm.full[s], 2 * (OP_BYTES + Smem<TN>::Q_BYTES));
                     const uint32_t bar = leader_full0 + (uint32_t)(s * sizeof(uint64_t));
-                    load_operand<HALF, 128, decltype(p_columns)::value>(sm.a[s], &tm_p, &tm_pc, bar,
-                                                                        w.i * TILE + (int)rank * HALF, kb * BK, w.e);
-                    load_operand<TN / 2, QW, decltype(q_columns)::value>(
-                        sm.b[s], &tm_q, &tm_qc, bar, w.j * TN + (int)rank * (TN / 2), kb * BK, w.e);
+                    load_operand<HALF, 128, decltype(p_columns)::value>(sm.a[s], &tm_p, &tm_pc, bar, p0, kb * BK, w.e);
+                    load_operand<TN / 2, QW, decltype(q_columns)::value>(sm.b[s], &tm_q, &tm_qc, bar, q0, kb * BK, w.e);
                     ++kb;
-                    ++seq;
+                    filled = min(filled + 1, STAGES);
+                    ph ^= s + 1 == STAGES;
+                    s = s + 1 == STAGES ? 0 : s + 1;
                 };
                 // a branch per block in place of these loops cost B X 10 %
                 while (ok && kb < min(turn_q, nkb))
@@ -560,11 +561,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     fill(std::true_type{}, std::true_type{});
             }
             // drain: every issued fill, of both CTAs, has landed before the
-            // leader goes to the closing barrier
+            // leader goes to the closing barrier; the stages before s were
+            // filled in this round (phase ph ^ 1), the others in the last
             if (leader)
-                for (int j = seq - STAGES; j < seq; ++j)
-                    if (j >= 0)
-                        mbar_wait(&sm.full[j % STAGES], (uint32_t)(j / STAGES) & 1u, wait_ns);
+                for (int j = 0; j < STAGES; ++j)
+                    if (j < s || filled == STAGES)
+                        mbar_wait(&sm.full[j], j < s ? ph ^ 1u : ph, wait_ns);
         }
     } else if (warp == EPI_WARPS + 1) {
         // ------------------------------------------------ leader: the pair's MMAs (one thread)

@@ -132,9 +132,9 @@ int ns_launch(NsOperand &p, NsOperand &q, NsOperand &o, const ns::Args &a, int p
 // (half the products, three quarters of the loads), of a 256 x 64 tile 75;
 // draining a tile takes about 1100, 550 and 275, hidden under the next tile's
 // blocks but for the last round. The narrow tiles win where they spread the
-// work over more pairs or where draining bounds: 238 us against 257 at (5, 1409,
-// 577), 101 against 143 at (4, 256, 256); the wide one at 361 against 425 at (8,
-// 1024, 1024), 400 against 442 at (16, 512, 2048).
+// work over more pairs or where draining bounds: 226 us against 253 at (5, 1409,
+// 577), 101 against 138 at (4, 256, 256); the wide one at 343 against 408 at (8,
+// 1024, 1024), 394 against 436 at (16, 512, 2048).
 template <int MODE, int TN>
 int ns_estimate(const ns::Args &a, int64_t blocks, int64_t block_cost, int64_t drain, int *pairs, int64_t *time)
 {

@@ -270,7 +270,9 @@ MXQ_DEV double loss_factor(int E, int k, double n) { return n > 0.0 ? (double)E 
 // instructions). Keys: the logit's order; 16-bit logits leave room for the
 // complement of the index below, so that one maximum gives value and index and
 // equal logits go to the lowest index; 32-bit ones carry it in a second word.
-// The next token's logits are loaded while this one is worked on.
+// The next token's logits are loaded while this one is worked on. 65536 tokens,
+// 256 experts, k = 8, bf16: 39 us, bound by the ALU pipe (2.9 instructions a
+// cycle), where reading the 34 MB would take 5.
 template <typename T, int LPT, int EPL>
 __global__ void __launch_bounds__(moe::ROUTE_THREADS)
     k_moe_route(const T *__restrict__ logits, int64_t tokens, int E, int64_t ld, const uint8_t *__restrict__ valid,
@@ -470,7 +472,7 @@ __global__ void __launch_bounds__(moe::ROUTE_THREADS)
 
 // Sums over the CTAs: a CTA of 32 warps takes 32 experts (one per lane), warp
 // w the rows w, w + 32, ...; the last CTA to finish adds the partial losses
-// in order.
+// in order. 296 CTAs' rows of 256 experts: about 5 us behind the kernel above.
 __global__ void __launch_bounds__(1024)
     k_moe_route_finish(moe::RoutePart part, int R, int E, int k, int32_t *counts, float *loss, float *loss_grad)
 {
@@ -545,6 +547,8 @@ __global__ void __launch_bounds__(1024)
 // Router backward. With G = sum_j g_j w_j and b_e = grad_loss * loss_grad[e]
 //   dl_e = p_e (b_e - sum p b) + { w_j g_j where e = id_j, - p_e G    plain
 //                                { w_j (g_j - G) where e = id_j       renormalized
+// The chosen experts' terms meet the dense ones in shared memory, one row per
+// token. 25 us at 65536 x 256, k = 8, bf16 (70 MB: 11), bound by instructions.
 template <typename T, int LPT, int EPL>
 __global__ void __launch_bounds__(moe::ROUTE_BWD_THREADS)
     k_moe_route_bwd(const T *__restrict__ logits, int64_t tokens, int E, int64_t ld, const uint8_t *__restrict__ valid,
@@ -893,7 +897,9 @@ MXQ_DEV int64_t slot_row(const int32_t *pos, int64_t i, int64_t M)
 }
 } // namespace moe
 
-// xs[pos[t][j]] = x[t]; rows from offs[E-1] to M are zero
+// xs[pos[t][j]] = x[t]; rows from offs[E-1] to M are zero. A row is read once
+// and written k times; HBM bounds it: 182 us at 16384 x 4 rows of 7168 bf16, 0.98
+// of the measured copy rate, 196 at 16384 x 8 rows of 4096.
 template <typename T, int V, int U>
 __global__ void __launch_bounds__(moe::ROW_THREADS)
     k_moe_dispatch(const T *__restrict__ x, int64_t tokens, int64_t K, int64_t ld, const int32_t *__restrict__ pos,
@@ -940,7 +946,8 @@ __global__ void __launch_bounds__(moe::ROW_THREADS)
 // slots are then looked up once a row). The loads of J slots are issued
 // together: a branch that is the same for the whole warp leaves out a dropped
 // slot, a lane behind the run's end reads the run's last vector and stores
-// nothing.
+// nothing. HBM bounds it on aligned rows: 185 us at 16384 x 4 rows of 7168 bf16
+// (floor 180); loads in flight on others: 50 at 5003 x 6 rows of 1419 fp32 (30).
 template <typename T, int V, int U, int J>
 __global__ void __launch_bounds__(moe::ROW_THREADS, V * sizeof(T) == 16 ? 4 : 5)
     k_moe_combine(const T *__restrict__ y, int64_t M, int64_t K, int64_t ld, const int32_t *__restrict__ pos,
@@ -1014,7 +1021,8 @@ __global__ void __launch_bounds__(moe::ROW_THREADS, V * sizeof(T) == 16 ? 4 : 5)
 
 // dy[pos[t][j]] = w[t][j] dout[t] and dw[t][j] = <dout[t], y[pos[t][j]]>, a
 // warp per entry; rows of dy from offs[E-1] to M are zero. dy or dw may be
-// NULL.
+// NULL. 338 us at 16384 x 4 rows of 7168 bf16, bound by HBM (floor 324, dout's row
+// re-read from L2), 77 at 5003 x 6 rows of 1419 fp32 (57).
 template <typename T, int V, int U>
 __global__ void __launch_bounds__(moe::ROW_THREADS)
     k_moe_combine_bwd(const T *__restrict__ dout, int64_t ldd, const T *__restrict__ y, int64_t ldy, int64_t M,

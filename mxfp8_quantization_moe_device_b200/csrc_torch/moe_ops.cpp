@@ -9,7 +9,6 @@
 // again in the engine's thread); here 10, 12 and 60 to 75. Nothing is computed
 // here: checks, torch allocations on the current stream, the library's calls,
 // and what the backward keeps.
-#include <ATen/MemoryOverlap.h>
 #include <ATen/cuda/CUDAContext.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -71,18 +70,37 @@ Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Device &dev)
     return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
 }
 using Given = std::optional<Tensor>; // an output that the caller may have
-Tensor output(const Given &t, const char *name, at::ScalarType type, at::IntArrayRef shape, const at::Device &dev,
-              at::TensorList inputs = {})
+Tensor output(const Given &t, const char *name, at::ScalarType type, at::IntArrayRef shape, const at::Device &dev)
 {
     if (!t || !t->defined())
         return empty(shape, type, dev);
     array(*t, name, type, shape, dev);
-    for (const Tensor &i : inputs) { // rows are read while others are written
-        const auto overlap = at::get_overlap_status(*t, i);
-        TORCH_CHECK_VALUE(overlap != at::MemOverlapStatus::Full && overlap != at::MemOverlapStatus::Partial, name,
-                          " must not overlap an input");
-    }
     return *t;
+}
+
+// Whether `out`, contiguous, shares a byte with `t`: contiguous, or rows of
+// contiguous elements that do not overlap (the gaps between them count as free).
+bool overlaps(const Tensor &out, const Tensor &t)
+{
+    if (out.numel() == 0 || t.numel() == 0)
+        return false;
+    const auto at = [](const Tensor &x) { return reinterpret_cast<intptr_t>(x.const_data_ptr()); };
+    const int64_t size = t.element_size(), lo = at(out) - at(t), hi = lo + (int64_t)out.nbytes();
+    if (t.is_contiguous())
+        return lo < (int64_t)t.nbytes() && hi > 0;
+    // rows [i step, i step + row): the first that ends behind lo must begin before hi
+    const int64_t row = t.size(1) * size, step = t.stride(0) * size;
+    const int64_t i = lo < row ? 0 : (lo - row) / step + 1;
+    return i < t.size(0) && i * step < hi;
+}
+// The kernels read some rows while others are written, so a given output
+// overlaps no input.
+void apart(const Given &out, const char *name, std::initializer_list<std::reference_wrapper<const Tensor>> inputs)
+{
+    if (!out || !out->defined())
+        return;
+    for (const Tensor &i : inputs)
+        TORCH_CHECK_VALUE(!i.defined() || !overlaps(*out, i), name, " must not overlap an input");
 }
 Tensor given(const Given &t) { return t.value_or(Tensor()); }
 Tensor workspace(size_t bytes, const at::Device &dev)
@@ -183,7 +201,8 @@ Tensor route_backward(const Tensor &logits, const Tensor &weights, const Tensor 
         array(loss_grad, "loss_grad", at::kFloat, {l.cols}, dev);
     }
     const c10::cuda::CUDAGuard guard(dev);
-    const Tensor out = output(out_, "out", logits.scalar_type(), {l.rows, l.cols}, dev, {logits});
+    const Tensor out = output(out_, "out", logits.scalar_type(), {l.rows, l.cols}, dev);
+    apart(out_, "out", {logits});
     check("moe_route_backward",
           moe_route_backward(ptr(logits), l.dtype, l.rows, l.cols, l.stride, ptr_as<uint8_t>(valid), (int)k,
                              renormalize, ptr_as<float>(weights), ptr_as<int32_t>(ids), ptr_as<float>(loss_grad),
@@ -231,7 +250,8 @@ Tensor dispatch(const Tensor &x, const Tensor &pos, const Tensor &offs, const Gi
     TORCH_CHECK_TYPE(mine || out_->dim() == 2, "out must be a (rows, cols) tensor");
     const int64_t rows = mine ? (pos.numel() + 15) / 16 * 16 : out_->size(0);
     const c10::cuda::CUDAGuard guard(dev);
-    const Tensor out = output(out_, "out", x.scalar_type(), {rows, r.cols}, dev, {x});
+    const Tensor out = output(out_, "out", x.scalar_type(), {rows, r.cols}, dev);
+    apart(out_, "out", {x});
     check("moe_dispatch", moe_dispatch(ptr(x), r.dtype, r.rows, r.cols, r.stride, ptr_as<int32_t>(pos),
                                        (int)std::min<int64_t>(pos.size(1), INT32_MAX), ptr_as<int32_t>(offs),
                                        (int)offs.numel(), out_ptr(out), rows, stream(dev)));
@@ -247,7 +267,8 @@ Tensor combine(const Tensor &y, const Tensor &pos, const Given &weights_, const 
     if (weights.defined())
         array(weights, "weights", at::kFloat, pos.sizes(), dev);
     const c10::cuda::CUDAGuard guard(dev);
-    const Tensor out = output(out_, "out", y.scalar_type(), {pos.size(0), r.cols}, dev, {y});
+    const Tensor out = output(out_, "out", y.scalar_type(), {pos.size(0), r.cols}, dev);
+    apart(out_, "out", {y});
     check("moe_combine", moe_combine(ptr(y), r.dtype, r.rows, r.cols, r.stride, ptr_as<int32_t>(pos),
                                      ptr_as<float>(weights), pos.size(0),
                                      (int)std::min<int64_t>(pos.size(1), INT32_MAX), out_ptr(out), stream(dev)));
@@ -270,9 +291,11 @@ std::tuple<Given, Given> combine_backward(const Tensor &grad_out, const Tensor &
     const c10::cuda::CUDAGuard guard(dev);
     Tensor dy, dw;
     if (need_y)
-        dy = output(grad_y_, "grad_y", y.scalar_type(), {r.rows, r.cols}, dev, {y, grad_out});
+        dy = output(grad_y_, "grad_y", y.scalar_type(), {r.rows, r.cols}, dev);
     if (need_weights)
         dw = output(grad_weights_, "grad_weights", at::kFloat, pos.sizes(), dev);
+    if (need_y)
+        apart(grad_y_, "grad_y", {y, grad_out});
     check("moe_combine_backward",
           moe_combine_backward(ptr(grad_out), g.stride, ptr(y), r.stride, r.dtype, r.rows, r.cols,
                                ptr_as<int32_t>(pos), ptr_as<float>(weights), pos.size(0),
@@ -377,6 +400,7 @@ Tensor grad_combine(const Tensor &y, const Tensor &pos, const Tensor &weights, c
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m)
 {
+    m.def("overlaps", &overlaps);
     m.def("moe_route", &route);
     m.def("moe_route_backward", &route_backward);
     m.def("moe_dispatch_plan", &plan);

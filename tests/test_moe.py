@@ -197,6 +197,24 @@ def test_fake_shapes():
     assert dy.shape == (96, 24) and dw.shape == (30, 3) and dw.dtype == torch.float32
 
 
+def test_overlap_of_an_output_with_strided_rows():
+    """Every placement of a contiguous output against rows in a wider buffer,
+    by the sets of their bytes."""
+    overlaps = mxq.torch_ops().overlaps
+    buf = torch.zeros(64, dtype=torch.bfloat16)
+    for rows, cols, stride in ((1, 5, 9), (3, 4, 4), (3, 4, 9), (4, 1, 6), (5, 3, 7)):
+        t = buf.as_strided((rows, cols), (stride, 1), 8)
+        mine = {8 + i * stride + j for i in range(rows) for j in range(cols)}
+        for n in (0, 1, 2, 5, 20):
+            for at in range(64 - n):
+                assert overlaps(buf[at:at + n], t) == bool(mine & set(range(at, at + n))), (rows, cols, stride, n, at)
+    assert not overlaps(buf, buf.as_strided((0, 4), (9, 1), 8))
+    # other types over the same memory
+    words = buf.view(torch.int32)
+    assert overlaps(words[2:5], buf[9:10]) and not overlaps(words[2:5], buf[10:12])
+    assert overlaps(buf[5:7], words[3:4]) and not overlaps(buf[4:6], words[3:4])
+
+
 @pytest.mark.gpu
 def test_registered_ops():
     import mxfp8_quantization_moe_device_b200.ops  # noqa: F401
@@ -761,3 +779,30 @@ def test_outputs_over_inputs_are_refused():
         with pytest.raises(ValueError, match="overlap"):
             call()
     assert torch.equal(mxq.moe_combine(big[:T], pos, w, out=big[T:]), mxq.moe_combine(big[:T].clone(), pos, w))
+
+
+@pytest.mark.gpu
+def test_outputs_over_strided_rows_are_refused():
+    T, E, k, K = 16, 4, 1, 64
+    buf = torch.randn(4 * T, 2 * K, device=DEV)
+    x, y, l = buf[:T, :K], buf[T:2 * T, K:], buf[2 * T:3 * T, 8:8 + E]
+    before = buf.clone()
+    g = torch.zeros(E, device=DEV)
+    w, ids, _, _ = mxq.moe_route(l, k, loss_grad=g)
+    pos, offs = mxq.moe_dispatch_plan(ids, E)
+    flat = buf.view(-1)
+    over_x = flat[2 * K:2 * K + T * K].view(T, K)  # from the second row of x on
+    over_y = flat[2 * K * T:2 * K * T + T * K].view(T, K)
+    over_l = flat[2 * T * 2 * K + 8 + E - 1:][:T * E].view(T, E)  # the first row's last logit
+    for call in (lambda: mxq.moe_dispatch(x, pos, offs, out=over_x), lambda: mxq.moe_combine(y, pos, w, out=over_y),
+                 lambda: mxq.moe_combine_backward(x, y, pos, w, offs, grad_y=over_x),
+                 lambda: mxq.moe_combine_backward(x, y, pos, w, offs, grad_y=over_y),
+                 lambda: mxq.moe_route_backward(l, w, ids, g, w, None, out=over_l)):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    assert torch.equal(buf, before)
+    # between two rows there is room
+    gap = flat[2 * K + K:2 * K + 2 * K].view(1, K)
+    row = mxq.moe_combine(x, torch.tensor([[3]], dtype=torch.int32, device=DEV), out=gap)
+    assert torch.equal(row[0], x[3])
+    assert mxq.device_status() == 0

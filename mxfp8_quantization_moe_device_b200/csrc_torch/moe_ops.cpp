@@ -94,13 +94,16 @@ bool overlaps(const Tensor &out, const Tensor &t)
     return i < t.size(0) && i * step < hi;
 }
 // The kernels read some rows while others are written, so a given output
-// overlaps no input.
-void apart(const Given &out, const char *name, std::initializer_list<std::reference_wrapper<const Tensor>> inputs)
+// overlaps no input, nor another output.
+using Tensors = std::initializer_list<std::reference_wrapper<const Tensor>>;
+void apart(const Given &out, const char *name, Tensors inputs, Tensors outputs = {})
 {
     if (!out || !out->defined())
         return;
     for (const Tensor &i : inputs)
         TORCH_CHECK_VALUE(!i.defined() || !overlaps(*out, i), name, " must not overlap an input");
+    for (const Tensor &o : outputs)
+        TORCH_CHECK_VALUE(!o.defined() || !overlaps(*out, o), name, " must not overlap another output");
 }
 Tensor given(const Given &t) { return t.value_or(Tensor()); }
 Tensor workspace(size_t bytes, const at::Device &dev)
@@ -220,6 +223,8 @@ std::tuple<Tensor, Tensor> plan(const Tensor &ids, int64_t experts, const Given 
     const c10::cuda::CUDAGuard guard(dev);
     const Tensor pos = output(pos_, "pos", at::kInt, ids.sizes(), dev);
     const Tensor offs = output(offs_, "offs", at::kInt, {experts}, dev);
+    apart(pos_, "pos", {ids}, {offs});
+    apart(offs_, "offs", {ids}, {pos});
     const size_t bytes = moe_dispatch_plan_workspace_bytes(ids.numel(), experts);
     const Tensor ws = workspace(bytes, dev);
     check("moe_dispatch_plan", moe_dispatch_plan(ptr_as<int32_t>(ids), ids.numel(), experts, out_as<int32_t>(pos),

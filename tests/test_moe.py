@@ -806,3 +806,25 @@ def test_outputs_over_strided_rows_are_refused():
     row = mxq.moe_combine(x, torch.tensor([[3]], dtype=torch.int32, device=DEV), out=gap)
     assert torch.equal(row[0], x[3])
     assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,k", [(1, 1), (16, 2), (2048, 2), (5000, 4)])  # one tile, one launch of several, two launches
+def test_places_over_their_ids_are_refused(T, k):
+    E = 8
+    ids = ids_of(T, E, k, T).to(DEV)
+    want = mxq.moe_dispatch_plan(ids, E)
+    buf = torch.zeros(2 * T * k + E, dtype=torch.int32, device=DEV)
+    inside = buf[E:E + T * k].view(T, k)
+    inside.copy_(ids)
+    before = buf.clone()
+    for call in (lambda: mxq.moe_dispatch_plan(inside, E, pos=inside), lambda: mxq.moe_dispatch_plan(inside, E, offs=buf[1:E + 1]),
+                 lambda: mxq.moe_dispatch_plan(inside, E, pos=buf[E + T * k - 1:][:T * k].view(T, k)),
+                 lambda: mxq.moe_dispatch_plan(ids, E, pos=inside, offs=buf[1:E + 1])):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    assert torch.equal(buf, before)
+    # right beside one another
+    got = mxq.moe_dispatch_plan(inside, E, pos=buf[E + T * k:].view(T, k), offs=buf[:E])
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(inside, ids)
+    assert mxq.device_status() == 0

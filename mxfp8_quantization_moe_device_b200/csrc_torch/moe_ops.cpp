@@ -174,6 +174,11 @@ std::tuple<Tensor, Tensor, Tensor, Tensor> route(const Tensor &logits, int64_t k
     const Tensor ids = output(ids_, "ids", at::kInt, {l.rows, k}, dev);
     const Tensor counts = output(counts_, "counts", at::kInt, {l.cols}, dev);
     const Tensor loss = output(loss_, "loss", at::kFloat, {}, dev);
+    apart(weights_, "weights", {logits, valid}, {ids, counts, loss, loss_grad});
+    apart(ids_, "ids", {logits, valid}, {counts, loss, loss_grad});
+    apart(counts_, "counts", {logits, valid}, {loss, loss_grad});
+    apart(loss_, "loss", {logits, valid}, {loss_grad});
+    apart(loss_grad_, "loss_grad", {logits, valid});
     const size_t bytes = moe_route_workspace_bytes(l.rows, l.cols);
     const Tensor ws = workspace(bytes, dev);
     check("moe_route", moe_route(ptr(logits), l.dtype, l.rows, l.cols, l.stride, ptr_as<uint8_t>(valid),
@@ -205,7 +210,7 @@ Tensor route_backward(const Tensor &logits, const Tensor &weights, const Tensor 
     }
     const c10::cuda::CUDAGuard guard(dev);
     const Tensor out = output(out_, "out", logits.scalar_type(), {l.rows, l.cols}, dev);
-    apart(out_, "out", {logits});
+    apart(out_, "out", {logits, valid, weights, ids, loss_grad, gw, gl});
     check("moe_route_backward",
           moe_route_backward(ptr(logits), l.dtype, l.rows, l.cols, l.stride, ptr_as<uint8_t>(valid), (int)k,
                              renormalize, ptr_as<float>(weights), ptr_as<int32_t>(ids), ptr_as<float>(loss_grad),

@@ -828,3 +828,45 @@ def test_places_over_their_ids_are_refused(T, k):
     got = mxq.moe_dispatch_plan(inside, E, pos=buf[E + T * k:].view(T, k), offs=buf[:E])
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(inside, ids)
     assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_outputs_of_the_router_apart():
+    T, E, k = 40, 8, 2
+    l = torch.randn(T, E, device=DEV)
+    valid = torch.ones(T, dtype=torch.bool, device=DEV)
+    g = torch.zeros(E, device=DEV)
+    w, ids, _, _ = mxq.moe_route(l, k, valid=valid, loss_grad=g)
+    flat = l.view(-1)
+    ints = flat.view(torch.int32)
+    a = torch.zeros(T * k, device=DEV)
+    gw, gl = torch.ones(T, k, device=DEV), torch.ones((), device=DEV)
+    big = torch.zeros(4 * T * E, device=DEV)
+    kept = [t.clone() for t in (l, valid, a, w, ids, g)]
+    for call in (lambda: mxq.moe_route(l, k, weights=flat[T * E - T * k:].view(T, k)),
+                 lambda: mxq.moe_route(l, k, ids=ints[:T * k].view(T, k)),
+                 lambda: mxq.moe_route(l, k, counts=ints[5:5 + E]), lambda: mxq.moe_route(l, k, loss=flat[7]),
+                 lambda: mxq.moe_route(l, k, loss_grad=flat[:E]),
+                 lambda: mxq.moe_route(l, k, valid=valid, counts=valid.view(torch.int32)[2:2 + E]),
+                 lambda: mxq.moe_route(l, k, weights=a.view(T, k), ids=a.view(torch.int32).view(T, k)),
+                 lambda: mxq.moe_route(l, k, weights=a.view(T, k), loss=a[3]),
+                 lambda: mxq.moe_route(l, k, loss=g[E - 1], loss_grad=g),
+                 lambda: mxq.moe_route(l, k, counts=a[:E].view(torch.int32), loss_grad=a[E - 1:2 * E - 1])):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    for t, n in ((w, T * k), (gw, T * k), (ids, T * k), (g, E), (gl, 1)):
+        part = big[T * E - n:T * E].view(t.dtype).view(t.shape)
+        part.copy_(t)
+        args = [part if t is x else x for x in (w, ids, g, gw, gl)]
+        with pytest.raises(ValueError, match="overlap"):
+            mxq.moe_route_backward(l, *args, out=big[:T * E].view(T, E))
+        want = mxq.moe_route_backward(l, w, ids, g, gw, gl)
+        assert torch.equal(mxq.moe_route_backward(l, *args, out=big[T * E:2 * T * E].view(T, E)), want)
+    assert all(torch.equal(t, b) for t, b in zip((l, valid, a, w, ids, g), kept))
+    # side by side in one buffer
+    o = torch.zeros(2 * T * k + 2 * E + 1, device=DEV)
+    i = o.view(torch.int32)
+    got = mxq.moe_route(l, k, weights=o[:T * k].view(T, k), ids=i[T * k:2 * T * k].view(T, k), counts=i[2 * T * k:][:E],
+                        loss=o[-1], loss_grad=o[2 * T * k + E:][:E])
+    assert all(torch.equal(a, b) for a, b in zip(got, mxq.moe_route(l, k))) and torch.equal(o[-1 - E:-1], g)
+    assert mxq.device_status() == 0

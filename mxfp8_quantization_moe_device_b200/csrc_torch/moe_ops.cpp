@@ -261,7 +261,7 @@ Tensor dispatch(const Tensor &x, const Tensor &pos, const Tensor &offs, const Gi
     const int64_t rows = mine ? (pos.numel() + 15) / 16 * 16 : out_->size(0);
     const c10::cuda::CUDAGuard guard(dev);
     const Tensor out = output(out_, "out", x.scalar_type(), {rows, r.cols}, dev);
-    apart(out_, "out", {x});
+    apart(out_, "out", {x, pos, offs});
     check("moe_dispatch", moe_dispatch(ptr(x), r.dtype, r.rows, r.cols, r.stride, ptr_as<int32_t>(pos),
                                        (int)std::min<int64_t>(pos.size(1), INT32_MAX), ptr_as<int32_t>(offs),
                                        (int)offs.numel(), out_ptr(out), rows, stream(dev)));
@@ -278,7 +278,7 @@ Tensor combine(const Tensor &y, const Tensor &pos, const Given &weights_, const 
         array(weights, "weights", at::kFloat, pos.sizes(), dev);
     const c10::cuda::CUDAGuard guard(dev);
     const Tensor out = output(out_, "out", y.scalar_type(), {pos.size(0), r.cols}, dev);
-    apart(out_, "out", {y});
+    apart(out_, "out", {y, pos, weights});
     check("moe_combine", moe_combine(ptr(y), r.dtype, r.rows, r.cols, r.stride, ptr_as<int32_t>(pos),
                                      ptr_as<float>(weights), pos.size(0),
                                      (int)std::min<int64_t>(pos.size(1), INT32_MAX), out_ptr(out), stream(dev)));
@@ -305,7 +305,9 @@ std::tuple<Given, Given> combine_backward(const Tensor &grad_out, const Tensor &
     if (need_weights)
         dw = output(grad_weights_, "grad_weights", at::kFloat, pos.sizes(), dev);
     if (need_y)
-        apart(grad_y_, "grad_y", {y, grad_out});
+        apart(grad_y_, "grad_y", {y, grad_out, pos, weights, offs}, {dw});
+    if (need_weights)
+        apart(grad_weights_, "grad_weights", {y, grad_out, pos, weights, offs}, {dy});
     check("moe_combine_backward",
           moe_combine_backward(ptr(grad_out), g.stride, ptr(y), r.stride, r.dtype, r.rows, r.cols,
                                ptr_as<int32_t>(pos), ptr_as<float>(weights), pos.size(0),

@@ -870,3 +870,44 @@ def test_outputs_of_the_router_apart():
                         loss=o[-1], loss_grad=o[2 * T * k + E:][:E])
     assert all(torch.equal(a, b) for a, b in zip(got, mxq.moe_route(l, k))) and torch.equal(o[-1 - E:-1], g)
     assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,k,K", [(16, 2, 64), (300, 3, 130)])
+def test_outputs_of_the_row_movement_apart(T, k, K):
+    E = 5
+    x = torch.randn(T, K, device=DEV)
+    w, dout = torch.rand(T, k, device=DEV), torch.randn(T, K, device=DEV)
+    pos, offs = mxq.moe_dispatch_plan(ids_of(T, E, k, 3, 0.2).to(DEV), E)
+    M = mxq.moe_dispatch_rows(T * k)
+    y = mxq.moe_dispatch(x, pos, offs)
+    out, (dy, dw) = mxq.moe_combine(y, pos, w), mxq.moe_combine_backward(dout, y, pos, w, offs)
+    size = max(M * K, T * K)
+    big = torch.zeros(2 * size, device=DEV)
+    calls = {"dispatch": lambda p, o, ww, at: mxq.moe_dispatch(x, p, o, out=big[at:at + M * K].view(M, K)),
+             "combine": lambda p, o, ww, at: mxq.moe_combine(y, p, ww, out=big[at:at + T * K].view(T, K)),
+             "rows": lambda p, o, ww, at: mxq.moe_combine_backward(dout, y, p, ww, o, grad_y=big[at:at + M * K].view(M, K))[0]}
+    want = {"dispatch": y, "combine": out, "rows": dy}
+    reads = {"dispatch": (pos, offs), "combine": (pos, w), "rows": (pos, offs, w)}
+    for name, call in calls.items():
+        for t in reads[name]:
+            part = big[5:5 + t.numel()].view(t.dtype).view(t.shape)
+            part.copy_(t)
+            args = [part if t is v else v for v in (pos, offs, w)]
+            with pytest.raises(ValueError, match="overlap an input"):
+                call(*args, 0)
+            assert torch.equal(call(*args, size), want[name])
+    # the weights' gradient over what is read, and over the rows'
+    buf = torch.zeros(M * K + T * k, device=DEV)
+    over = buf[M * K - 1:][:T * k].view(T, k)
+    for kw in ({"grad_weights": w}, {"grad_weights": pos.view(torch.float32)}, {"grad_weights": dout.view(-1)[:T * k].view(T, k)},
+               {"grad_weights": y.view(-1)[K:][:T * k].view(T, k)}, {"grad_weights": w, "need_y": False},
+               {"grad_y": buf[:M * K].view(M, K), "grad_weights": over}):
+        with pytest.raises(ValueError, match="overlap"):
+            mxq.moe_combine_backward(dout, y, pos, w, offs, **kw)
+    a = mxq.moe_combine_backward(dout, y, pos, w, offs, grad_y=buf[:M * K].view(M, K), grad_weights=buf[M * K:].view(T, k))
+    assert torch.equal(a[0], dy) and torch.equal(a[1], dw)
+    # what is not asked for is not looked at
+    b = mxq.moe_combine_backward(dout, y, pos, w, offs, need_weights=False, grad_weights=w)
+    assert torch.equal(b[0], dy) and b[1] is None
+    assert mxq.device_status() == 0

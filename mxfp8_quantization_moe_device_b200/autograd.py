@@ -194,7 +194,8 @@ def fp8_grouped_mm(a, w, offs):
 # Their autograd nodes are C++ (csrc_torch/moe_ops.cpp): a call is a few
 # launches of microseconds, and a Python node would cost more than they do.
 # Inside a stream capture they refuse an input whose autograd graph was built on
-# the default stream and still lives: the captured backward would wait there.
+# the default stream and still lives, and their backward a pass that reaches
+# such a graph anywhere behind them: the captured backward would wait there.
 
 def moe_route(logits, top_k, *, valid=None, renormalize=False):
     """(weights (T, top_k) fp32, ids (T, top_k) int32, counts (E,) int32, loss

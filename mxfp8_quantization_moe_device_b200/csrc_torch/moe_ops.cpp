@@ -13,7 +13,11 @@
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/graph_task.h>
 #include <torch/extension.h>
+
+#include <unordered_set>
+#include <vector>
 
 #include "mxq.h"
 
@@ -137,18 +141,52 @@ variable_list once(variable_list grads)
 // stream capture, a leaf or node whose own stream is the default one (a graph
 // that was built before the capture and still lives) would have the captured
 // pass wait on that stream, which breaks the capture and can end the process.
+// The forward refuses such an input, the backward such a node anywhere behind it.
+bool capturing(const at::Device &dev)
+{
+    const c10::cuda::CUDAGuard guard(dev);
+    return c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None;
+}
+bool on_default_stream(torch::autograd::Node &node)
+{
+    const auto at = node.stream();
+    return at && at->device_type() == at::kCUDA && *at == c10::cuda::getDefaultCUDAStream(at->device_index()).unwrap();
+}
+constexpr const char *LIVING = " belongs to an autograd graph built on the default stream before this capture; free that"
+                               " graph first (and warm up on a side stream), or capture without gradients";
+
 void check_capture(const Tensor &t, const char *name)
 {
-    if (!at::GradMode::is_enabled() || !t.requires_grad() || !t.is_cuda())
-        return;
-    const c10::cuda::CUDAGuard guard(t.device());
-    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None)
+    if (!at::GradMode::is_enabled() || !t.requires_grad() || !t.is_cuda() || !capturing(t.device()))
         return;
     const auto node = t.grad_fn() ? t.grad_fn() : torch::autograd::impl::try_get_grad_accumulator(t);
-    const auto at = node ? node->stream() : std::nullopt;
-    TORCH_CHECK(!at || *at != c10::cuda::getDefaultCUDAStream(t.device().index()).unwrap(), name,
-                " belongs to an autograd graph built on the default stream before this capture; free that graph first"
-                " (and warm up on a side stream), or capture without gradients");
+    TORCH_CHECK(!node || !on_default_stream(*node), name, LIVING);
+}
+
+// in a node's backward: the nodes that this pass reaches through it
+void check_captured_pass(const at::Device &dev)
+{
+    if (!capturing(dev))
+        return;
+    const auto *runs = torch::autograd::get_current_graph_task_exec_info(); // empty: all do
+    std::unordered_set<torch::autograd::Node *> seen;
+    std::vector<torch::autograd::Node *> open{torch::autograd::get_current_node().get()};
+    while (!open.empty()) {
+        torch::autograd::Node *const node = open.back();
+        open.pop_back();
+        for (const auto &edge : node->next_edges()) {
+            torch::autograd::Node *const next = edge.function.get();
+            if (!next || !seen.insert(next).second)
+                continue;
+            if (runs && !runs->empty()) {
+                const auto at = runs->find(next);
+                if (at == runs->end() || !at->second.should_execute())
+                    continue;
+            }
+            TORCH_CHECK(!on_default_stream(*next), next->name(), LIVING);
+            open.push_back(next);
+        }
+    }
 }
 
 // ------------------------------------------------------------------ calls
@@ -339,6 +377,7 @@ struct MoERoute : torch::autograd::Function<MoERoute> {
         if (gw.defined())
             gw = gw.contiguous();
         const auto saved = ctx->get_saved_variables();
+        check_captured_pass(saved[0].device());
         const Tensor out = route_backward(saved[0], saved[1], saved[2], saved[3], gw, gl, saved[4],
                                           ctx->saved_data["renormalize"].toBool(), {});
         return once({out, Tensor(), Tensor(), Tensor()});
@@ -362,6 +401,7 @@ struct MoEDispatch : torch::autograd::Function<MoEDispatch> {
         if (!grads[0].defined())
             return {Tensor(), Tensor(), Tensor()};
         const Tensor pos = ctx->get_saved_variables()[0];
+        check_captured_pass(pos.device());
         return once({combine(grads[0].contiguous(), pos, {}, {}), Tensor(), Tensor()});
     }
 };
@@ -382,6 +422,7 @@ struct MoECombine : torch::autograd::Function<MoECombine> {
         if (!grads[0].defined())
             return {Tensor(), Tensor(), Tensor(), Tensor()};
         const auto saved = ctx->get_saved_variables();
+        check_captured_pass(saved[0].device());
         auto [dy, dw] = combine_backward(grads[0].contiguous(), saved[0], saved[1], saved[2], saved[3],
                                          ctx->needs_input_grad(0), ctx->needs_input_grad(2), {}, {});
         return once({given(dy), Tensor(), given(dw), Tensor()});

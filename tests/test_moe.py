@@ -911,3 +911,55 @@ def test_outputs_of_the_row_movement_apart(T, k, K):
     b = mxq.moe_combine_backward(dout, y, pos, w, offs, need_weights=False, grad_weights=w)
     assert torch.equal(b[0], dy) and b[1] is None
     assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_captured_backward_into_a_living_graph_is_refused():
+    """The inputs come out of operations within the capture, the leaf behind
+    them also belongs to a graph on the default stream that lives on."""
+    T, E, k, K = 64, 8, 2, 64
+    x = torch.randn(T, K, device=DEV)
+    bias = torch.randn(E, device=DEV, requires_grad=True)
+    base = torch.randn(T, E, device=DEV)
+    scale = torch.ones(K, device=DEV, requires_grad=True)
+    share = torch.ones((), device=DEV, requires_grad=True)
+    keep = [base + bias, x * scale, share * 1.0]
+    w, ids, _, _ = mxq.moe_route(keep[0].detach(), k)
+    xs, pos, offs = autograd.moe_dispatch(x, ids, E)
+    dl = torch.randn(T, k, device=DEV)
+    dx, dout = torch.randn(xs.shape, device=DEV), torch.randn(T, K, device=DEV)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        logits = base + bias
+        got, _, _, loss = autograd.moe_route(logits, k)
+        rows = autograd.moe_dispatch(x * scale, ids, E)[0]
+        out = autograd.moe_combine(xs, pos, w * share, offs)
+        both = autograd.moe_combine(rows, pos, w, offs)
+        for call in (lambda: torch.autograd.grad(got, bias, dl, retain_graph=True),
+                     lambda: torch.autograd.grad(loss, bias, retain_graph=True),
+                     lambda: got.backward(dl, retain_graph=True),
+                     lambda: torch.autograd.grad(rows, scale, dx, retain_graph=True),
+                     lambda: torch.autograd.grad(out, share, dout, retain_graph=True),
+                     lambda: torch.autograd.grad(both, scale, dout, retain_graph=True)):
+            with pytest.raises(RuntimeError, match="default stream before this capture"):
+                call()
+        (inner,) = torch.autograd.grad(got, logits, dl)  # ends before the leaf
+    gr.replay()
+    torch.cuda.synchronize()
+    l = keep[0].detach().requires_grad_(True)
+    assert torch.equal(got, w) and torch.equal(inner, torch.autograd.grad(autograd.moe_route(l, k)[0], l, dl)[0])
+    assert bias.grad is None and torch.equal(both, mxq.moe_combine(mxq.moe_dispatch(x, pos, offs), pos, w))
+    # the same with that graph gone
+    del keep, logits, got, loss, rows, out, both, call
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.autograd.grad(autograd.moe_route(base + bias, k)[0], bias, dl)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        (d,) = torch.autograd.grad(autograd.moe_route(base + bias, k)[0], bias, dl)
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(d, torch.autograd.grad(autograd.moe_route(base + bias, k)[0], bias, dl)[0])
+    assert mxq.device_status() == 0

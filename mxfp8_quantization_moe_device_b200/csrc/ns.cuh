@@ -24,8 +24,14 @@
 //     and X <- (a + beta_r) X + B' X, row by row. On random 64 x 1000 matrices
 //     1.9e-3 falls to 2.5e-4, on 512 x 512 ones 1.5e-3 to 7e-4.
 // Scales are powers of two: X 2^8 (a random 2048 x 7168 matrix starts with
-// elements near 2^-12, fp16's normal range ends at 2^-14), A' and B' 2^10, lo
-// 2^11 on top of X's.
+// elements near 2^-12, fp16's normal range ends at 2^-14), lo 2^11 on top of
+// X's, A' 2^10, B' 2^10 or as much less as the step's coefficients ask for.
+// With singular values s <= 4 the elements of A are at most 16, but those of B
+// up to the largest |b s^2 + c s^4|: 444 for the usual coefficients at s = 4,
+// while 2^10 B' ends at 64. The host bounds s from step to step (s <= 1 at the
+// start) and with it B. The smaller scale costs what small elements lose below
+// fp16's normal range: an absolute error of B (at most 2^-27), beside the a of
+// order one that it is added to.
 //
 // Every matrix is written once, by rows, and read by rows or by columns
 // (K-major or MN-major) as a product needs it. A = X X^T takes X by rows twice,
@@ -78,7 +84,7 @@ constexpr int CHUNK_BYTES = CHUNK * CHUNK * 2;
 constexpr int MAX_PARTS = 256;         // partial sums of squares per matrix
 
 constexpr float SX = 256.0f;           // stored X  = X 2^8
-constexpr float SA = 1024.0f;          // stored A', B' = A', B' 2^10
+constexpr float SA = 1024.0f;          // stored A' = A' 2^10, and B' unless its range asks for less
 constexpr float SLO = 2048.0f;         // stored lo = (X 2^8 - hi) 2^11
 
 template <int TN> struct __align__(1024) Smem {
@@ -108,6 +114,8 @@ enum Mode { GRAM = 0, POLY = 1, STEP = 2, LAST = 3 };
 struct Args {
     int E, m, n;          // batch, X is (m, n)
     float a, b, c;
+    float pb, pc;         // b and c times the scale of B' over that of A'
+    float unscale;        // one over the scale of B'
     uint16_t *hi, *lo;    // X as the epilogue keeps it: chunks of (m, n)
     uint16_t *a_own;      // A' as the epilogue keeps it: chunks of (m, m)
     float *alpha, *beta;  // (E, m): the diagonals of A and B
@@ -701,12 +709,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if constexpr (MODE == POLY) {
                             const float a0 = own + __shfl_sync(0xffffffffu, alpha_c, 2 * k);
                             const float a1 = own + __shfl_sync(0xffffffffu, alpha_c, 2 * k + 1);
-                            v0 = fmaf(q.c * (1.0f / SA), d0, fmaf(q.c, a0, q.b) * oh.x);
-                            v1 = fmaf(q.c * (1.0f / SA), d1, fmaf(q.c, a1, q.b) * oh.y);
+                            v0 = fmaf(q.pc * (1.0f / SA), d0, fmaf(q.pc, a0, q.pb) * oh.x);
+                            v1 = fmaf(q.pc * (1.0f / SA), d1, fmaf(q.pc, a1, q.pb) * oh.y);
                         } else {
                             const float2 ol = unpack_half2(word_of(old_l[k >> 2], k & 3));
-                            v0 = fmaf(own, fmaf(ol.x, 1.0f / SLO, oh.x), d0 * (1.0f / SA));
-                            v1 = fmaf(own, fmaf(ol.y, 1.0f / SLO, oh.y), d1 * (1.0f / SA));
+                            v0 = fmaf(own, fmaf(ol.x, 1.0f / SLO, oh.x), d0 * q.unscale);
+                            v1 = fmaf(own, fmaf(ol.y, 1.0f / SLO, oh.y), d1 * q.unscale);
                         }
                     }
                     if constexpr (SYM) {

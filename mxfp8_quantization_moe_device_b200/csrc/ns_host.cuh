@@ -51,6 +51,53 @@ int ns_check(int64_t E, int64_t rows, int64_t cols, int32_t steps)
     return MXQ_OK;
 }
 
+// The largest |a s + b s^3 + c s^5| (what a step makes of a singular value s)
+// and |b s^2 + c s^4| (B) for s in [0, r], at the end or where the derivative is
+// zero.
+double ns_largest_x(double a, double b, double c, double r)
+{
+    const auto at = [&](double u) { return std::fabs(std::sqrt(u) * (a + u * (b + u * c))); };
+    double most = at(r * r);
+    const double disc = 9.0 * b * b - 20.0 * a * c; // a + 3 b u + 5 c u^2 = 0
+    if (disc >= 0.0) {
+        const double q = -0.5 * (3.0 * b + std::copysign(std::sqrt(disc), b));
+        for (const double u : {q / (5.0 * c), a / q})
+            if (u > 0.0 && u < r * r)
+                most = std::max(most, at(u));
+    }
+    return most;
+}
+double ns_largest_b(double b, double c, double r)
+{
+    const auto at = [&](double u) { return std::fabs(u * (b + u * c)); };
+    const double u = -b / (2.0 * c);
+    return u > 0.0 && u < r * r ? std::max(at(r * r), at(u)) : at(r * r);
+}
+
+// The coefficients with the scale of B' over that of A' in every step. The
+// singular values are bounded by 1 at the start, then by what a step makes of
+// them, and by 4 by the caller's word; 2^-8 more for what rounding adds, and B
+// stays a factor of two from fp16's end.
+constexpr double NS_LARGEST = 4.0;
+ns::Coefs ns_coefs(const float *coefficients, int32_t steps)
+{
+    ns::Coefs co = {};
+    std::memcpy(co.v, coefficients, sizeof(float) * 3 * (size_t)steps);
+    double r = 1.0 + 0x1p-8;
+    for (int s = 0; s < steps; ++s) {
+        const float a = co.v[3 * s], b = co.v[3 * s + 1], c = co.v[3 * s + 2];
+        const double most = ns_largest_b(b, c, r) * ns::SA;
+        float part = 1.0f;
+        while (most * part > 32752.0)
+            part *= 0.5f;
+        co.pb[s] = b * part;
+        co.pc[s] = c * part;
+        co.unscale[s] = 1.0f / (ns::SA * part);
+        r = std::min(NS_LARGEST, ns_largest_x(a, b, c, r) * (1.0 + 0x1p-8));
+    }
+    return co;
+}
+
 // how a product reads or writes a matrix: boxes of width x rows elements, the
 // operands' with 128-byte rows and swizzle, but for narrow column tiles' 32 x 64,
 // which has the 64-byte one as the epilogue's stores
@@ -258,8 +305,7 @@ int ns_small(const T *g, int64_t E, int64_t rows, int64_t cols, int32_t steps, c
     const int rc = ns_small_attributes<T>();
     if (rc != MXQ_OK)
         return rc;
-    ns::Coefs co;
-    std::memcpy(co.v, coefficients, sizeof(float) * 3 * (size_t)steps);
+    const ns::Coefs co = ns_coefs(coefficients, steps);
     const int ctas = (int)((std::max(rows, cols) + ns::SM_SLAB - 1) / ns::SM_SLAB);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -297,7 +343,7 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
         return MXQ_ERR_NULL;
     if (!(eps >= 0.0) || eps > 1e30)
         return MXQ_ERR_UNSUPPORTED;
-    // larger coefficients would leave fp16's range in B
+    // up to here the scale of B' (ns_coefs) holds singular values of up to 4
     for (int i = 0; i < 3 * steps; ++i)
         if (!(coefficients[i] >= -16.0f && coefficients[i] <= 16.0f))
             return MXQ_ERR_UNSUPPORTED;
@@ -336,10 +382,14 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
     a.out = static_cast<uint16_t *>(out);
     a.out_t = p.tall;
     a.out_vec = cols % 8 == 0 && aligned(out, 16);
+    const ns::Coefs co = ns_coefs(coefficients, steps);
     for (int s = 0; s < steps; ++s) {
-        a.a = coefficients[3 * s];
-        a.b = coefficients[3 * s + 1];
-        a.c = coefficients[3 * s + 2];
+        a.a = co.v[3 * s];
+        a.b = co.v[3 * s + 1];
+        a.c = co.v[3 * s + 2];
+        a.pb = co.pb[s];
+        a.pc = co.pc[s];
+        a.unscale = co.unscale[s];
         NsOperand &x = xs[s & 1], &next = xs[(s + 1) & 1];
         if ((rc = ns_product<ns::GRAM>(x, x, A, a, stream)) != MXQ_OK ||
             (rc = ns_product<ns::POLY>(A, A, B, a, stream)) != MXQ_OK ||

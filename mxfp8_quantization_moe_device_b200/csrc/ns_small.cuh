@@ -35,6 +35,8 @@ constexpr int MAX_STEPS = 64;
 
 struct Coefs {
     float v[3 * MAX_STEPS];
+    float pb[MAX_STEPS], pc[MAX_STEPS]; // b and c times the scale of B' over that of A'
+    float unscale[MAX_STEPS];           // one over the scale of B'
 };
 
 struct __align__(1024) SmallSmem {
@@ -296,6 +298,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
 #pragma unroll 1
     for (int s = 0; s < steps; ++s) {
         const float cb = co.v[3 * s + 1], cc = co.v[3 * s + 2];
+        const float pb = co.pb[s], pc = co.pc[s];
         // ---- A = X X^T
         product(d_a, sm.xh[0], sm.xh[0], false, m16, n16);
         if (active) {
@@ -389,10 +392,10 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
                         for (int k = 0; k < 4; ++k) {
                             const float2 f = unpack_half2(w[k]);
                             const float2 ac = *reinterpret_cast<const float2 *>(&sm.alpha[32 * ch + 8 * q + 2 * k]);
-                            h[k] = pack_half2(fmaf(cc * (1.0f / SA), __uint_as_float(v[8 * q + 2 * k]),
-                                                   fmaf(cc, alpha_r + ac.x, cb) * f.x),
-                                              fmaf(cc * (1.0f / SA), __uint_as_float(v[8 * q + 2 * k + 1]),
-                                                   fmaf(cc, alpha_r + ac.y, cb) * f.y));
+                            h[k] = pack_half2(fmaf(pc * (1.0f / SA), __uint_as_float(v[8 * q + 2 * k]),
+                                                   fmaf(pc, alpha_r + ac.x, pb) * f.x),
+                                              fmaf(pc * (1.0f / SA), __uint_as_float(v[8 * q + 2 * k + 1]),
+                                                   fmaf(pc, alpha_r + ac.y, pb) * f.y));
                         }
                         *reinterpret_cast<uint4 *>(p) = make_uint4(h[0], h[1], h[2], h[3]);
                     }
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
         // ---- X = (a + beta) X + B' X
         product(d_y, sm.ab[0], sm.xh[0], true, n16, m16);
         if (active) {
-            const float scale = co.v[3 * s] + sm.beta[r];
+            const float scale = co.v[3 * s] + sm.beta[r], unscale = co.unscale[s];
 #pragma unroll 1
             for (int ch = part; 32 * ch < n16; ch += 4) {
                 uint32_t v[32], y[32];
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1)
 #pragma unroll
                 for (int k = 0; k < 32; ++k) // behind n16 no product was written, and X is zero
                     x[k] = fmaf(scale, __uint_as_float(v[k]),
-                                32 * ch + (k & 16) < n16 ? __uint_as_float(y[k]) * (1.0f / SA) : 0.0f);
+                                32 * ch + (k & 16) < n16 ? __uint_as_float(y[k]) * unscale : 0.0f);
                 const int c0 = 32 * ch;
                 if (s + 1 < steps) {
                     put_x(c0, x);

@@ -307,3 +307,95 @@ def test_update_from_the_weight_gradient():
     up = mxq.newton_schulz(dw)
     assert bool((up[1] == 0).all())  # the expert without tokens
     check(up[[0, 2]], dw[[0, 2]], [COEF] * 5)
+
+
+# ------------------------------------------------------------ large values on the way
+def emulate_wide(g, coefs, b_scales, eps=1e-7):
+    """`emulate` with a scale of B of its own in every step, so that B' stays
+    within fp16 where singular values come near to 4."""
+    def half(v, scale):
+        return (v * scale).half().double() / scale
+
+    x = g.double()
+    x = x / (torch.linalg.vector_norm(x, dim=(-2, -1), keepdim=True) + eps)
+    t = x.shape[-2] > x.shape[-1]
+    x = x.mT if t else x
+    for (a, b, c), scale in zip(coefs, b_scales):
+        hi = half(x, 256.0)
+        x = hi + half(x - hi, 256.0 * 2048.0)
+        A = hi @ hi.mT
+        alpha = torch.diagonal(A, dim1=-2, dim2=-1)
+        A = half(A - torch.diag_embed(alpha), 1024.0)
+        D = A @ A
+        beta = b * alpha + c * alpha * alpha + c * torch.diagonal(D, dim1=-2, dim2=-1)
+        B = c * D + (b + c * (alpha[..., :, None] + alpha[..., None, :])) * A
+        B = half(B - torch.diag_embed(torch.diagonal(B, dim1=-2, dim2=-1)), scale)
+        x = (a + beta)[..., None] * x + B @ hi
+    x = x.mT if t else x
+    return x.bfloat16().double()
+
+
+WIDE = [(2, 96, 224), (2, 224, 96), (2, 100, 257), (1, 17, 1300), (2, 300, 260), (1, 513, 1030), (1, 700, 300)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,N,K", WIDE)
+@pytest.mark.parametrize("second,scale", [(COEF, 64.0), ((16.0, 16.0, 16.0), 4.0), ((0.5, -15.0, 0.0), 64.0)])
+def test_singular_values_near_four(E, N, K, second, scale):
+    """Two like rows (or columns) hold nearly all of G, so its singular value
+    after the first step is nearly 3.9 and B has 198, 1972 and -114 off its
+    diagonal: times 2^10, what A is stored in, the first two are past fp16."""
+    x = matrices(E, N, K, torch.float32, N + K, "noise") * 1e-3
+    if N <= K:
+        x[:, 0] += torch.randn(E, K, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+        x[:, 1] = x[:, 0] + x[:, 1]
+    else:
+        x[:, :, 0] += torch.randn(E, N, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+        x[:, :, 1] = x[:, :, 0] + x[:, :, 1]
+    co = [(3.9, 0.0, 0.0), second]
+    want, scheme = exact(x, co), emulate_wide(x, co, (1024.0, scale))
+    assert bool(scheme.isfinite().all()) and bool((norm(scheme - want) <= 2.0 ** -7 * norm(want)).all())
+    for tile in (0, 64, 128, 256):
+        mxq.testing_set(mxq.TESTING_NS_TILE, tile)
+        try:
+            got = mxq.newton_schulz(x, steps=2, coefficients=co)
+        finally:
+            mxq.testing_set(mxq.TESTING_NS_TILE, 0)
+        assert bool(got.isfinite().all())
+        assert bool((norm(got.double() - want) <= 1.25 * norm(scheme - want) + 2.0 ** -20 * norm(want)).all())
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_singular_value_near_four_of_two_by_two():
+    """ones(2, 2): s = 3.9 after the first step, A = 7.6 everywhere, B off its
+    diagonal 198.6, and a + b s^2 + c s^4 = 400.7 in every element's factor.
+    Roundings, at most half a step of 2^-10 each: of X in A (2 b s^2 + 4 c s^4
+    of 2^-11: 0.99), of A' (198.6 2^-11 in B', 2 c A'^2 2^-11 in beta: 0.21), of
+    B' (0.1) and of X in B' X (0.1): 1.4 of 400.7, 3.5e-3, and bf16's 2^-8:
+    below 2^-7."""
+    g = torch.ones(2, 2, device=DEV)
+    co = [(3.9, 0.0, 0.0), COEF]
+    want = exact(g, co)
+    for tile in (0, 64, 128, 256):
+        mxq.testing_set(mxq.TESTING_NS_TILE, tile)
+        try:
+            got = mxq.newton_schulz(g, steps=2, coefficients=co).double()
+        finally:
+            mxq.testing_set(mxq.TESTING_NS_TILE, 0)
+        assert bool(((got - want).abs() <= 2.0 ** -7 * want.abs()).all()), got
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,N,K", [(2, 96, 224), (2, 100, 257), (2, 300, 260)])
+def test_a_loose_bound_costs_no_accuracy(E, N, K):
+    """Coefficients whose bound on the singular values is far above what these
+    matrices reach: B is stored at a scale 2^-7 of what it could be, which stays
+    below what the scheme costs anyway."""
+    g = matrices(E, N, K, torch.float32, 3, "noise")
+    for co in ([(1.0, 16.0, -16.0), (2.0, -4.0, 16.0), (1.0, 0.5, -2.0)], [(2.0, 16.0, 16.0), (1.5, -1.0, 16.0), (1.5, -0.5, 0.0)]):
+        s = torch.linalg.svdvals(g.double() / norm(g.double())[:, None, None]).max()
+        for a, b, c in co[:-1]:
+            s = max(s, abs(a * s + b * s ** 3 + c * s ** 5))
+        assert s < 4
+        check(mxq.newton_schulz(g, steps=3, coefficients=co), g, co)

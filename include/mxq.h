@@ -535,12 +535,16 @@ int moe_combine_backward(const void *grad_out, int64_t grad_row_stride, const vo
  * in fp16 with fp32 sums on X held in 22 bits; B's scale is chosen per step so
  * that nothing leaves fp16's range while the singular values of X before every
  * step are at most 4 (they start at 1 or less and stay below 1.3 for the usual
- * coefficients; after the last step they may be any) and coefficients within
- * [-16, 16]. A matrix of zeros gives zeros; a NaN or infinity makes its own
- * matrix NaN and no other. rows, cols <= 65536 and a matrix below 2^31 elements,
- * batch <= 65535, steps <= 64. workspace: newton_schulz_workspace_bytes() bytes
- * (NULL when 0; asked for with the device of the call current), 256-byte
- * aligned, not shared by calls that overlap on the GPU.
+ * coefficients; after the last step they may be any). Coefficients lie within
+ * [-16, 16]; a step may have larger ones, up to 256, if no singular value can
+ * leave it above 4: with r = 1 at the start and r <- min(4, max over s in [0, r]
+ * of |a s + b s^3 + c s^5|), and 2^-8 of it for rounding, from step to step, that
+ * maximum is at most 4. A matrix of zeros gives zeros; a NaN or infinity makes
+ * its own matrix NaN and no other. rows, cols <= 65536 and a matrix below 2^31
+ * elements, batch <= 65535, steps <= 64. workspace:
+ * newton_schulz_workspace_bytes() bytes (NULL when 0; asked for with the device
+ * of the call current), 256-byte aligned, not shared by calls that overlap on
+ * the GPU.
  * ------------------------------------------------------------------------ */
 size_t newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, int32_t steps);
 int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int64_t cols, int32_t steps,

@@ -664,8 +664,9 @@ def newton_schulz(g, *, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-
     """Orthogonalise every matrix of g (E, N, K) (or one, (N, K)) bf16 or fp32
     by Newton-Schulz products: X = G / (|G|_F + eps), then steps times A = X
     X^T, X = a X + (b A + c A A) X (on the transpose when N > K).
-    coefficients: one (a, b, c) for all steps or one per step. Returns bf16 of
-    g's shape; out, where given, must not overlap g. Takes the expert weight
+    coefficients: one (a, b, c) for all steps or one per step, within [-16, 16],
+    or larger where no singular value can leave that step above 4 (singular
+    values above 4 before a step are past what it holds). Returns bf16 of g's shape; out, where given, must not overlap g. Takes the expert weight
     gradients (or their momentum) that the weight-gradient GEMMs return."""
     _cuda(g, "g")
     if g.dim() not in (2, 3) or g.dtype not in _DTYPES or not g.is_contiguous():

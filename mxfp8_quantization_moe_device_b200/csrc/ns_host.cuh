@@ -74,28 +74,38 @@ double ns_largest_b(double b, double c, double r)
     return u > 0.0 && u < r * r ? std::max(at(r * r), at(u)) : at(r * r);
 }
 
-// The coefficients with the scale of B' over that of A' in every step. The
-// singular values are bounded by 1 at the start, then by what a step makes of
-// them, and by 4 by the caller's word; 2^-8 more for what rounding adds, and B
-// stays a factor of two from fp16's end.
+// The coefficients with the scale of B' over that of A' in every step, false
+// where the scheme does not carry them. The singular values are bounded by 1 at
+// the start, then by what a step makes of them, and by 4 by the caller's word;
+// 2^-8 more for what rounding adds, and B stays a factor of two from fp16's end.
+// Coefficients of up to 16 leave the scale of B at 4 or more. Larger ones (a
+// schedule's first steps, (8.2, -22.9, 16.5) say) are taken where the bound
+// alone keeps the step's result within 4; at 256 the scale of B would be 1/4.
 constexpr double NS_LARGEST = 4.0;
-ns::Coefs ns_coefs(const float *coefficients, int32_t steps)
+bool ns_coefs(const float *coefficients, int32_t steps, ns::Coefs &co)
 {
-    ns::Coefs co = {};
-    std::memcpy(co.v, coefficients, sizeof(float) * 3 * (size_t)steps);
     double r = 1.0 + 0x1p-8;
     for (int s = 0; s < steps; ++s) {
-        const float a = co.v[3 * s], b = co.v[3 * s + 1], c = co.v[3 * s + 2];
+        const float a = coefficients[3 * s], b = coefficients[3 * s + 1], c = coefficients[3 * s + 2];
+        const float size = std::max(std::fabs(a), std::max(std::fabs(b), std::fabs(c)));
+        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c) || size > 256.0f)
+            return false;
+        const double next = ns_largest_x(a, b, c, r) * (1.0 + 0x1p-8);
+        if (size > 16.0f && next > NS_LARGEST)
+            return false;
         const double most = ns_largest_b(b, c, r) * ns::SA;
         float part = 1.0f;
         while (most * part > 32752.0)
             part *= 0.5f;
+        co.v[3 * s] = a;
+        co.v[3 * s + 1] = b;
+        co.v[3 * s + 2] = c;
         co.pb[s] = b * part;
         co.pc[s] = c * part;
         co.unscale[s] = 1.0f / (ns::SA * part);
-        r = std::min(NS_LARGEST, ns_largest_x(a, b, c, r) * (1.0 + 0x1p-8));
+        r = std::min(NS_LARGEST, next);
     }
-    return co;
+    return true;
 }
 
 // how a product reads or writes a matrix: boxes of width x rows elements, the
@@ -299,13 +309,12 @@ bool ns_is_small(int64_t rows, int64_t cols)
 }
 
 template <typename T>
-int ns_small(const T *g, int64_t E, int64_t rows, int64_t cols, int32_t steps, const float *coefficients, double eps,
+int ns_small(const T *g, int64_t E, int64_t rows, int64_t cols, int32_t steps, const ns::Coefs &co, double eps,
              uint16_t *out, cudaStream_t stream)
 {
     const int rc = ns_small_attributes<T>();
     if (rc != MXQ_OK)
         return rc;
-    const ns::Coefs co = ns_coefs(coefficients, steps);
     const int ctas = (int)((std::max(rows, cols) + ns::SM_SLAB - 1) / ns::SM_SLAB);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -343,10 +352,9 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
         return MXQ_ERR_NULL;
     if (!(eps >= 0.0) || eps > 1e30)
         return MXQ_ERR_UNSUPPORTED;
-    // up to here the scale of B' (ns_coefs) holds singular values of up to 4
-    for (int i = 0; i < 3 * steps; ++i)
-        if (!(coefficients[i] >= -16.0f && coefficients[i] <= 16.0f))
-            return MXQ_ERR_UNSUPPORTED;
+    ns::Coefs co = {};
+    if (!ns_coefs(coefficients, steps, co))
+        return MXQ_ERR_UNSUPPORTED;
     if (batch == 0 || rows == 0 || cols == 0)
         return MXQ_OK;
     if (!g || !out)
@@ -354,9 +362,9 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
     if (!aligned(g, dtype_size(dtype)) || !aligned(out, 2))
         return MXQ_ERR_ALIGN;
     if (ns_is_small(rows, cols))
-        return dtype == MXQ_BF16 ? ns_small(static_cast<const uint16_t *>(g), batch, rows, cols, steps, coefficients, eps,
+        return dtype == MXQ_BF16 ? ns_small(static_cast<const uint16_t *>(g), batch, rows, cols, steps, co, eps,
                                             static_cast<uint16_t *>(out), stream)
-                                 : ns_small(static_cast<const float *>(g), batch, rows, cols, steps, coefficients, eps,
+                                 : ns_small(static_cast<const float *>(g), batch, rows, cols, steps, co, eps,
                                             static_cast<uint16_t *>(out), stream);
     const NsPlan p = ns_plan(batch, rows, cols, steps);
     if (!workspace || workspace_bytes < p.bytes)
@@ -382,7 +390,6 @@ int newton_schulz(const void *g, int32_t dtype, int64_t batch, int64_t rows, int
     a.out = static_cast<uint16_t *>(out);
     a.out_t = p.tall;
     a.out_vec = cols % 8 == 0 && aligned(out, 16);
-    const ns::Coefs co = ns_coefs(coefficients, steps);
     for (int s = 0; s < steps; ++s) {
         a.a = co.v[3 * s];
         a.b = co.v[3 * s + 1];

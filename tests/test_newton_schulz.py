@@ -399,3 +399,55 @@ def test_a_loose_bound_costs_no_accuracy(E, N, K):
             s = max(s, abs(a * s + b * s ** 3 + c * s ** 5))
         assert s < 4
         check(mxq.newton_schulz(g, steps=3, coefficients=co), g, co)
+
+
+# ------------------------------------------------------------ schedules with large first steps
+# a schedule of five steps that takes every singular value from 1e-3 to 1 near
+# one, scaled so that none passes 2 (1.02 per power)
+SCHEDULE = [(a / 1.02, b / 1.02 ** 3, c / 1.02 ** 5) for a, b, c in
+            ((8.287, -23.596, 17.3), (4.107, -2.948, 0.545), (3.949, -2.909, 0.552), (3.318, -2.488, 0.51),
+             (2.301, -1.669, 0.419))]
+
+
+def test_larger_coefficients_where_the_bound_holds():
+    L = mxq.lib()
+
+    def status(*co):
+        flat = [v for c in co for v in c]
+        return L.newton_schulz(None, 0, 3, 0, 8, len(co), (ctypes.c_float * len(flat))(*flat), 1e-7, None, None, 0, None)
+
+    assert status(*SCHEDULE) == mxq.OK
+    assert status((8.3, -23.6, 17.3)) == mxq.OK          # 2.0 at s = 1, 2.1 at 1 + 2^-8
+    assert status((20.0, 0.0, 0.0)) == mxq.ERR_UNSUPPORTED
+    assert status((3.0, -17.0, 2.0)) == mxq.ERR_UNSUPPORTED   # -12 at s = 1
+    assert status((2.0, -20.0, 21.0)) == mxq.OK          # 3 at s = 1
+    assert status((2.0, -20.0, 21.98)) == mxq.ERR_UNSUPPORTED  # 3.98 there, 4.3 at 1 + 2^-8
+    # the bound is carried on: the same step behind one that may reach 4
+    assert status((4.0, 0.0, 0.0), (2.0, -20.0, 21.0)) == mxq.ERR_UNSUPPORTED
+    assert status((0.9, 0.0, 0.0), (2.0, -20.0, 21.0)) == mxq.OK
+    # inner maximum alone: 27 s - 27 s^3 is 10.4 at s^2 = 1/3, 0 at 1
+    assert status((27.0, -27.0, 0.0)) == mxq.ERR_UNSUPPORTED
+    assert status((10.0, -18.0, 8.0)) == mxq.OK          # 3 at s = 0.5, 0 at 1
+    assert status((-8.3, 23.6, -17.3)) == mxq.OK
+    assert status((1.0, -256.5, 256.5)) == mxq.ERR_UNSUPPORTED
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for i in range(3):
+            assert status(tuple(bad if j == i else 1.0 for j in range(3))) == mxq.ERR_UNSUPPORTED
+    # up to 16 the caller's word counts
+    assert status(*[(16.0, -16.0, 16.0)] * 5) == mxq.OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,N,K", [(2, 96, 224), (2, 257, 100), (2, 300, 260), (1, 256, 512)])
+@pytest.mark.parametrize("kind", ["gradient", "noise", "decay"])
+def test_schedule(E, N, K, kind):
+    g = matrices(E, N, K, torch.float32, 7, kind)
+    want, scheme = exact(g, SCHEDULE), emulate(g, SCHEDULE)
+    for tile in (0, 64, 128, 256):
+        mxq.testing_set(mxq.TESTING_NS_TILE, tile)
+        try:
+            got = mxq.newton_schulz(g, coefficients=SCHEDULE).double()
+        finally:
+            mxq.testing_set(mxq.TESTING_NS_TILE, 0)
+        assert bool((norm(got - want) <= 1.25 * norm(scheme - want) + 2.0 ** -20 * norm(want)).all())
+    assert mxq.device_status() == 0

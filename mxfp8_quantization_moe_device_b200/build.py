@@ -18,6 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmxq.so")
 TORCH_SRC = os.path.join(HERE, "csrc_torch", "moe_ops.cpp")
 TORCH_OPS = os.path.join(HERE, "_torch_ops.so")
+TORCH_OPS_KEY = TORCH_OPS + ".key"  # the torch and Python that it was built against
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -34,9 +35,25 @@ def _up_to_date(out, srcs):
     return os.path.exists(out) and all(os.path.getmtime(out) >= os.path.getmtime(s) for s in srcs)
 
 
+def _torch_key():
+    """What a module compiled against torch's C++ classes is bound to."""
+    import torch
+    return "\n".join((torch.__version__, torch.version.git_version, str(torch._C._GLIBCXX_USE_CXX11_ABI),
+                      sysconfig.get_config_var("SOABI")))
+
+
+def _built_key():
+    try:
+        with open(TORCH_OPS_KEY) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def build_torch_ops(force=False, verbose=False):
     """_torch_ops.so: host code only, against torch's headers and libmxq.so."""
-    if not force and _up_to_date(TORCH_OPS, [TORCH_SRC, os.path.join(INCLUDE, "mxq.h")]):
+    if (not force and _built_key() == _torch_key()
+            and _up_to_date(TORCH_OPS, [TORCH_SRC, os.path.join(INCLUDE, "mxq.h")])):
         return TORCH_OPS
     import torch
     root = os.path.dirname(torch.__file__)
@@ -51,6 +68,8 @@ def build_torch_ops(force=False, verbose=False):
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
     os.replace(TORCH_OPS + ".tmp", TORCH_OPS)
+    with open(TORCH_OPS_KEY, "w") as f:
+        f.write(_torch_key())
     return TORCH_OPS
 
 

@@ -215,6 +215,41 @@ def test_overlap_of_an_output_with_strided_rows():
     assert overlaps(buf[5:7], words[3:4]) and not overlaps(buf[4:6], words[3:4])
 
 
+def test_torch_module_is_rebuilt_for_another_torch(tmp_path, monkeypatch):
+    from mxfp8_quantization_moe_device_b200 import build
+    so = tmp_path / "_torch_ops.so"
+    monkeypatch.setattr(build, "TORCH_OPS", str(so))
+    monkeypatch.setattr(build, "TORCH_OPS_KEY", str(so) + ".key")
+    runs = []
+
+    def compiler(cmd, check):
+        runs.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w"):
+            pass
+
+    monkeypatch.setattr(build.subprocess, "run", compiler)
+    for _ in range(2):
+        assert build.build_torch_ops() == str(so)
+    assert len(runs) == 1 and so.exists()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "9.9.9")
+        for _ in range(2):
+            build.build_torch_ops()
+        assert len(runs) == 2
+    build.build_torch_ops()  # and back
+    assert len(runs) == 3
+    with monkeypatch.context() as m:
+        m.setattr(build.sysconfig, "get_config_var", lambda name: "cpython-399")
+        build.build_torch_ops()
+        assert len(runs) == 4
+    build.build_torch_ops()
+    (tmp_path / "_torch_ops.so.key").unlink()  # built before there was a key
+    build.build_torch_ops()
+    assert len(runs) == 6
+    build.build_torch_ops(force=True)
+    assert len(runs) == 7
+
+
 @pytest.mark.gpu
 def test_registered_ops():
     import mxfp8_quantization_moe_device_b200.ops  # noqa: F401

@@ -579,15 +579,17 @@ _ops = None
 
 
 def torch_ops():
-    """Load _torch_ops.so once. Raises if it has not been built."""
+    """Load _torch_ops.so once. Raises if it has not been built, or for another
+    torch than this one."""
     global _ops
     if _ops is None:
         lib()
         try:
             from . import _torch_ops as ops
         except ImportError as e:
-            raise RuntimeError("_torch_ops.so is not built; build it with "
-                               "`python -m mxfp8_quantization_moe_device_b200.build`") from e
+            there = os.path.exists(os.path.join(_HERE, "_torch_ops.so"))
+            raise RuntimeError(f"_torch_ops.so {f'cannot be loaded ({e})' if there else 'is not built'}; build it "
+                               f"{'anew ' if there else ''}with `python -m mxfp8_quantization_moe_device_b200.build`") from e
         _ops = ops
     return _ops
 

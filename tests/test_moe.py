@@ -250,6 +250,24 @@ def test_torch_module_is_rebuilt_for_another_torch(tmp_path, monkeypatch):
     assert len(runs) == 7
 
 
+@pytest.mark.parametrize("there", [True, False])
+def test_what_is_wrong_with_the_torch_module_is_said(there, tmp_path, monkeypatch):
+    import sys
+    import mxfp8_quantization_moe_device_b200 as package
+    mxq.torch_ops()
+    name = package.__name__ + "._torch_ops"
+    monkeypatch.setattr(mxq, "_ops", None)
+    monkeypatch.delattr(package, "_torch_ops")
+    monkeypatch.setitem(sys.modules, name, None)  # an import that fails, with a text of its own
+    if not there:
+        monkeypatch.setattr(mxq, "_HERE", str(tmp_path))
+    with pytest.raises(RuntimeError) as e:
+        mxq.torch_ops()
+    assert isinstance(e.value.__cause__, ImportError)
+    assert ("is not built" in str(e.value)) == (not there) and (str(e.value.__cause__) in str(e.value)) == there
+    assert "mxfp8_quantization_moe_device_b200.build" in str(e.value)
+
+
 @pytest.mark.gpu
 def test_registered_ops():
     import mxfp8_quantization_moe_device_b200.ops  # noqa: F401

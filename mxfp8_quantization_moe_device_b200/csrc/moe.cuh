@@ -158,19 +158,21 @@ constexpr float LOG2E = 1.4426950408889634f;
 
 // exp(v - m) as 2^(v log2(e) - c) with c = m log2(e): one instruction to the
 // exponent, and c's own rounding is a factor of all of a token's values, which
-// cancels. Where |m| is so large (2^20) that this factor is no small one, all
-// tokens of the warp take 2^((v - m) log2(e)).
+// cancels. Where |m| is so large (2^20) that this factor is no small one, the
+// token takes 2^((v - m) log2(e)); the other tokens of its warp keep theirs, so
+// that a token's results are the same bits beside any others.
 struct Shift {
-    float m, c;
-    bool far; // the same in every lane of the warp
+    float m, c; // one of them is zero
+    bool far;   // a token of the warp is far (the same in every lane)
 
     MXQ_DEV explicit Shift(float largest)
     {
-        m = largest == -INFINITY ? 0.0f : largest;
-        c = m * LOG2E;
-        far = __any_sync(0xffffffffu, fabsf(m) > 0x1p20f);
+        const bool mine = fabsf(largest) > 0x1p20f && largest != -INFINITY;
+        m = mine ? largest : 0.0f;
+        c = mine || largest == -INFINITY ? 0.0f : largest * LOG2E;
+        far = __any_sync(0xffffffffu, mine);
     }
-    MXQ_DEV float exp(float v) const { return exp2_fast(far ? (v - m) * LOG2E : fmaf(v, LOG2E, -c)); }
+    MXQ_DEV float exp(float v) const { return exp2_fast(fmaf(v - m, LOG2E, -c)); }
 };
 
 // a token's logits in its lanes become exp(v - m), rz the reciprocal of their
@@ -182,8 +184,8 @@ template <int LPT, int EPL> MXQ_DEV bool exponentials(float (&v)[EPL], const Shi
     if (shift.far) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            v[i] = exp2_fast((v[i] - shift.m) * LOG2E);
-    } else {
+            v[i] = shift.exp(v[i]);
+    } else { // m is zero
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
             v[i] = exp2_fast(fmaf(v[i], LOG2E, -shift.c));

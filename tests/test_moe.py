@@ -1016,3 +1016,35 @@ def test_captured_backward_into_a_living_graph_is_refused():
     torch.cuda.synchronize()
     assert torch.equal(d, torch.autograd.grad(autograd.moe_route(base + bias, k)[0], bias, dl)[0])
     assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,k", [(4, 2), (20, 3), (60, 8), (300, 4)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_token_beside_any_others(E, k, dtype):
+    """Weights, choices and gradients of a token are the same bits whatever
+    tokens stand beside it: far from zero, infinite, NaN, padded, or none."""
+    T = 150
+    l = logits_of(T, E, dtype, E)
+    odd = torch.zeros(T, dtype=torch.bool)
+    odd[::7] = True
+    valid = torch.ones(T, dtype=torch.bool)
+    valid[::21] = False
+    gw = torch.randn(T, k, generator=torch.Generator().manual_seed(2))
+    far = l.clone()
+    rows = far[odd]
+    for i in range(rows.shape[0]):
+        rows[i] = (rows[i] + 2e6, rows[i] - 1e30, rows[i] * math.inf, rows[i] * math.nan, rows[i] * 1e9, rows[i] - math.inf)[i % 6]
+    far[odd] = rows
+
+    def run(l, valid, gw, renorm):
+        x = l.to(DEV).requires_grad_(True)
+        w, ids, _, _ = autograd.moe_route(x, k, valid=valid.to(DEV), renormalize=renorm)
+        return w.detach(), ids, torch.autograd.grad(w, x, gw.to(DEV))[0]
+
+    for renorm in (False, True):
+        want = run(l[~odd], valid[~odd], gw[~odd], renorm)
+        for got in (run(l, valid, gw, renorm), run(far, valid, gw, renorm)):
+            for a, b in zip(got, want):
+                assert torch.equal(a[~odd], b)
+    assert mxq.device_status() == 0

@@ -471,9 +471,12 @@ typedef enum mxq_dtype {
  * -1, weights 0, no part in counts and loss. An expert with logit -inf is
  * never chosen; where fewer than top_k experts are left the slots' ids are -1
  * and their weights 0. A row with a NaN or +inf chooses nothing, its weights
- * are NaN, and so is the loss. experts <= 1024, top_k <= 32. workspace:
- * moe_route_workspace_bytes() bytes (asked for with the device of the call
- * current), 256-byte aligned, not shared by calls that overlap on the GPU. */
+ * are NaN, and so is the loss. The order by expert drops such a token, and
+ * moe_combine gives it zeros, not NaN, as it does for every token without
+ * rows: it shows in the weights, the loss and the gradient of the logits alone.
+ * experts <= 1024, top_k <= 32. workspace: moe_route_workspace_bytes() bytes
+ * (asked for with the device of the call current), 256-byte aligned, not shared
+ * by calls that overlap on the GPU. */
 size_t moe_route_workspace_bytes(int64_t tokens, int64_t experts);
 int moe_route(const void *logits, int32_t dtype, int64_t tokens, int64_t experts, int64_t row_stride,
               const uint8_t *valid, int32_t top_k, int32_t renormalize, float *weights, int32_t *ids,
@@ -509,10 +512,11 @@ int moe_dispatch(const void *x, int32_t dtype, int64_t tokens, int64_t cols, int
                  cudaStream_t stream);
 
 /* out[t] = sum_j weights[t][j] * y[pos[t][j]] over the slots with pos >= 0
- * (weights NULL: ones), slots in order, fp32, rounded once. y (rows, cols)
- * with row_stride, out (tokens, cols) row-major. Also the gradient of
- * moe_dispatch by x, with weights NULL. A pos >= rows is skipped and recorded
- * as MXQ_ERR_BAD_INDEX. */
+ * (weights NULL: ones), slots in order, fp32, rounded once; zeros where a token
+ * has no such slot. The weight of a dropped slot is not looked at, whatever it
+ * is, NaN too. y (rows, cols) with row_stride, out (tokens, cols) row-major.
+ * Also the gradient of moe_dispatch by x, with weights NULL. A pos >= rows is
+ * skipped and recorded as MXQ_ERR_BAD_INDEX. */
 int moe_combine(const void *y, int32_t dtype, int64_t rows, int64_t cols, int64_t row_stride, const int32_t *pos,
                 const float *weights, int64_t tokens, int32_t top_k, void *out, cudaStream_t stream);
 

@@ -201,7 +201,9 @@ def moe_route(logits, top_k, *, valid=None, renormalize=False):
     """(weights (T, top_k) fp32, ids (T, top_k) int32, counts (E,) int32, loss
     () fp32) of router logits (T, E) bf16 or fp32; weights and loss are
     differentiable in the logits (the counts inside the loss are constants).
-    See binding.moe_route."""
+    A token whose logits hold a NaN or +inf shows in the weights, the loss and
+    the logits' gradient; dispatch drops it and moe_combine gives it zeros. See
+    binding.moe_route."""
     return mxq.torch_ops().grad_route(logits, top_k, valid, renormalize)
 
 

@@ -602,7 +602,8 @@ def moe_route(logits, top_k, *, valid=None, renormalize=False, weights=None, ids
     (weights (T, top_k) fp32, ids (T, top_k) int32, counts (E,) int32, loss ()
     fp32); a slot without an expert (padding, experts at -inf) has id -1 and
     weight 0; a row with a NaN or +inf has ids -1 and NaN weights, and makes
-    the loss NaN. loss_grad: optional (E,) fp32 buffer that receives d loss /
+    the loss NaN (moe_combine, which takes no notice of a dropped slot's weight,
+    gives its token zeros). loss_grad: optional (E,) fp32 buffer that receives d loss /
     d p[t][e], for moe_route_backward."""
     return torch_ops().moe_route(logits, top_k, valid, renormalize, weights, ids, counts, loss, loss_grad)
 
@@ -641,7 +642,8 @@ def moe_dispatch(x, pos, offs, *, out=None):
 
 def moe_combine(y, pos, weights=None, *, out=None):
     """The way back: out[t] = sum_j weights[t][j] * y[pos[t][j]] over the slots
-    with pos >= 0, in fp32, rounded once. y (M, K) bf16 or fp32 with
+    with pos >= 0, in fp32, rounded once; the weights of other slots may be
+    anything, and a token without a row gets zeros. y (M, K) bf16 or fp32 with
     contiguous rows, weights (T, top_k) fp32 or None (ones). Returns out
     (T, K); rows of y that no slot names are not read."""
     return torch_ops().moe_combine(y, pos, weights, out)

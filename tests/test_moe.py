@@ -1048,3 +1048,37 @@ def test_a_token_beside_any_others(E, k, dtype):
             for a, b in zip(got, want):
                 assert torch.equal(a[~odd], b)
     assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("renorm", [False, True])
+def test_a_bad_token_through_the_layer(renorm):
+    """A token with a NaN or +inf among its logits: NaN weights, loss and logit
+    gradients, zeros out of the layer, no trace in the other tokens."""
+    T, E, k, K = 50, 8, 2, 96
+    l = torch.randn(T, E, device=DEV)
+    x = torch.randn(T, K, device=DEV)
+    bad = torch.zeros(T, dtype=torch.bool, device=DEV)
+    bad[[0, 17, 49]] = True
+    l[0, 3], l[17, 0], l[49, 7] = math.nan, math.inf, math.nan
+    dout = torch.randn(T, K, device=DEV)
+
+    def layer(l, x, d):
+        l, x = l.clone().requires_grad_(True), x.clone().requires_grad_(True)
+        w, ids, counts, loss = autograd.moe_route(l, k, renormalize=renorm)
+        xs, pos, offs = autograd.moe_dispatch(x, ids, E)
+        out = autograd.moe_combine(2 * xs, pos, w, offs)
+        return w, ids, counts, loss, out, *torch.autograd.grad(out, (l, x), d)
+
+    w, ids, counts, loss, out, dl, dx = layer(l, x, dout)
+    assert bool((ids[bad] == -1).all()) and bool(w[bad].isnan().all()) and bool(loss.isnan())
+    assert bool((out[bad] == 0).all()) and bool((dx[bad] == 0).all()) and bool(dl[bad].isnan().all())
+    alone = layer(l[~bad], x[~bad], dout[~bad])
+    assert torch.equal(counts, alone[2]) and torch.equal(ids[~bad], alone[1])
+    for got, want in zip((w, out, dl, dx), (alone[0], *alone[4:])):
+        assert torch.equal(got[~bad], want)
+    # weights of dropped slots count for nothing
+    xs, pos, offs = autograd.moe_dispatch(x, ids, E)
+    ww = torch.where(pos < 0, torch.full_like(w, math.inf), w)
+    assert torch.equal(mxq.moe_combine(2 * xs, pos, ww), out) and torch.equal(mxq.moe_combine(2 * xs, pos, w), out)
+    assert mxq.device_status() == 0

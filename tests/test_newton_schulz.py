@@ -451,3 +451,88 @@ def test_schedule(E, N, K, kind):
             mxq.testing_set(mxq.TESTING_NS_TILE, 0)
         assert bool((norm(got - want) <= 1.25 * norm(scheme - want) + 2.0 ** -20 * norm(want)).all())
     assert mxq.device_status() == 0
+
+
+# ------------------------------------------------------------ the one-launch path alone
+SMALL = [(2, 96, 224), (2, 224, 96), (2, 100, 257), (2, 1030, 37)]  # one CTA a matrix, then clusters
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,N,K", SMALL)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_small_steps_coefficients_and_scale(E, N, K, dtype):
+    assert mxq.lib().newton_schulz_workspace_bytes(E, N, K, 5) == 0
+    g = matrices(E, N, K, dtype, 9)
+    for steps in (1, 2, 7):
+        check(mxq.newton_schulz(g, steps=steps), g, [COEF] * steps)
+    co = [(4.0, -8.0, 5.0), (3.5, -5.0, 2.2), (1.875, -1.25, 0.375)]
+    check(mxq.newton_schulz(g, steps=3, coefficients=co), g, co)
+    check(mxq.newton_schulz(g, steps=3, coefficients=co[::-1]), g, co[::-1])
+    for s in (1e-18, 1e-25, 1e25):
+        check(mxq.newton_schulz(g * s, eps=0.0), g * s, [COEF] * 5, eps=0.0)
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,K", [(96, 224), (224, 96), (100, 257), (1030, 37)])
+def test_small_zeros_nan_and_neighbours(N, K):
+    g = matrices(5, N, K, torch.float32, 4)
+    want = mxq.newton_schulz(g)
+    g[1] = 0.0
+    g[2, 3, 4] = float("nan")
+    g[3, N - 1, K - 1] = float("inf")
+    got = mxq.newton_schulz(g)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[4], want[4])
+    assert bool((got[1] == 0).all()) and bool(got[2].isnan().all()) and bool(got[3].isnan().all())
+    assert bool((mxq.newton_schulz(g[1:2], eps=0.0) == 0).all())
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,K", [(17, 30), (33, 65), (1, 9), (100, 250), (97, 301), (50, 1290), (1000, 75), (3, 4000)])
+def test_small_behind_nans(N, K):
+    """What a matrix finds on its SMs, rows and columns behind its own in shared
+    and tensor memory, it does not read: NaN matrices on every SM come first."""
+    g = matrices(3, N, K, torch.float32, 2)
+    want = mxq.newton_schulz(g)
+    if min(N, K) >= 16:  # of fewer rows, single roundings would decide
+        check(want, g, [COEF] * 5)
+    for shape in ((600, 128, 256), (64, 128, 2048)):
+        poison = torch.full(shape, float("nan"), device=DEV)
+        got = []
+        for _ in range(3):
+            assert bool(mxq.newton_schulz(poison, steps=1).isnan().all())
+            got.append(mxq.newton_schulz(g))
+        assert all(torch.equal(x, want) for x in got)
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,N,K", [(40, 96, 224), (30, 100, 257), (20, 90, 4000)])
+def test_small_streams_graphs_and_calls_at_once(E, N, K):
+    g, h = matrices(E, N, K, torch.bfloat16, 8), matrices(3, 400, 700, torch.bfloat16, 8)
+    want, other = mxq.newton_schulz(g), mxq.newton_schulz(h)
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(4):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            outs.append((mxq.newton_schulz(g), mxq.newton_schulz(h), mxq.newton_schulz(g)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, want) and torch.equal(b, other) and torch.equal(c, want) for a, b, c in outs)
+    graphs = []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            graphs.append((gr, mxq.newton_schulz(g)))
+    g.copy_(matrices(E, N, K, torch.bfloat16, 18))
+    torch.cuda.synchronize()
+    for gr, _ in graphs:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            gr.replay()
+    torch.cuda.synchronize()
+    want = mxq.newton_schulz(g)
+    assert all(torch.equal(o, want) for _, o in graphs)
+    check(want, g, [COEF] * 5)
+    assert mxq.device_status() == 0

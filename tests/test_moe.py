@@ -1082,3 +1082,35 @@ def test_a_bad_token_through_the_layer(renorm):
     ww = torch.where(pos < 0, torch.full_like(w, math.inf), w)
     assert torch.equal(mxq.moe_combine(2 * xs, pos, ww), out) and torch.equal(mxq.moe_combine(2 * xs, pos, w), out)
     assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", [(2000000, 8, 2), (40000003, 4, 1), (1500001, 64, 3), (6000000, 256, 8), (1000000, 1000, 2)])
+@pytest.mark.parametrize("alike", [False, True])
+def test_loss_of_many_tokens(T, E, k, alike):
+    """Sums of p over the tokens: a lane adds its tokens in fp32 (n of them, all
+    terms positive, so n 2^-24 of the sum at most, and 16 more for the lanes and
+    warps of a CTA), the CTAs are added in fp64; p is good to 2^-18. n is the
+    tokens over 2 CTAs per SM, 16 warps each, 32 / lanes tokens at a time.
+    `alike`: the same token throughout, whose roundings all go one way."""
+    lanes = 1
+    while lanes < 32 and lanes * 8 < E:
+        lanes *= 2
+    g = torch.Generator(device=DEV).manual_seed(E)
+    if alike:
+        l = (torch.randn(1, E, generator=g, device=DEV) * 2).bfloat16().expand(T, E).contiguous()
+    else:
+        l = torch.randn(T, E, generator=g, device=DEV, dtype=torch.bfloat16)
+    w, ids, counts, loss = mxq.moe_route(l, k)
+    assert int(counts.sum()) == T * k
+    total = torch.zeros(E, dtype=torch.float64, device=DEV)
+    seen = torch.zeros(E, dtype=torch.int64, device=DEV)
+    for a, i in zip(l.split(1 << 18), ids.split(1 << 18)):
+        total += torch.softmax(a.double(), 1).sum(0)
+        seen += torch.bincount(i.reshape(-1), minlength=E)
+    assert torch.equal(counts.long(), seen)
+    want = E * float((seen.double() * total).sum()) / (k * float(T) ** 2)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n = math.ceil(T / (2 * sms * 16 * (32 // lanes)))
+    assert abs(float(loss) - want) <= ((n + 17) * 2.0 ** -24 + 2.0 ** -18) * want
+    assert mxq.device_status() == 0

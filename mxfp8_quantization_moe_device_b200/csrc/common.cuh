@@ -200,7 +200,9 @@ MXQ_DEV void red_release_gpu_add(int *p, int v)
 
 // ---------------------------------------------------------------- programmatic launches
 // A kernel launched so starts while the one before it in the stream finishes,
-// and waits here for its results before it touches global memory.
+// and waits here for its results before it touches global memory. Those results
+// are not read-only for as long as it runs: no __restrict__ on a pointer to
+// them, which would allow loads ahead of the wait.
 MXQ_DEV void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 MXQ_DEV void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 

@@ -740,9 +740,9 @@ __global__ void __launch_bounds__(moe::PLAN_THREADS)
 
 // hist (C, E) of pass 1, or NULL when the grid is one CTA over one tile, or
 // few enough that each counts the entries before and behind its own (a launch
-// less)
+// less). No __restrict__ on hist: it is written while this kernel already runs.
 __global__ void __launch_bounds__(moe::PLAN_THREADS)
-    k_moe_plan_rank(const int32_t *__restrict__ ids, int64_t n, int E, int64_t chunk, const int *__restrict__ hist,
+    k_moe_plan_rank(const int32_t *__restrict__ ids, int64_t n, int E, int64_t chunk, const int *hist,
                     int C, int32_t *__restrict__ pos, int32_t *__restrict__ offs)
 {
     using namespace moe;

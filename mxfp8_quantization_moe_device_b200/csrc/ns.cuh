@@ -351,10 +351,11 @@ MXQ_DEV void scale_factors(double norm, float &f0, float &f1)
 // tile as it is read, or its transpose, goes to X, and both halves to the
 // epilogue's chunks. A thread moves pairs of neighbours. 380 us at (16, 2048,
 // 7168) bf16, 1.9 GB (288 at the copy rate): loads, then stores, so residency
-// counts, and eight CTAs per SM took 495 us where six took 585 (with X^T).
+// counts, and eight CTAs per SM took 495 us where six took 585 (with X^T). No
+// __restrict__ on part: it is written while this kernel already runs.
 template <typename T>
 __global__ void __launch_bounds__(256, 8)
-    k_ns_init(const T *__restrict__ g, int rows, int cols, int pair, const double *__restrict__ part, int parts,
+    k_ns_init(const T *__restrict__ g, int rows, int cols, int pair, const double *part, int parts,
               double eps, int tall, uint16_t *__restrict__ xh, int ldx, uint16_t *__restrict__ hi,
               uint16_t *__restrict__ lo)
 {

@@ -1114,3 +1114,33 @@ def test_loss_of_many_tokens(T, E, k, alike):
     n = math.ceil(T / (2 * sms * 16 * (32 // lanes)))
     assert abs(float(loss) - want) <= ((n + 17) * 2.0 ** -24 + 2.0 ** -18) * want
     assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", [(4097, 8, 4), (20000, 1000, 3), (40000, 37, 8)])
+def test_orders_back_to_back(T, E, k):
+    """The ranking kernel starts while the counting one still runs, and its
+    workspace is the one of the call before: counts of another call's ids must
+    not show."""
+    L = mxq.lib()
+    n = T * k
+    batches = [torch.randint(-1, e, (T, k), device=DEV, dtype=torch.int32) for e in (E, 1, E // 2 + 1, 3, E, 2)]
+    want = [mxq.moe_dispatch_plan(b, E) for b in batches]
+    for b, (pos, offs) in zip(batches, want):
+        key = torch.where(b < 0, E, b).reshape(-1).long()
+        assert torch.equal(offs.long(), torch.cumsum(torch.bincount(key, minlength=E + 1)[:E], 0))
+        order = torch.sort(key, stable=True).indices[:int(offs[-1])]
+        assert torch.equal(pos.reshape(-1)[order].long(), torch.arange(order.numel(), device=DEV))
+    nbytes = L.moe_dispatch_plan_workspace_bytes(n, E)
+    assert nbytes > 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=DEV)
+    reps = 20
+    pos = torch.empty(reps * len(batches), T, k, dtype=torch.int32, device=DEV)
+    offs = torch.empty(reps * len(batches), E, dtype=torch.int32, device=DEV)
+    stream = torch.cuda.current_stream().cuda_stream
+    for i in range(reps * len(batches)):
+        assert L.moe_dispatch_plan(batches[i % len(batches)].data_ptr(), n, E, pos[i].data_ptr(), offs[i].data_ptr(),
+                                   ws.data_ptr(), nbytes, stream) == mxq.OK
+    for i in range(reps * len(batches)):
+        assert torch.equal(pos[i], want[i % len(batches)][0]) and torch.equal(offs[i], want[i % len(batches)][1])
+    assert mxq.device_status() == 0

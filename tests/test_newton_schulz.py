@@ -536,3 +536,29 @@ def test_small_streams_graphs_and_calls_at_once(E, N, K):
     assert all(torch.equal(o, want) for _, o in graphs)
     check(want, g, [COEF] * 5)
     assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,N,K", [(3, 140, 150), (1, 700, 1100)])
+def test_calls_back_to_back(E, N, K):
+    """The kernel that scales G starts while the one that sums its squares still
+    runs, and their workspace is the one of the call before: the norm of another
+    call's matrices must not show."""
+    L = mxq.lib()
+    base = matrices(E, N, K, torch.float32, 5)
+    batches = [base * s for s in (1.0, 1e6, 1e-6, 3.0)]
+    want = [mxq.newton_schulz(b) for b in batches]
+    for b, w in zip(batches, want):
+        check(w, b, [COEF] * 5)
+    nbytes = L.newton_schulz_workspace_bytes(E, N, K, 1)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=DEV)
+    want = [mxq.newton_schulz(b, steps=1) for b in batches]
+    outs = torch.empty(60, E, N, K, dtype=torch.bfloat16, device=DEV)
+    co = (ctypes.c_float * 3)(*COEF)
+    stream = torch.cuda.current_stream().cuda_stream
+    for i in range(60):
+        assert L.newton_schulz(batches[i % 4].data_ptr(), 1, E, N, K, 1, co, 1e-7, outs[i].data_ptr(), ws.data_ptr(),
+                               nbytes, stream) == mxq.OK
+    for i in range(60):
+        assert torch.equal(outs[i], want[i % 4])
+    assert mxq.device_status() == 0

@@ -1144,3 +1144,66 @@ def test_orders_back_to_back(T, E, k):
     for i in range(reps * len(batches)):
         assert torch.equal(pos[i], want[i % len(batches)][0]) and torch.equal(offs[i], want[i % len(batches)][1])
     assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_the_largest_order():
+    """2^31 - 1 entries, the most that int32 places and ends can hold: against
+    running counts, a part of the entries at a time."""
+    n, E = 2 ** 31 - 1, 5
+    ids = torch.empty(n, 1, dtype=torch.int32, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    for part in ids.split(1 << 27):
+        part.copy_(torch.randint(-1, E, part.shape, generator=g, device=DEV, dtype=torch.int32))
+    pos, offs = mxq.moe_dispatch_plan(ids, E)
+    counts = torch.zeros(E, dtype=torch.int64, device=DEV)
+    for part in ids.split(1 << 27):
+        counts += torch.stack([(part == e).sum() for e in range(E)])
+    ends = torch.cumsum(counts, 0)
+    assert torch.equal(offs.long(), ends)
+    first = (ends - counts).tolist()
+    for part, got in zip(ids.split(1 << 26), pos.split(1 << 26)):
+        assert bool((got[part < 0] == -1).all())
+        for e in range(E):
+            mine = got[part == e]
+            assert torch.equal(mine.long(), torch.arange(first[e], first[e] + mine.numel(), device=DEV))
+            first[e] += mine.numel()
+    assert first == ends.tolist()
+    assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_the_most_tokens():
+    """Tokens up to the limit of 2^31 - 1 slots through every call, in rows of
+    one or two elements."""
+    T, E, k = 2 ** 30 - 11, 2, 2  # 2^31 - 22 slots, 2^31 - 16 rows
+    l = torch.empty(T, E, dtype=torch.bfloat16, device=DEV)
+    bits = torch.arange(T, device=DEV, dtype=torch.int32)
+    l[:, 0] = (bits & 1).bfloat16()
+    l[:, 1] = (bits & 2).bfloat16()
+    w, ids, counts, loss = mxq.moe_route(l, k)
+    assert counts.tolist() == [T, T]
+    four = mxq.moe_route(l[:4], k)
+    tail = slice(T - T % 4 - 4, T - T % 4)
+    for got, want in ((w, four[0]), (ids, four[1])):
+        assert torch.equal(got[tail], want) and torch.equal(got[:4], want)
+    p = torch.softmax(l[:4].double(), 1).mean(0)
+    assert abs(float(loss) - float(p.sum())) <= 2.0 ** -9
+    del l, w
+    pos, offs = mxq.moe_dispatch_plan(ids, E)
+    assert offs.tolist() == [T, 2 * T]
+    assert torch.equal(pos[-4:].sort(1).values.long(), torch.arange(T - 4, T, device=DEV)[:, None] + torch.tensor([0, T], device=DEV))
+    del ids
+    x = (bits % 256)[:, None].bfloat16()
+    xs = mxq.moe_dispatch(x, pos, offs)
+    assert xs.shape[0] == 2 * T + 6 and bool((xs[2 * T:] == 0).all())
+    for half in (xs[:T], xs[T:2 * T]):
+        assert torch.equal(half, x)
+    with pytest.raises(mxq.MXQError):  # 2^31 - 10 slots would make 2^31 rows
+        mxq.moe_dispatch(torch.zeros(2 ** 30 - 5, 1, device=DEV), torch.zeros(2 ** 30 - 5, 2, dtype=torch.int32, device=DEV), offs)
+    out = mxq.moe_combine(xs, pos)
+    assert torch.equal(out, 2 * x)
+    ww = torch.full((T, k), 0.5, device=DEV)
+    dy, dw = mxq.moe_combine_backward(x, xs, pos, ww, offs)
+    assert torch.equal(dy, 0.5 * xs) and torch.equal(dw[:, 0], x[:, 0].float().square()) and torch.equal(dw[:, 1], dw[:, 0])
+    assert mxq.device_status() == 0

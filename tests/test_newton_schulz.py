@@ -562,3 +562,34 @@ def test_calls_back_to_back(E, N, K):
     for i in range(60):
         assert torch.equal(outs[i], want[i % 4])
     assert mxq.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,K", [(65536, 32760), (32760, 65536), (65536, 1000), (65536, 9)])
+def test_the_largest_matrices(N, K):
+    """Sides of 65536 and just below 2^31 elements, one step, 2 + 66 rows of X^T
+    against 64 bits: a X + (b A + c A A) X with A summed in parts. The scheme's
+    error stays below 1e-3 of the norm and the result's rounding is 1.7e-3."""
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    g = torch.randn(N, K, generator=gen, device=DEV, dtype=torch.bfloat16)
+    out = mxq.newton_schulz(g, steps=1)
+    gt, ot = (g, out) if N >= K else (g.t(), out.t())  # X^T and its update
+    n, m = gt.shape
+    A = torch.zeros(m, m, dtype=torch.float64, device=DEV)
+    for part in gt.split(4096):
+        p = part.double()
+        A += p.t() @ p
+    f = 1.0 / (A.diagonal().sum().sqrt() + 1e-7)
+    A *= f * f
+    rows = torch.cat([torch.tensor([0, n - 1]), torch.randint(0, n, (64,), generator=torch.Generator().manual_seed(2)),
+                      torch.tensor([n // 2, n - 2])]).to(DEV)
+    X = gt[rows].double() * f
+    a, b, c = COEF
+    XA = X @ A
+    want = a * X + b * XA + c * (XA @ A)
+    off = ot[rows].double() - want
+    size = norm(want)
+    assert bool(norm(off) <= 2.0 ** -8.97 * size), float(norm(off) / size)
+    # no row and no column of them off by more than rounding makes it
+    assert bool((off.abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -7 * size / want.numel() ** 0.5).all())
+    assert bool(out.isfinite().all()) and mxq.device_status() == 0

@@ -196,6 +196,7 @@ def fp8_grouped_mm(a, w, offs):
 # Inside a stream capture they refuse an input whose autograd graph was built on
 # the default stream and still lives, and their backward a pass that reaches
 # such a graph anywhere behind them: the captured backward would wait there.
+# torch.compile cannot trace them and runs them between its graphs.
 
 def moe_route(logits, top_k, *, valid=None, renormalize=False):
     """(weights (T, top_k) fp32, ids (T, top_k) int32, counts (E,) int32, loss

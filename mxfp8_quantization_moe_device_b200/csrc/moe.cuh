@@ -272,9 +272,13 @@ MXQ_DEV double loss_factor(int E, int k, double n) { return n > 0.0 ? (double)E 
 // instructions). Keys: the logit's order; 16-bit logits leave room for the
 // complement of the index below, so that one maximum gives value and index and
 // equal logits go to the lowest index; 32-bit ones carry it in a second word.
-// The next token's logits are loaded while this one is worked on. 65536 tokens,
-// 256 experts, k = 8, bf16: 39 us, bound by the ALU pipe (2.9 instructions a
-// cycle), where reading the 34 MB would take 5.
+// The next token's logits are loaded while this one is worked on. A lane's sums
+// of p are one fp32 chain of its n tokens (all terms positive: off by n 2^-24 at
+// most, 14 at 65536 tokens of 256 experts), the CTAs' are added in fp64. 65536
+// tokens, 256 experts, k = 8, bf16: 39 us, bound by the ALU pipe (2.9
+// instructions a cycle), where reading the 34 MB would take 5. fp32 logits, with
+// keys of 64 bits, take 70 with the finishing kernel; above 512 experts they
+// spill (576 bytes a thread): 130 at 16384 x 1024.
 template <typename T, int LPT, int EPL>
 __global__ void __launch_bounds__(moe::ROUTE_THREADS)
     k_moe_route(const T *__restrict__ logits, int64_t tokens, int E, int64_t ld, const uint8_t *__restrict__ valid,
@@ -686,7 +690,7 @@ __global__ void __launch_bounds__(moe::ROUTE_BWD_THREADS)
 // equals (match.any), and the warps' counters are then summed in order. One
 // tile needs no pass 1. No atomics across CTAs, nothing to clear. match.any
 // bounds the ranking, so tiles are small and spread over the SMs: 131072
-// entries took 10.8 us in tiles of 8192.
+// entries of 64 experts take 7.8 us, in tiles of 8192 they took 19.9.
 namespace moe {
 constexpr int PLAN_THREADS = 512;
 constexpr int PLAN_WARPS = PLAN_THREADS / 32;
@@ -948,8 +952,9 @@ __global__ void __launch_bounds__(moe::ROW_THREADS)
 // slots are then looked up once a row). The loads of J slots are issued
 // together: a branch that is the same for the whole warp leaves out a dropped
 // slot, a lane behind the run's end reads the run's last vector and stores
-// nothing. HBM bounds it on aligned rows: 185 us at 16384 x 4 rows of 7168 bf16
-// (floor 180); loads in flight on others: 50 at 5003 x 6 rows of 1419 fp32 (30).
+// nothing. HBM bounds it on aligned rows: 174 to 182 us at 16384 x 4 rows of
+// 7168 bf16 (180 at the measured copy rate); loads in flight on others: 45 at
+// 5003 x 6 rows of 1419 fp32, a tenth of them dropped (28).
 template <typename T, int V, int U, int J>
 __global__ void __launch_bounds__(moe::ROW_THREADS, V * sizeof(T) == 16 ? 4 : 5)
     k_moe_combine(const T *__restrict__ y, int64_t M, int64_t K, int64_t ld, const int32_t *__restrict__ pos,
@@ -1023,8 +1028,9 @@ __global__ void __launch_bounds__(moe::ROW_THREADS, V * sizeof(T) == 16 ? 4 : 5)
 
 // dy[pos[t][j]] = w[t][j] dout[t] and dw[t][j] = <dout[t], y[pos[t][j]]>, a
 // warp per entry; rows of dy from offs[E-1] to M are zero. dy or dw may be
-// NULL. 338 us at 16384 x 4 rows of 7168 bf16, bound by HBM (floor 324, dout's row
-// re-read from L2), 77 at 5003 x 6 rows of 1419 fp32 (57).
+// NULL. 331 us at 16384 x 4 rows of 7168 bf16, bound by HBM (324 at the measured
+// copy rate, dout's row re-read from L2), 66 at 5003 x 6 rows of 1419 fp32, a
+// tenth of them dropped (54).
 template <typename T, int V, int U>
 __global__ void __launch_bounds__(moe::ROW_THREADS)
     k_moe_combine_bwd(const T *__restrict__ dout, int64_t ldd, const T *__restrict__ y, int64_t ldy, int64_t M,

@@ -23,7 +23,8 @@ RouteShape route_shape(int64_t E)
 }
 
 // CTAs of the router: one for few tokens (it then needs no second launch),
-// else enough for every warp to take a few groups of tokens
+// else a warp for every group of tokens up to two CTAs per SM, which then take
+// the groups in turn
 int64_t route_grid(int64_t T, int64_t E, int sms)
 {
     const int64_t per_cta = (int64_t)moe::ROUTE_WARPS * (32 / route_shape(E).lpt);
@@ -141,11 +142,11 @@ int row_vector(std::initializer_list<RowOperand> ops, int64_t K, int size)
 // Vectors of V elements, and how many of them a lane has in flight: U of one
 // row where one row is read, U4 of each of up to four slots, U8 of each of J8
 // slots where there are more (more in flight costs residency: at 16384 x 4 rows
-// of 7168 bf16, U4 = 2 with four CTAs per SM sums in 186 us, with two CTAs and
-// twice the loads in 197, with five CTAs and spills in 235). Single elements want
-// more of both: at 5003 x 6 rows of 1419 fp32, U8 = 4 of three slots with five
-// CTAs per SM sums in 51 us, of four slots with four in 55; the backward takes
-// 78 us with U = 12 and 82 with 8.
+// of 7168 bf16, U4 = 2 with four CTAs per SM, 24 bytes of spills a thread, sums in
+// 186 us, with two CTAs and twice the loads in 197, with five CTAs and more spills
+// in 235). Single elements want more of both: at 5003 x 6 rows of 1419 fp32, U8 =
+// 4 of three slots with five CTAs per SM sums in 51 us, of four slots with four in
+// 55; the backward takes 78 us with U = 12 and 82 with 8 (nothing dropped).
 #define MXQ_ROW_VARIANTS(X) X(MXQ_BF16, uint16_t, 8, 4, 2, 8, 1) X(MXQ_BF16, uint16_t, 2, 8, 4, 4, 4) X(MXQ_BF16, uint16_t, 1, 12, 4, 3, 4) X(MXQ_FP32, float, 4, 4, 2, 8, 1) X(MXQ_FP32, float, 1, 12, 4, 3, 4)
 
 unsigned row_grid(int64_t warps, int sms)

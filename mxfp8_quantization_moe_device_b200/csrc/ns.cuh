@@ -33,9 +33,9 @@
 // fp16's normal range: an absolute error of B (at most 2^-27), beside the a of
 // order one that it is added to.
 //
-// Every matrix is written once, by rows, and read by rows or by columns
+// For the products a matrix is kept by rows alone, and read by rows or by columns
 // (K-major or MN-major) as a product needs it. A = X X^T takes X by rows twice,
-// B X takes X by columns: X^T is never written. X is held twice, since the
+// B X takes X by columns: X^T is never written. X is held twice so, since the
 // tiles of B X read what others replace. A and A A are symmetric: computed on
 // and below the diagonal of 256 x 256 blocks, and a block of K above the
 // diagonal is read by columns from below. Writing X^T as well took 253 us in
@@ -43,13 +43,14 @@
 // halves of A and B 199 in place of 189 at (2, 1024, 1024).
 //
 // Epilogue. A lane holds one row of the accumulator, so what it writes along
-// the row lands in 32 different lines per store. What only the epilogue reads
-// (X as hi and lo, and A for the next product) is kept in chunks of 32 x 32
+// the row lands in 32 different lines per store. What the epilogue reads itself,
+// X as hi and lo and A for the next product, it keeps apart, in chunks of 32 x 32
 // elements in the order in which the warp holds them, 16 bytes per lane and
-// access, padded to whole chunks so that nothing is predicated; what the
-// products read goes through shared memory and a TMA store. Row-wise 16-byte
-// accesses in their place kept the load/store unit busy for 16 K cycles a tile
-// against 8 K of MMAs, 2-byte accesses down the columns cost 1.6 us a chunk.
+// access, padded to whole chunks so that nothing is predicated; what the products
+// read goes through shared memory and a TMA store. So hi and A are written twice,
+// and a workspace holds four arrays of X's size (two by rows, hi, lo). Row-wise
+// 16-byte accesses to one copy kept the load/store unit busy for 16 K cycles a
+// tile against 8 K of MMAs, 2-byte accesses down the columns cost 1.6 us a chunk.
 //
 // Kernel: the CTA-pair pipeline of gemm2.cuh (tcgen05.mma.cta_group::2, one
 // 256 x 256 tile per pair of SMs, six 32 KB stages of 64 fp16 columns, two
@@ -351,8 +352,9 @@ MXQ_DEV void scale_factors(double norm, float &f0, float &f1)
 // tile as it is read, or its transpose, goes to X, and both halves to the
 // epilogue's chunks. A thread moves pairs of neighbours. 380 us at (16, 2048,
 // 7168) bf16, 1.9 GB (288 at the copy rate): loads, then stores, so residency
-// counts, and eight CTAs per SM took 495 us where six took 585 (with X^T). No
-// __restrict__ on part: it is written while this kernel already runs.
+// counts, and eight CTAs per SM, with 48 to 60 bytes of spills a thread, took 495
+// us where six took 585 (with X^T). No __restrict__ on part: it is written while
+// this kernel already runs.
 template <typename T>
 __global__ void __launch_bounds__(256, 8)
     k_ns_init(const T *__restrict__ g, int rows, int cols, int pair, const double *part, int parts,
